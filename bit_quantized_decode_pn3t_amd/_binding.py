@@ -28,6 +28,8 @@ EXPORTS = ("pn_weights_per_block", "pn_row_bytes", "pn_gemv", "pn_gemv2",
            "pn_gemm_smallm", "pn_set_smallm_math", "pn_get_smallm_math", "pn_set_gemv_kernel",
            "pn_get_gemv_kernel", "pn_dequantize", "pn_rotate", "pn_gemm_prefill", "pn_gemm_prefill_group",
            "pn_group_create", "pn_group_create_smallm", "pn_group_run", "pn_group_destroy", "pn_gemv_batch",
+           "pn_kv4_page_bytes", "pn_kv4_plan", "pn_kv4_store", "pn_kv4_load", "pn_kv4_attn_workspace",
+           "pn_kv4_attn", "pn_spec_workspace", "pn_spec_verify",
            "pn_read_probe_scratch_bytes", "pn_read_probe", "pn_status_str", "pn_last_variant",
            "pn_variant_name")
 
@@ -54,6 +56,24 @@ class pn_gemm_desc(ctypes.Structure):
                 ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("ldx", ctypes.c_int64),
                 ("ldy", ctypes.c_int64), ("type", ctypes.c_int32), ("M", ctypes.c_int32)]
 
+
+class pn_kv4_cache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("dim", ctypes.c_int32)]
+
+
+class pn_kv4_store_desc(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ldq", ctypes.c_int64),
+                ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64), ("q_gain", ctypes.c_void_p),
+                ("k_gain", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("ldo", ctypes.c_int64),
+                ("T", ctypes.c_int64), ("row_type", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("rot", ctypes.c_int32), ("pairs", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+KV4_BLOCK = 64  # PN_KV4_BLOCK
+KV4_MAX_BATCH = 8192  # PN_KV4_MAX_BATCH
+ROW_TYPES = {"f32": 0, "f16": 1, 0: 0, 1: 1}  # PN_ROWS_*
 
 _lib = None
 
@@ -104,6 +124,25 @@ def lib():
     L.pn_group_destroy.restype = None
     L.pn_gemv_batch.argtypes = [ctypes.POINTER(pn_gemv_desc), i32, vp]
     L.pn_gemv_batch.restype = i32
+    cache = ctypes.POINTER(pn_kv4_cache)
+    L.pn_kv4_page_bytes.argtypes = [i32, i32, i32]
+    L.pn_kv4_page_bytes.restype = ctypes.c_size_t
+    L.pn_kv4_plan.argtypes = [vp, vp, vp, i32, vp, i32, i32, vp, i64, i32, vp, vp, vp, vp, vp, i64, vp, vp]
+    L.pn_kv4_plan.restype = i32
+    L.pn_kv4_store.argtypes = [cache, ctypes.POINTER(pn_kv4_store_desc), vp]
+    L.pn_kv4_store.restype = i32
+    L.pn_kv4_load.argtypes = [cache, vp, i64, vp, vp, vp]
+    L.pn_kv4_load.restype = i32
+    L.pn_kv4_attn_workspace.argtypes = [cache, i32, i32, i64, i64, i64, i32, i32]
+    L.pn_kv4_attn_workspace.restype = ctypes.c_size_t
+    L.pn_kv4_attn.argtypes = [cache, vp, i64, i32, vp, vp, vp, i64, i32, i64, i64, i64, ctypes.c_float, i32, i32,
+                              vp, i64, vp, ctypes.c_size_t, vp]
+    L.pn_kv4_attn.restype = i32
+    L.pn_spec_workspace.argtypes = [i32, i64]
+    L.pn_spec_workspace.restype = ctypes.c_size_t
+    L.pn_spec_verify.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i64, i32, i32, i64, vp, i64, vp, vp,
+                                 ctypes.c_size_t, vp]
+    L.pn_spec_verify.restype = i32
     L.pn_read_probe_scratch_bytes.argtypes = []
     L.pn_read_probe_scratch_bytes.restype = ctypes.c_size_t
     L.pn_read_probe.argtypes = [vp, ctypes.c_size_t, vp, ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t), vp]
@@ -301,6 +340,79 @@ def pn_gemv_batch(problems, stream=None, check=True):
     st = lib().pn_gemv_batch(arr, len(problems), _stream(stream))
     if check:
         _check(st, "pn_gemv_batch")
+    return st
+
+
+def pn_kv4_page_bytes(page_size, heads, dim):
+    return lib().pn_kv4_page_bytes(page_size, heads, dim)
+
+
+class KV4Cache:
+    """A paged pn4t cache over `pages` (num_pages * pn_kv4_page_bytes bytes of
+    device memory, which it keeps alive)."""
+
+    def __init__(self, pages, num_pages, page_size, heads, dim):
+        self.desc = pn_kv4_cache(_ptr(pages), num_pages, page_size, heads, dim)
+        self.keep = pages
+
+
+def pn_kv4_plan(ctx_len, new_len, held, B, free_pages, num_free, page_size, table, ld_table, max_pages, held_out,
+                q_start, kv_len, positions, slots, max_tokens, info, stream=None, check=True):
+    """Block tables, slots and positions of one step from request lengths."""
+    st = lib().pn_kv4_plan(_ptr(ctx_len), _ptr(new_len), _ptr(held), B, _ptr(free_pages), num_free, page_size,
+                           _ptr(table), ld_table, max_pages, _ptr(held_out), _ptr(q_start), _ptr(kv_len),
+                           _ptr(positions), _ptr(slots), max_tokens, _ptr(info), _stream(stream))
+    if check:
+        _check(st, "pn_kv4_plan")
+    return st
+
+
+def pn_kv4_store(cache, T, q, k, v, row_type, ldq, ldk, ldv, q_heads, q_gain, k_gain, eps, inv_freq, rot, pairs,
+                 positions, slots, q_out, ldo, stream=None, check=True):
+    """Norm and rotate query and key heads; quantize keys and values into the cache."""
+    d = pn_kv4_store_desc(_ptr(q), _ptr(k), _ptr(v), ldq, ldk, ldv, _ptr(q_gain), _ptr(k_gain), _ptr(inv_freq),
+                          _ptr(positions), _ptr(slots), _ptr(q_out), ldo, T, ROW_TYPES.get(row_type, -1), q_heads,
+                          rot, 1 if pairs else 0, eps)
+    st = lib().pn_kv4_store(ctypes.byref(cache.desc), ctypes.byref(d), _stream(stream))
+    if check:
+        _check(st, "pn_kv4_store")
+    return st
+
+
+def pn_kv4_load(cache, slots, T, k, v, stream=None, check=True):
+    """The cached keys and values of T slots as exact fp32."""
+    st = lib().pn_kv4_load(ctypes.byref(cache.desc), _ptr(slots), T, _ptr(k), _ptr(v), _stream(stream))
+    if check:
+        _check(st, "pn_kv4_load")
+    return st
+
+
+def pn_kv4_attn_workspace(cache, q_heads, B, total_q, max_q, max_kv, window=0, sinks=0):
+    return lib().pn_kv4_attn_workspace(ctypes.byref(cache.desc), q_heads, B, total_q, max_q, max_kv, window, sinks)
+
+
+def pn_kv4_attn(cache, q, ldq, q_heads, q_start, kv_len, table, ld_table, B, total_q, max_q, max_kv, scale, window,
+                sinks, out, ldo, ws, ws_bytes, stream=None, check=True):
+    """Attention of a ragged batch over the paged cache."""
+    st = lib().pn_kv4_attn(ctypes.byref(cache.desc), _ptr(q), ldq, q_heads, _ptr(q_start), _ptr(kv_len), _ptr(table),
+                           ld_table, B, total_q, max_q, max_kv, scale, window, sinks, _ptr(out), ldo, _ptr(ws),
+                           ws_bytes, _stream(stream))
+    if check:
+        _check(st, "pn_kv4_attn")
+    return st
+
+
+def pn_spec_workspace(B, V):
+    return lib().pn_spec_workspace(B, V)
+
+
+def pn_spec_verify(target, ldt, draft, ldd, tokens, ld_tok, n_draft, u, ldu, B, k, V, out, ld_out, accepted, ws,
+                   ws_bytes, stream=None, check=True):
+    """Accept drafted tokens against the target's probabilities and draw one more."""
+    st = lib().pn_spec_verify(_ptr(target), ldt, _ptr(draft), ldd, _ptr(tokens), ld_tok, _ptr(n_draft), _ptr(u), ldu,
+                              B, k, V, _ptr(out), ld_out, _ptr(accepted), _ptr(ws), ws_bytes, _stream(stream))
+    if check:
+        _check(st, "pn_spec_verify")
     return st
 
 

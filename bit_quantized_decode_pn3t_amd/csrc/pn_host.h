@@ -31,6 +31,11 @@ enum Variant {
     kVarBatchRows = 15,
     kVarBatchStream = 16,
     kVarPrefillGroup = 17,
+    kVarKv4Plan = 18,
+    kVarKv4Store = 19,
+    kVarKv4Load = 20,
+    kVarKv4Attn = 21,
+    kVarSpecVerify = 22,
 };
 
 extern thread_local int g_last_variant;

@@ -1042,6 +1042,11 @@ const char *pn_variant_name(int v)
     case kVarGroupStream: return "gemv_stream_group";
     case kVarBatchRows: return "gemv_rows_batch";
     case kVarBatchStream: return "gemv_stream_batch";
+    case kVarKv4Plan: return "kv4_plan";
+    case kVarKv4Store: return "kv4_store";
+    case kVarKv4Load: return "kv4_load";
+    case kVarKv4Attn: return "kv4_attn";
+    case kVarSpecVerify: return "spec_verify";
     }
     return "unknown";
 }

@@ -1,0 +1,210 @@
+// pn_kv4_plan.hip - block tables, slots and positions of one decoding step,
+// built on the device from request lengths (pn_kv4_plan), for AMD Instinct
+// MI355X (gfx950).
+//
+// Two prefix sums over the requests (new tokens, fresh pages) order
+// everything else: token t belongs to the last request that starts at or
+// before t, and the i-th fresh page to the last request whose pages start at
+// or before i.  Every workgroup computes both sums for itself into LDS (at
+// most 8192 requests of 12 bytes, which the L2s hold) and then takes its
+// share of the tokens and of the fresh pages by binary search, so the whole
+// step is one launch with no workgroup waiting for another, no atomics, and
+// the same result every time.  Sums saturate at INT32_MAX: saturating
+// addition of non-negative numbers is associative, so the scan may group as
+// it likes.
+//
+// Latency bounds it: the bytes are a few MB at most.
+#include "pn_kv4.h"
+
+using namespace pn::host;
+
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kPer = PN_KV4_MAX_BATCH / kThreads;  // requests a thread scans at most
+
+struct PlanArgs {
+    const int32_t *ctx, *fresh, *held, *free_pages;
+    int32_t *table, *held_out, *q_start, *kv_len, *positions, *info;
+    int64_t *slots;
+    int64_t ld_table, max_tokens;
+    int32_t B, num_free, shift, max_pages;
+};
+
+__device__ __forceinline__ int32_t sat(int64_t v) { return v > INT32_MAX ? INT32_MAX : (int32_t)v; }
+__device__ __forceinline__ int32_t sat_add(int32_t a, int32_t b) { return sat((int64_t)a + b); }
+__device__ __forceinline__ int32_t pos0(int32_t v) { return v < 0 ? 0 : v; }
+
+// Last index i in [0, n) with a[i] <= v; a ascending, a[0] <= v.
+__device__ __forceinline__ int last_at_most(const int32_t *a, int n, int32_t v)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= v) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int32_t pages_for(int64_t tokens, int shift)
+{
+    return (int32_t)((tokens + ((int64_t)1 << shift) - 1) >> shift);
+}
+
+__global__ __launch_bounds__(kThreads) void kv4_plan(PlanArgs a)
+{
+    __shared__ int32_t start[PN_KV4_MAX_BATCH + 1];  // first token of each request
+    __shared__ int32_t page0[PN_KV4_MAX_BATCH + 1];  // first fresh page of each request
+    __shared__ int32_t part[2][kThreads / 64];
+    __shared__ int32_t lost[kThreads / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int per = (a.B + kThreads - 1) / kThreads;
+
+    // thread-local sums, then a wave scan, then the waves' totals
+    int32_t tok[kPer], pg[kPer], ts = 0, ps = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int i = tid * per + j;
+        tok[j] = ts;
+        pg[j] = ps;
+        if (j < per && i < a.B) {
+            const int32_t n = pos0(a.fresh[i]);
+            const int32_t need = pages_for((int64_t)pos0(a.ctx[i]) + n, a.shift);
+            ts = sat_add(ts, n);
+            ps = sat_add(ps, pos0(need - pos0(a.held[i])));
+        }
+    }
+    int32_t ti = ts, pi = ps;  // inclusive over the wave
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int32_t t = __shfl_up(ti, d, 64), p = __shfl_up(pi, d, 64);
+        if (lane >= d) {
+            ti = sat_add(ti, t);
+            pi = sat_add(pi, p);
+        }
+    }
+    if (lane == 63) {
+        part[0][wave] = ti;
+        part[1][wave] = pi;
+    }
+    // exclusive over the wave
+    int32_t te = __shfl_up(ti, 1, 64), pe = __shfl_up(pi, 1, 64);
+    if (lane == 0) te = pe = 0;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) {
+        te = sat_add(te, part[0][w]);
+        pe = sat_add(pe, part[1][w]);
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int i = tid * per + j;
+        if (j < per && i < a.B) {
+            start[i] = sat_add(te, tok[j]);
+            page0[i] = sat_add(pe, pg[j]);
+        }
+    }
+    if (tid == kThreads - 1) {
+        start[a.B] = sat_add(te, ts);
+        page0[a.B] = sat_add(pe, ps);
+    }
+    __syncthreads();
+
+    const int64_t step = (int64_t)gridDim.x * kThreads, first = (int64_t)blockIdx.x * kThreads + tid;
+    const int32_t total = start[a.B], pages = page0[a.B];
+
+    // what each request gets
+    for (int64_t i = first; i <= a.B; i += step) {
+        a.q_start[i] = start[i];
+        if (i == a.B) break;
+        const int64_t len = (int64_t)pos0(a.ctx[i]) + pos0(a.fresh[i]);
+        const int32_t need = pages_for(len, a.shift), held = pos0(a.held[i]);
+        a.kv_len[i] = sat(len);
+        a.held_out[i] = need > held ? need : held;
+    }
+    // fresh pages into the table
+    for (int64_t p = first; p < pages; p += step) {
+        const int i = last_at_most(page0, a.B, (int32_t)p);
+        const int64_t col = (int64_t)pos0(a.held[i]) + (p - page0[i]);
+        if (col < a.max_pages) a.table[i * a.ld_table + col] = p < a.num_free ? a.free_pages[p] : -1;
+    }
+    // the step's tokens
+    for (int64_t t = first; t < a.max_tokens; t += step) {
+        int32_t pos = -1;
+        int64_t slot = -1;
+        if (t < total) {
+            const int i = last_at_most(start, a.B, (int32_t)t);
+            const int64_t at = (int64_t)pos0(a.ctx[i]) + (t - start[i]);
+            const int32_t col = (int32_t)(at >> a.shift), held = pos0(a.held[i]);
+            int32_t page = -1;
+            if (col < a.max_pages) {
+                if (col < held) {
+                    page = a.table[i * a.ld_table + col];
+                } else {
+                    const int64_t p = (int64_t)page0[i] + (col - held);
+                    if (p < a.num_free) page = a.free_pages[p];
+                }
+            }
+            pos = sat(at);
+            if (page >= 0) slot = ((int64_t)page << a.shift) + (at & ((1 << a.shift) - 1));
+        }
+        a.positions[t] = pos;
+        a.slots[t] = slot;
+    }
+
+    if (blockIdx.x != 0) return;  // the same for the whole workgroup
+    // A request loses the tokens from its first missing page on, and those
+    // past max_tokens: both a tail.
+    int32_t mine = 0;
+    for (int i = tid; i < a.B; i += kThreads) {
+        const int64_t ctx = pos0(a.ctx[i]), n = pos0(a.fresh[i]), held = pos0(a.held[i]);
+        const int64_t took = page0[i + 1] - page0[i];
+        int64_t got = (int64_t)a.num_free - page0[i];
+        got = got < 0 ? 0 : got < took ? got : took;
+        const int64_t cols = held + got < a.max_pages ? held + got : a.max_pages;
+        int64_t keep = (cols << a.shift) - ctx;  // of its new tokens
+        const int64_t room = a.max_tokens - start[i];
+        if (room < keep) keep = room;
+        if (keep < 0) keep = 0;
+        if (keep < n) mine = sat_add(mine, (int32_t)(n - keep));
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) mine = sat_add(mine, __shfl_xor(mine, d, 64));
+    if (lane == 0) lost[wave] = mine;
+    __syncthreads();
+    if (tid == 0) {
+        int32_t all = 0;
+        for (int w = 0; w < kThreads / 64; ++w) all = sat_add(all, lost[w]);
+        a.info[0] = pages < a.num_free ? pages : a.num_free;
+        a.info[1] = all;
+    }
+}
+
+}  // namespace
+
+extern "C" pn_status pn_kv4_plan(const int32_t *ctx_len, const int32_t *new_len, const int32_t *held, int B,
+                                 const int32_t *free_pages, int num_free, int page_size, int32_t *table,
+                                 int64_t ld_table, int max_pages, int32_t *held_out, int32_t *q_start,
+                                 int32_t *kv_len, int32_t *positions, int64_t *slots, int64_t max_tokens,
+                                 int32_t *info, void *stream)
+{
+    if (!ctx_len || !new_len || !held || !table || !held_out || !q_start || !kv_len || !positions || !slots || !info ||
+        (!free_pages && num_free != 0))
+        return PN_EINVAL;
+    const int shift = page_shift(page_size);
+    if (B < 1 || num_free < 0 || shift < 0 || max_pages < 1 || ld_table < max_pages || max_tokens < 1) return PN_ESHAPE;
+    const void *words[] = {ctx_len, new_len, held, free_pages, table, held_out, q_start, kv_len, positions, info};
+    for (const void *p : words)
+        if (!aligned(p, 4)) return PN_EALIGN;
+    if (!aligned(slots, 8)) return PN_EALIGN;
+    if (held_out < held + B && held < held_out + B) return PN_EINVAL;  // workgroups read held while others write held_out
+    if (B > PN_KV4_MAX_BATCH || max_tokens > INT32_MAX) return PN_EUNSUPPORTED;
+    const PlanArgs a = {ctx_len, new_len, held, free_pages, table, held_out, q_start, kv_len, positions, info,
+                        slots, ld_table, max_tokens, B, num_free, shift, max_pages};
+    int64_t grid = (max_tokens + kThreads - 1) / kThreads;
+    if (grid > device_cus()) grid = device_cus();
+    hipLaunchKernelGGL(kv4_plan, dim3((unsigned)grid), dim3(kThreads), 0, (hipStream_t)stream, a);
+    if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
+    g_last_variant = kVarKv4Plan;
+    return PN_OK;
+}

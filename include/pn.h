@@ -303,6 +303,183 @@ size_t pn_read_probe_scratch_bytes(void);
 pn_status pn_read_probe(const void *buf, size_t bytes, void *scratch, size_t scratch_bytes,
                         size_t *bytes_read, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The attention side of a decoding step: what runs between a layer's packed
+ * products (q, k, v in; o out) and after the head, over a paged cache that
+ * holds keys and values in pn4t blocks.
+ *
+ * One step: pn_kv4_plan turns request lengths into slots, positions and block
+ * tables; in every layer pn_kv4_store norms and rotates the queries and keys
+ * the products gave and quantizes keys and values into the cache, and
+ * pn_kv4_attn attends over it; pn_spec_verify accepts or replaces drafted
+ * tokens.  None of them allocates, waits or reads device data on the host,
+ * and all can be captured into a HIP graph.
+ *
+ * Values read from device memory (lengths, tables, slots, tokens) cannot be
+ * checked on the host.  The kernels bound every one of them: a bad page or
+ * slot is left out, never followed.
+ *
+ * The cache.  A page holds page_size tokens of every key-value head; element
+ * blocks of PN_KV4_BLOCK = 64 along a head are pn4t blocks (a signed fp16
+ * scale d and 64 four-bit codes n, value d * (n - 8), packed as in a pn4t
+ * word), with codes and scales held apart so that every load is aligned.
+ * Pages follow each other; in a page, heads follow each other; a head has,
+ * for token o of the page and R = dim / 64 blocks:
+ *   K codes   page_size * dim / 2 bytes: row o of dim / 8 words, natural word
+ *             8 b + 4 h + g (b < R, h < 2, g < 4) at place g * 2 R + 2 b + h
+ *   V codes   page_size * dim / 2 bytes: word w of token o at 4-byte place
+ *             ((o / 4) * (dim / 8) + w) * 4 + o % 4
+ *   K scales  page_size * R fp16: token o, block b at o * R + b
+ *   V scales  likewise
+ * Keys are stored normed and rotated.  Slot s is token s % page_size of page
+ * s / page_size. */
+#define PN_KV4_BLOCK 64
+typedef struct pn_kv4_cache {
+    void *pages;       /* device, 16-byte aligned, num_pages * pn_kv4_page_bytes */
+    int32_t num_pages; /* >= 1                                                   */
+    int32_t page_size; /* tokens: 16, 32, 64, 128 or 256                         */
+    int32_t heads;     /* key-value heads, >= 1                                  */
+    int32_t dim;       /* elements of a head: 64, 128 or 256                     */
+} pn_kv4_cache;
+
+/* Bytes of one page; 0 for a page size or dim outside the list, or heads < 1. */
+size_t pn_kv4_page_bytes(int page_size, int heads, int dim);
+
+/* Block tables, slots and positions of one step, from request lengths, on the
+ * device and in one launch.  Request i has ctx_len[i] tokens in the cache,
+ * brings new_len[i] more (either may be 0; negative reads as 0) and holds
+ * held[i] pages: entries 0 .. held[i] - 1 of its table row.  For i < B:
+ *   need     = ceil((ctx_len + new_len) / page_size)
+ *   table[i][held .. need-1] = the next need - held entries of free_pages
+ *            (requests in order; -1 once they are used up); other entries of
+ *            the row are neither read nor written (those below held are read)
+ *   held_out = max(held, need),   kv_len = ctx_len + new_len
+ *   q_start  = sum of new_len over earlier requests (B + 1 entries)
+ * and for the step's tokens in order, t < max_tokens:
+ *   positions[t] = ctx_len[i] + its place in the request, -1 past the last
+ *   slots[t]     = page * page_size + position % page_size, -1 where the
+ *                  token has no page
+ *   info[0] = entries of free_pages taken (<= num_free)
+ *   info[1] = tokens without a place: past the free pages, past max_pages
+ *             columns or past max_tokens
+ * A request keeps pages that rejected drafts left ahead of its tokens, so a
+ * caller lowers ctx_len freely and returns pages only when a request ends.
+ *   table    : int32, B rows of ld_table >= max_pages; page ids
+ *   held_out : must not overlap held
+ *   B        : 1 .. PN_KV4_MAX_BATCH;  num_free >= 0;  max_tokens >= 1
+ * Sums saturate at INT32_MAX. */
+#define PN_KV4_MAX_BATCH 8192
+pn_status pn_kv4_plan(const int32_t *ctx_len, const int32_t *new_len, const int32_t *held, int B,
+                      const int32_t *free_pages, int num_free, int page_size, int32_t *table, int64_t ld_table,
+                      int max_pages, int32_t *held_out, int32_t *q_start, int32_t *kv_len, int32_t *positions,
+                      int64_t *slots, int64_t max_tokens, int32_t *info, void *stream);
+
+/* Queries, keys and values of T tokens on their way from a layer's products:
+ * for each token t and each head of q and k
+ *   y  = x * g / sqrt(mean(x^2) + eps)            (gain NULL: y = x)
+ *   (a, b) -> (a cos - b sin, a sin + b cos)       over rot / 2 pairs, with
+ *             angle positions[t] * inv_freq[i] for pair i: elements (i,
+ *             i + rot/2), or (2 i, 2 i + 1) with pairs != 0; elements from
+ *             rot on stay
+ * Queries are rounded to fp16 into q_out; keys, and values as they come, are
+ * quantized into the cache at slots[t].  The block rule is the weights': d =
+ * fp16_rne(-w / 8) with w the element of largest magnitude (the lowest index
+ * of equals), code = 8 + clamp(rint(y / d), -8, 7), ties to even; d = 0 gives
+ * code 8; |d| saturates at 65504; a NaN is stored as 0.  Keys are computed
+ * and both are quantized in fp64, so codes do not depend on the order of
+ * sums; queries in fp32, angles in fp64.
+ * A token with a negative position is skipped, one with a slot outside the
+ * cache is not stored (its query is written).  Slots must differ.
+ *   q, k, v   : T rows of q_heads (or the cache's heads) * dim elements, fp32
+ *               or fp16 (PN_ROWS_*), 16-byte aligned, ld in elements, >= the
+ *               row and a multiple of 8 (fp16) or 4 (fp32).  q NULL: keys
+ *               and values only; k and v both NULL: queries only
+ *   q_out     : fp16, T rows, 16-byte aligned, ldo >= q_heads * dim and a
+ *               multiple of 8; must not overlap q
+ *   rot       : 0 .. dim, a multiple of 16 (else PN_EUNSUPPORTED); inv_freq
+ *               rot / 2 fp32 values, NULL only with rot = 0
+ *   T         : >= 0 (0 does nothing) */
+enum { PN_ROWS_F32 = 0, PN_ROWS_F16 = 1 };
+typedef struct pn_kv4_store_desc {
+    const void *q, *k, *v;
+    int64_t ldq, ldk, ldv;
+    const float *q_gain, *k_gain; /* fp32 [dim], 16-byte aligned, or NULL */
+    const float *inv_freq;
+    const int32_t *positions;     /* [T] */
+    const int64_t *slots;         /* [T], 8-byte aligned; may be NULL without k, v */
+    uint16_t *q_out;
+    int64_t ldo;
+    int64_t T;
+    int32_t row_type;             /* PN_ROWS_F32 or PN_ROWS_F16, of q, k and v */
+    int32_t q_heads;
+    int32_t rot;
+    int32_t pairs;
+    float eps;
+} pn_kv4_store_desc;
+pn_status pn_kv4_store(const pn_kv4_cache *cache, const pn_kv4_store_desc *d, void *stream);
+
+/* The cached keys and values of T slots as fp32, d * (n - 8) exactly: k[t] and
+ * v[t] rows of heads * dim, 16-byte aligned (either may be NULL); a slot
+ * outside the cache gives zeros.  The check path of pn_kv4_store, and how a
+ * request's cache is read back. */
+pn_status pn_kv4_load(const pn_kv4_cache *cache, const int64_t *slots, int64_t T, float *k, float *v, void *stream);
+
+/* Attention of a ragged batch over the cache.  Request i has queries
+ * q_start[i] .. q_start[i+1]-1, the last of its kv_len[i] tokens: query j of
+ * Q stands at position p = kv_len - Q + j.  Query head h reads key-value head
+ * h / (q_heads / heads).
+ *   out = sum_t w_t v_t / sum_t w_t,   w_t = exp(scale * q . k_t)
+ * over the visible tokens t <= p; with window > 0 only t > p - window or
+ * t < sinks.  A token whose table entry is not a page of the cache is not
+ * visible; a query that sees nothing gives zeros.  Masked places may hold any
+ * bytes.
+ * Scores and sums are fp32; codes enter the products exactly; a weight times
+ * the value's scale is rounded once to fp16.
+ *   q, out   : fp16, total_q rows, 16-byte aligned, ld >= q_heads * dim and a
+ *              multiple of 8; must not overlap
+ *   table    : int32, B rows of ld_table >= ceil(max_kv / page_size)
+ *   max_q    : at least every request's queries (those past it are left out)
+ *   max_kv   : at least every kv_len (keys past it are left out)
+ *   sinks    : >= 0, read only with window > 0 (0: no window)
+ *   ws       : device, 16-byte aligned, ws_bytes (may be NULL with 0): room
+ *              for the parts of rows whose keys are split over workgroups.
+ *              Any size is right; pn_kv4_attn_workspace says how much the
+ *              call can use (less means fewer splits).  One workspace serves
+ *              calls that follow each other on a stream; calls that may
+ *              overlap need their own.
+ * PN_EUNSUPPORTED: B > 65535, or heads * row tiles past the grid's limits. */
+size_t pn_kv4_attn_workspace(const pn_kv4_cache *cache, int q_heads, int B, int64_t total_q, int64_t max_q,
+                             int64_t max_kv, int window, int sinks);
+pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, int64_t ldq, int q_heads, const int32_t *q_start,
+                      const int32_t *kv_len, const int32_t *table, int64_t ld_table, int B, int64_t total_q,
+                      int64_t max_q, int64_t max_kv, float scale, int window, int sinks, uint16_t *out, int64_t ldo,
+                      void *ws, size_t ws_bytes, void *stream);
+
+/* Verification of drafted tokens against the target's probabilities, from
+ * given random numbers u in [0, 1).  Request i has n = n_draft[i] drafts
+ * (clamped to 0..k; NULL: k), target rows p_0 .. p_k and, with `draft`, rows
+ * q_0 .. q_{k-1}:
+ *   draft j is accepted if all before it were and u[i][j] * q_j(x_j) <
+ *   p_j(x_j) (compared exactly; without `draft` q_j(x_j) = 1; a token outside
+ *   0..V-1 is refused);
+ *   with a = accepted drafts, one more token is drawn from r = max(p_a - q_a,
+ *   0) if a < n (without `draft`: p_a with x_a's entry 0), else from p_n: the
+ *   first index whose inclusive prefix sum (fp64) is above u[i][k] * sum r.
+ * Entries that are not positive and finite count as 0.  If r has none, the
+ * token is drawn from p_a; if that has none either it is -1.
+ *   out[i]      : the accepted drafts, the drawn token, then -1 (k + 1)
+ *   accepted[i] : a
+ *   target  : fp32, row (i, j) at (i * (k + 1) + j) * ldt, ldt >= V
+ *   draft   : fp32, row (i, j) at (i * k + j) * ldd, ldd >= V, or NULL
+ *   tokens  : int32, B rows of ld_tok >= k;  u : fp32, B rows of ldu >= k + 1;
+ *   out     : int32, B rows of ld_out >= k + 1
+ *   B 1..65535, k 0..1024, V 1..2^31-1
+ *   ws      : device, 8-byte aligned, at least pn_spec_workspace(B, V) bytes */
+size_t pn_spec_workspace(int B, int64_t V);
+pn_status pn_spec_verify(const float *target, int64_t ldt, const float *draft, int64_t ldd, const int32_t *tokens,
+                         int64_t ld_tok, const int32_t *n_draft, const float *u, int64_t ldu, int B, int k, int64_t V,
+                         int32_t *out, int64_t ld_out, int32_t *accepted, void *ws, size_t ws_bytes, void *stream);
+
 /* Text for a status code. */
 const char *pn_status_str(pn_status e);
 
