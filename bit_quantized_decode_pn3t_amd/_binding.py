@@ -158,17 +158,31 @@ def lib():
 
 
 def _ptr(a):
-    if a is None:
-        return None
-    if isinstance(a, int):
+    if a is None or isinstance(a, int):
         return a
     return a.data_ptr()
 
 
+def _current_stream():
+    """Handle of torch's current stream on the current device.  Small calls
+    feel the few microseconds of building torch's Stream object, so the raw
+    handle is asked for where this torch offers it."""
+    global _current_stream
+    import torch
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    torch.cuda.init()
+    if raw is None or device is None:
+        def _current_stream():
+            return torch.cuda.current_stream().cuda_stream
+    else:
+        def _current_stream():
+            return raw(device())
+    return _current_stream()
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -353,6 +367,7 @@ class KV4Cache:
 
     def __init__(self, pages, num_pages, page_size, heads, dim):
         self.desc = pn_kv4_cache(_ptr(pages), num_pages, page_size, heads, dim)
+        self.ref = ctypes.byref(self.desc)
         self.keep = pages
 
 
@@ -373,7 +388,7 @@ def pn_kv4_store(cache, T, q, k, v, row_type, ldq, ldk, ldv, q_heads, q_gain, k_
     d = pn_kv4_store_desc(_ptr(q), _ptr(k), _ptr(v), ldq, ldk, ldv, _ptr(q_gain), _ptr(k_gain), _ptr(inv_freq),
                           _ptr(positions), _ptr(slots), _ptr(q_out), ldo, T, ROW_TYPES.get(row_type, -1), q_heads,
                           rot, 1 if pairs else 0, eps)
-    st = lib().pn_kv4_store(ctypes.byref(cache.desc), ctypes.byref(d), _stream(stream))
+    st = lib().pn_kv4_store(cache.ref, d, _stream(stream))
     if check:
         _check(st, "pn_kv4_store")
     return st
@@ -381,20 +396,20 @@ def pn_kv4_store(cache, T, q, k, v, row_type, ldq, ldk, ldv, q_heads, q_gain, k_
 
 def pn_kv4_load(cache, slots, T, k, v, stream=None, check=True):
     """The cached keys and values of T slots as exact fp32."""
-    st = lib().pn_kv4_load(ctypes.byref(cache.desc), _ptr(slots), T, _ptr(k), _ptr(v), _stream(stream))
+    st = lib().pn_kv4_load(cache.ref, _ptr(slots), T, _ptr(k), _ptr(v), _stream(stream))
     if check:
         _check(st, "pn_kv4_load")
     return st
 
 
 def pn_kv4_attn_workspace(cache, q_heads, B, total_q, max_q, max_kv, window=0, sinks=0):
-    return lib().pn_kv4_attn_workspace(ctypes.byref(cache.desc), q_heads, B, total_q, max_q, max_kv, window, sinks)
+    return lib().pn_kv4_attn_workspace(cache.ref, q_heads, B, total_q, max_q, max_kv, window, sinks)
 
 
 def pn_kv4_attn(cache, q, ldq, q_heads, q_start, kv_len, table, ld_table, B, total_q, max_q, max_kv, scale, window,
                 sinks, out, ldo, ws, ws_bytes, stream=None, check=True):
     """Attention of a ragged batch over the paged cache."""
-    st = lib().pn_kv4_attn(ctypes.byref(cache.desc), _ptr(q), ldq, q_heads, _ptr(q_start), _ptr(kv_len), _ptr(table),
+    st = lib().pn_kv4_attn(cache.ref, _ptr(q), ldq, q_heads, _ptr(q_start), _ptr(kv_len), _ptr(table),
                            ld_table, B, total_q, max_q, max_kv, scale, window, sinks, _ptr(out), ldo, _ptr(ws),
                            ws_bytes, _stream(stream))
     if check:

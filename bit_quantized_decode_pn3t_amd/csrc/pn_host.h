@@ -67,7 +67,7 @@ int device_cus();
 
 // Run `set` (raising a kernel's LDS limit with hipFuncSetAttribute) once per
 // device and flag; later calls return the first call's result.  Thread-safe.
-enum AttrFlag { kAttrRows = 0, kAttrSmallM = 1, kAttrPrefill = 2, kAttrProbe = 3, kAttrCount = 4 };
+enum AttrFlag { kAttrRows = 0, kAttrSmallM = 1, kAttrPrefill = 2, kAttrProbe = 3, kAttrKv4 = 4, kAttrCount = 5 };
 bool once_per_device(AttrFlag f, bool (*set)());
 
 // The calling thread's kernel selections (pn_set_gemv_kernel and

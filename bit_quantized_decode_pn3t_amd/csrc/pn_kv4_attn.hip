@@ -1,17 +1,16 @@
 // pn_kv4_attn.hip - attention over the paged pn4t cache (pn_kv4_attn), for
 // AMD Instinct MI355X (gfx950).
 //
-//   out = sum_t w_t v_t / sum_t w_t,   w_t = exp2(s_t - m),
-//   s_t = scale log2(e) * sum_b dk[t][b] * (sum over block b of q . (n_k - 8))
+//   out = sum_t w_t v_t / sum_t w_t,   w_t = exp2(c s_t - m),  c = scale log2(e)
+//   s_t = sum_b dk[t][b] * (sum over block b of q . (n_k - 8))
 //
-// One pass over the keys with a running maximum m and sum per query row
-// (rows: the queries of a request times the query heads that share a
-// key-value head).  A wave takes 16 NT rows and steps through 32 tokens at a
-// time:
+// One pass over the keys with a running maximum and sum for each row (rows:
+// the queries of a request times the query heads that share a key-value
+// head).  A wave takes 16 NT rows and steps through 32 tokens at a time:
 //   S^T = K Q^T   v_mfma_f32_16x16x32_f16, A = 16 tokens, B = 16 rows.  A code
 //                 word is one lane's 8 elements of A: the cache keeps a row's
 //                 words in the order that gives each lane its words of all
-//                 blocks in one load, and every product lies in one block, so
+//                 blocks side by side, and every product lies in one block, so
 //                 the codes enter as exact small integers and the block's
 //                 scale multiplies the fp32 sum.
 //   O^T += V^T P  A = 16 elements x 32 tokens, B = P^T.  A score's place after
@@ -20,18 +19,28 @@
 //                 exactly too; the scale of a token's block multiplies the
 //                 weight, and that product is the one rounding to fp16 (half a
 //                 step, 2^-11 relative).  Weights are <= 1 and scales may have
-//                 any fp16 size, so each wave keeps a power of two that puts
-//                 the scales it has met below 2^11: with fp32 sums nothing
-//                 overflows, and products down to 2^-25 of the largest keep
-//                 full precision.
+//                 any fp16 size, so each wave keeps a power of two 2^u that
+//                 puts the scales it has met below 2^11, inside the exponent
+//                 of w: with fp32 sums nothing overflows, and products down to
+//                 2^-25 of the largest keep full precision.
 // A row of A is element 2 i + (r >> 3) of word r & 7 of a block (r = lane &
 // 15, product i < 4), so that one product stays in one block; two v_perm-ed
 // words give the token pairs.
 //
-// Keys are cut into chunks over workgroups when the rows alone do not fill
-// the device (kv4_merge joins the parts), and inside a workgroup over its
-// four waves (KW = 4); with enough rows each wave takes rows of its own
-// (KW = 1).  All sums have a fixed order.
+// Packed bytes go from the pages into LDS by DMA, a few steps ahead, each
+// wave into a ring of its own (no barrier in the loop); a key row's 16-byte
+// pieces are permuted on the way so that the reads spread over the banks.
+//
+// Work is dealt in equal shares, whatever the lengths: the items (request,
+// key-value head, row tile), each as long as its request has steps to see and
+// a little more for its start and end, form one line that the workgroups cut
+// into equal parts.  Every workgroup sums the requests for itself.  Later row
+// tiles of a prompt see more keys than earlier ones: a part of an item is a
+// part of the steps it really has, and the tiles are taken from both ends in
+// turn, so that neighbours make up for each other.  A workgroup's eight waves
+// take every eighth step and are joined through LDS; an item cut between
+// workgroups leaves parts in the workspace, which kv4_join adds.  All sums
+// have a fixed order.
 #include "pn_kv4.h"
 #include "pn_device.h"
 
@@ -43,23 +52,31 @@ namespace {
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float4_t __attribute__((ext_vector_type(4)));
 typedef unsigned short ushort2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) void lds_void;
 
-constexpr int kThreads = 256;
-constexpr int kWaves = 4;
-constexpr int kStep = 32;         // tokens of a step
-constexpr float kLowest = -1e30f; // a maximum before any score
+constexpr int kThreads = 512;
+constexpr int kWaves = 8;
+constexpr int kStep = 32;          // tokens of a step
+constexpr float kLowest = -1e30f;  // a maximum before any score
+constexpr int kShare = 16;         // steps of a workgroup at least
+constexpr int kOver = 32;          // what an item's start and end cost, in steps
+constexpr int kNothing = (int)0x80000000;  // an offset past every buffer: reads zero
 
 struct AttnArgs {
     Kv4 c;
     const uint16_t *q;
     const int32_t *q_start, *kv_len, *table;
     uint16_t *out;
-    float *lse;   // [splits][rows of the call], with more than one split
-    float *part;  // [splits][rows of the call][dim]
+    float *part;      // fragments of a workgroup's first and last cut item
+    float2 *part_ml;  // their rows' maxima and sums
+    int2 *cuts;       // [item]: first and last workgroup of the item
     int64_t ldq, ldo, ld_table, total_q;
     int64_t max_q, max_kv;
-    int32_t q_heads, group, B, max_pages, window, sinks, splits, chunk;  // chunk: steps of a split
-    float scale2;  // scale * log2(e)
+    int32_t q_heads, group, B, max_pages, window, sinks;
+    int32_t workers, whole;  // workgroups; whole: items are not cut
+    int32_t tiles;           // row tiles of a request at most
+    int32_t negate;          // scale < 0: the queries are negated
+    float c2;                // |scale| log2(e), above 0
 };
 
 // The part of a request that a row tile works on.
@@ -105,77 +122,138 @@ __device__ __forceinline__ void span(const AttnArgs &a, Work &w, int i0, int i1)
     w.steps = w.sink_steps + (end > w.lo ? end - w.lo : 0);
 }
 
-// The pages of a step's two 16-token tiles (-1: not visible).
-struct Tiles {
-    int32_t page[2];
+// What the line counts for request b: its row tiles and the steps that all of
+// its queries see together.  Queries without keys count one step: they have
+// zeros to write.
+struct Cost {
+    Work w;
+    int32_t steps, tiles;
 };
 
-__device__ __forceinline__ Tiles tiles(const AttnArgs &a, const int32_t *row, int step)
+__device__ __forceinline__ Cost cost(const AttnArgs &a, int b, int tile_rows)
 {
-    Tiles t;
+    Cost c;
+    c.w = request(a, b);
+    c.steps = c.tiles = 0;
+    if (c.w.qn < 1) return c;
+    Work all = c.w;
+    span(a, all, 0, c.w.qn - 1);
+    c.steps = all.steps < 1 ? 1 : all.steps;
+    c.tiles = (c.w.qn * a.group + tile_rows - 1) / tile_rows;
+    return c;
+}
+
+__device__ __forceinline__ int64_t length(const AttnArgs &a, const Cost &c)
+{
+    return (int64_t)(c.steps + kOver) * c.tiles * a.c.heads;
+}
+
+// ---------------------------------------------------------------------------
+// A wave's ring of staged steps.
+// ---------------------------------------------------------------------------
+template <int D> struct Ring {
+    using L = Kv4Layout<D>;
+    static constexpr int R = L::R;
+    static constexpr int kTile = 16 * L::kRow;         // codes of 16 tokens
+    static constexpr int kV = 2 * kTile;               // K of both tiles, then V, then the scales
+    static constexpr int kScales = 4 * kTile;          // of a tile: K's, V's (32 R bytes each), 256 bytes kept
+    static constexpr int kStage = kScales + 512;
+    static constexpr int kStages = D == 256 ? 2 : D == 128 ? 3 : 4;
+    static constexpr int kWide = D == 64 ? 4 : 16;     // bytes of a lane's DMA
+    static constexpr int kEach = kTile / (64 * kWide); // DMA instructions of a tile's codes
+    static constexpr int kLoads = 2 * (2 * kEach + 1); // of a step
+    static constexpr int kBytes = kWaves * kStages * kStage;
+    static_assert((kStages - 1) * kLoads < 64, "vmcnt");
+
+    // 16-byte piece u (of a key row's D / 32) of row r
+    __device__ static constexpr int piece(int r, int u)
+    {
+        return D == 128 ? 4 * r + (u ^ (r >> 2)) : 8 * r + (u ^ (r >> 1 & 7));
+    }
+};
+
+// A lane's offsets within a head's part of a page.
+template <int D> struct Offsets {
+    int k[Ring<D>::kEach], v, s;
+    __device__ __forceinline__ void set(int lane, int P)
+    {
+        using G = Ring<D>;
+        using L = Kv4Layout<D>;
+#pragma unroll
+        for (int j = 0; j < G::kEach; ++j) {
+            const int x = 64 * j + lane;
+            if (D == 64) k[j] = 4 * x;
+            else if (D == 128) k[j] = 64 * (x >> 2) + 16 * ((x & 3) ^ (x >> 4));
+            else k[j] = 128 * (x >> 3) + 16 * ((x & 7) ^ (x >> 4 & 7));
+        }
+        v = L::v_codes(P) + G::kWide * lane;
+        s = lane < 8 * G::R ? L::k_scales(P) + 4 * lane
+            : lane < 16 * G::R ? L::v_scales(P) + 4 * (lane - 8 * G::R) : kNothing;
+    }
+};
+
+// The pages of a step's two 16-token tiles (-1: not of the cache).
+struct Pages {
+    int32_t p[2];
+};
+
+__device__ __forceinline__ Pages pages_of(const AttnArgs &a, const int32_t *row, int step)
+{
+    Pages t;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int at = (step * kStep + 16 * i) >> a.c.shift;
-        int32_t p = -1;
-        if (at < a.max_pages) p = row[at];
-        t.page[i] = uniform((uint32_t)p < (uint32_t)a.c.num_pages ? p : -1);
+        t.p[i] = at < a.max_pages ? row[at] : -1;
     }
     return t;
 }
 
-// What a lane holds of one step: two tiles' key words, value words and scales.
-template <int D> struct Step {
-    static constexpr int R = D / 64;
-    uint32_t k[2][2 * R];   // [tile][2 b + h]
-    uint32_t v[2][R][4];    // [tile][block][token]
-    uint32_t ks[2][2 * R];  // fp16 [token 4 g ..][block]
-    uint32_t vs[2][2 * R];
-};
-
-template <int D>
-__device__ __forceinline__ void fetch(Step<D> &s, const AttnArgs &a, const Tiles &t, int step, int head, int lane)
+__device__ __forceinline__ int32_t valid(const AttnArgs &a, int32_t p)
 {
+    return uniform((uint32_t)p < (uint32_t)a.c.num_pages ? p : -1);
+}
+
+// Loads of 4 or 16 bytes a lane into LDS.
+template <int BYTES>
+__device__ __forceinline__ void load_lds(const __amdgpu_buffer_rsrc_t &rs, uint8_t *to, int lane_off, int off)
+{
+    if constexpr (BYTES == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)to, 16, lane_off, off, 0, 0);
+    else __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)to, 4, lane_off, off, 0, 0);
+}
+
+// Start the loads of a step (none: `there` false; the count stays the same).
+template <int D>
+__device__ __forceinline__ void stage(const AttnArgs &a, uint8_t *to, const Offsets<D> &off, const Pages &t, int step,
+                                      int head, bool there)
+{
+    using G = Ring<D>;
     using L = Kv4Layout<D>;
-    constexpr int R = L::R;
-    const int P = 1 << a.c.shift, r = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int32_t page = t.page[i] < 0 ? 0 : t.page[i];
-        const uint8_t *base = a.c.pages + ((int64_t)page * a.c.heads + head) * a.c.chunk;
-        const int o = (step * kStep + 16 * i) & (P - 1);
-        const uint8_t *k = base + (o + r) * L::kRow + g * (8 * R);
-        if constexpr (R == 1) {
-            const uint2 x = *(const uint2 *)k;
-            s.k[i][0] = x.x, s.k[i][1] = x.y;
-        } else {
+        const int32_t page = valid(a, t.p[i]);
+        const int o = (step * kStep + 16 * i) & ((1 << a.c.shift) - 1);
+        const bool some = there && page >= 0;
+        const uint8_t *base = a.c.pages + ((int64_t)(some ? page : 0) * a.c.heads + head) * a.c.chunk;
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, some ? (uint32_t)a.c.chunk : 0u);
 #pragma unroll
-            for (int j = 0; j < R / 2; ++j) {
-                const uint4 x = *(const uint4 *)(k + 16 * j);
-                s.k[i][4 * j] = x.x, s.k[i][4 * j + 1] = x.y, s.k[i][4 * j + 2] = x.z, s.k[i][4 * j + 3] = x.w;
-            }
-        }
-        const uint8_t *v = base + L::v_codes(P) + ((o >> 2) + g) * (16 * L::W) + (r & 7) * 16;
+        for (int j = 0; j < G::kEach; ++j)
+            load_lds<G::kWide>(rs, to + i * G::kTile + 64 * G::kWide * j, off.k[j], o * L::kRow);
 #pragma unroll
-        for (int b = 0; b < R; ++b) {
-            const uint4 x = *(const uint4 *)(v + 128 * b);
-            s.v[i][b][0] = x.x, s.v[i][b][1] = x.y, s.v[i][b][2] = x.z, s.v[i][b][3] = x.w;
-        }
-        const uint8_t *d = base + L::k_scales(P) + (o + 4 * g) * (2 * R);
-        const uint8_t *e = base + L::v_scales(P) + (o + 4 * g) * (2 * R);
-        if constexpr (R == 1) {
-            const uint2 x = *(const uint2 *)d, y = *(const uint2 *)e;
-            s.ks[i][0] = x.x, s.ks[i][1] = x.y;
-            s.vs[i][0] = y.x, s.vs[i][1] = y.y;
-        } else {
-#pragma unroll
-            for (int j = 0; j < R / 2; ++j) {
-                const uint4 x = *(const uint4 *)(d + 16 * j), y = *(const uint4 *)(e + 16 * j);
-                s.ks[i][4 * j] = x.x, s.ks[i][4 * j + 1] = x.y, s.ks[i][4 * j + 2] = x.z, s.ks[i][4 * j + 3] = x.w;
-                s.vs[i][4 * j] = y.x, s.vs[i][4 * j + 1] = y.y, s.vs[i][4 * j + 2] = y.z, s.vs[i][4 * j + 3] = y.w;
-            }
-        }
+        for (int j = 0; j < G::kEach; ++j)
+            load_lds<G::kWide>(rs, to + G::kV + i * G::kTile + 64 * G::kWide * j, off.v, o * L::kRow + 64 * G::kWide * j);
+        load_lds<4>(rs, to + G::kScales + 256 * i, off.s, o * 2 * G::R);
     }
 }
+
+template <int N> __device__ __forceinline__ void wait_loads()
+{
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | (N >> 4) << 14);  // vmcnt(N)
+    asm volatile("" ::: "memory");
+}
+
+// The compiler schedules nothing across this: left alone it unpacks a whole
+// step ahead of its products and runs out of registers.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
 
 __device__ __forceinline__ half8_t codes8(uint32_t word)
 {
@@ -187,14 +265,28 @@ __device__ __forceinline__ half8_t codes8(uint32_t word)
     return r;
 }
 
-// Half h of token-major scales: token i, block b.
-template <int R> __device__ __forceinline__ float scale_of(const uint32_t *s, int i, int b)
+// N dwords from LDS, 8 or 16 bytes at a time.
+template <int N> __device__ __forceinline__ void read_words(uint32_t (&w)[N], const uint8_t *from)
 {
-    const int h = i * R + b;
-    return half_bits_to_float((s[h >> 1] >> (16 * (h & 1))) & 0xffffu);
+    if constexpr (N == 2) {
+        const uint2 x = *(const uint2 *)from;
+        w[0] = x.x, w[1] = x.y;
+    } else {
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j) {
+            const uint4 x = *(const uint4 *)(from + 16 * j);
+            w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
+        }
+    }
 }
 
-// Largest over the four 16-lane groups, in all of them.
+// Half h of packed fp16 values, as fp32 (folded into v_fma_mix).
+template <int N> __device__ __forceinline__ float half_at(const uint32_t (&w)[N], int h)
+{
+    return (float)as_half2(w[h >> 1])[h & 1];
+}
+
+// Largest over, or sum of, the four 16-lane groups, in all of them.
 __device__ __forceinline__ float group_max(float v)
 {
     auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -214,106 +306,135 @@ __device__ __forceinline__ float group_sum(float v)
 // of O^T the elements of rows 4 g .. 4 g + 3 of A.
 template <int D, int NT> struct State {
     static constexpr int R = D / 64;
-    half8_t q[NT][2 * R];
     float4_t o[NT][R][4];
-    float m[NT], l[NT];
-    float up;      // the power of two on the value scales
-    uint32_t cap;  // largest scale (fp16 bits) that `up` leaves below 2^15
+    float m[NT];   // largest score (before c2), kLowest if none
+    float mm[NT];  // m c2 - u
+    float l[NT];   // this lane's share of the sum of exp2(c2 s - mm)
+    int u;         // the power of two on the value scales
+    uint32_t cap;  // largest scale (fp16 bits) that 2^u leaves below 2^15
 };
 
-template <int D, int NT, bool MASKED>
-__device__ __forceinline__ void advance(State<D, NT> &st, Step<D> &s, const AttnArgs &a, const Tiles &t, int token0,
-                                        const int32_t (&pos)[NT], int end, int lane)
+// What a step that is not visible as a whole needs to know.
+struct Mask {
+    bool some;         // anything masked
+    bool page[2];      // the tiles' pages are of the cache
+    int32_t token0;    // of the step
+    int32_t end;       // keys of the request
+    int32_t low, high; // positions of the wave's first and last query
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void advance(State<D, NT> &st, const uint8_t *from, const half8_t *q, const AttnArgs &a,
+                                        const Mask &mask, const int32_t (&pos)[NT], int lane)
 {
-    constexpr int R = D / 64;
+    using G = Ring<D>;
+    constexpr int R = G::R;
     const int r = lane & 15, g = lane >> 4;
-
-    if (MASKED) {  // scales of unwritten places may be anything
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int n = t.page[i] < 0 ? 0 : end - (token0 + 16 * i + 4 * g);  // written tokens of the lane's four
-#pragma unroll
-            for (int h = 0; h < 4 * R; ++h)
-                if (h / R >= n) s.vs[i][h >> 1] &= (h & 1) ? 0x0000ffffu : 0xffff0000u;
-        }
-    }
-
-    // the value scales against the cap
-    ushort2_t top = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int h = 0; h < 2 * R; ++h)
-            top = __builtin_elementwise_max(top, __builtin_bit_cast(ushort2_t, s.vs[i][h] & 0x7fff7fffu));
-    uint32_t big = top[0] > top[1] ? top[0] : top[1];
-    if (__ballot(big > st.cap)) {
-#pragma unroll
-        for (int d = 16; d < 64; d <<= 1) {
-            const uint32_t o = __shfl_xor(big, d, 64);
-            big = o > big ? o : big;
-        }
-        const int e = (int)(big >> 10) < 30 ? (int)(big >> 10) : 30;  // scales < 2^(e - 14)
-        const float up = __builtin_ldexpf(1.0f, 25 - e);
-        const float f = up / st.up;  // the first time O is 0
-        st.up = up;
-        st.cap = e + 5 > 30 ? 0xffffu : (uint32_t)((e + 5) << 10) - 1;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int b = 0; b < R; ++b)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) st.o[n][b][i] *= f;
-    }
 
     // scores
     float4_t sc[NT][2];
+    uint32_t ks[2][2 * R];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2; ++i) read_words(ks[i], from + G::kScales + 256 * i + 8 * R * g);
 #pragma unroll
-        for (int b = 0; b < R; ++b) {
-            const half8_t k0 = codes8(s.k[i][2 * b]), k1 = codes8(s.k[i][2 * b + 1]);
-            float d[4];
+    for (int b = 0; b < R; ++b) {
+        half8_t k[2][2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) d[j] = scale_of<R>(s.ks[i], j, b) * a.scale2;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float4_t c = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, st.q[n][2 * b], (float4_t){0, 0, 0, 0}, 0, 0, 0);
-                c = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, st.q[n][2 * b + 1], c, 0, 0, 0);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sc[n][i][j] = b == 0 ? c[j] * d[j] : __builtin_fmaf(c[j], d[j], sc[n][i][j]);
-            }
+        for (int i = 0; i < 2; ++i) {
+            const uint8_t *row = from + i * G::kTile;
+            // words (b, 0) and (b, 1) of the lane's share of its token's row
+            const uint2 x = *(const uint2 *)(R == 1 ? row + 32 * r + 8 * g
+                                                    : row + 16 * G::piece(r, (R / 2) * g + b / 2) + 8 * (b & 1));
+            k[i][0] = codes8(x.x);
+            k[i][1] = codes8(x.y);
         }
-    }
-
-    uint32_t seen[NT];
-    if (MASKED) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            seen[n] = 0;
-            const int32_t under = a.window > 0 ? pos[n] - a.window : -1;  // >= INT32_MIN: pos >= -1
+            const half8_t q0 = q[(n * 2 * R + 2 * b) * 64 + lane], q1 = q[(n * 2 * R + 2 * b + 1) * 64 + lane];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float4_t c = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[i][0], q0, (float4_t){0, 0, 0, 0}, 0, 0, 0);
+                c = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[i][1], q1, c, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    sc[n][i][j] = __builtin_fmaf(c[j], half_at(ks[i], R * j + b), b == 0 ? 0.0f : sc[n][i][j]);
+            }
+        }
+        keep_order();
+    }
+
+    // Value scales of the lane's tokens.  One that no row sees may be
+    // anything, infinite or NaN: it becomes 0.
+    uint32_t d[2][2 * R];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) read_words(d[i], from + G::kScales + 256 * i + 32 * R + 8 * R * g);
+    if (mask.some) {
+        const int32_t under = a.window > 0 ? mask.low - a.window : -1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int key = mask.token0 + 16 * (j >> 2) + 4 * g + (j & 3);
+            const bool ok = mask.page[j >> 2] && key < mask.end && key <= mask.high && (key > under || key < a.sinks);
+#pragma unroll
+            for (int b = 0; b < R; ++b) {
+                const int h = R * (j & 3) + b;
+                if (!ok) d[j >> 2][h >> 1] &= h & 1 ? 0x0000ffffu : 0xffff0000u;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int32_t below = a.window > 0 ? pos[n] - a.window : -1;  // >= INT32_MIN: pos >= -1
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int key = token0 + 16 * (j >> 2) + 4 * g + (j & 3);
-                const bool ok = t.page[j >> 2] >= 0 && key < end && key <= pos[n] && (key > under || key < a.sinks);
-                seen[n] |= (uint32_t)ok << j;
+                const int key = mask.token0 + 16 * (j >> 2) + 4 * g + (j & 3);
+                const bool ok = mask.page[j >> 2] && key < mask.end && key <= pos[n] && (key > below || key < a.sinks);
+                sc[n][j >> 2][j & 3] = ok ? sc[n][j >> 2][j & 3] : -__builtin_inff();
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (!(seen[n] >> j & 1)) sc[n][j >> 2][j & 3] = -__builtin_inff();
         }
     }
 
+    // the scales against the cap
+    ushort2_t most = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2 * R; ++j)
+            most = __builtin_elementwise_max(most, __builtin_bit_cast(ushort2_t, d[i][j] & 0x7fff7fffu));
+    uint32_t big = most[0] > most[1] ? most[0] : most[1];
+    if (__ballot(big > st.cap)) {
+#pragma unroll
+        for (int x = 16; x < 64; x <<= 1) {
+            const uint32_t y = __shfl_xor(big, x, 64);
+            big = y > big ? y : big;
+        }
+        const int e = (int)(big >> 10) < 30 ? (int)(big >> 10) : 30;  // scales < 2^(e - 14)
+        const int u = 25 - e;
+        const float f = __builtin_ldexpf(1.0f, u - st.u);  // the first time l and O are 0
+        st.cap = e + 5 > 30 ? 0xffffu : (uint32_t)((e + 5) << 10) - 1;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            st.mm[n] -= (float)(u - st.u);
+            st.l[n] *= f;
+#pragma unroll
+            for (int b = 0; b < R; ++b)
+#pragma unroll
+                for (int i2 = 0; i2 < 4; ++i2) st.o[n][b][i2] *= f;
+        }
+        st.u = u;
+    }
+
+    keep_order();
     // weights
     half8_t p[NT][R];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        float mx = sc[n][0][0];
-#pragma unroll
-        for (int j = 1; j < 8; ++j) mx = fmaxf(mx, sc[n][j >> 2][j & 3]);
-        mx = group_max(mx);
+        float mx = fmaxf(fmaxf(sc[n][0][0], sc[n][0][1]), sc[n][0][2]);
+        mx = fmaxf(fmaxf(mx, sc[n][0][3]), sc[n][1][0]);
+        mx = fmaxf(fmaxf(mx, sc[n][1][1]), sc[n][1][2]);
+        mx = group_max(fmaxf(mx, sc[n][1][3]));
         if (__ballot(mx > st.m[n])) {
-            const float m = fmaxf(st.m[n], mx), f = __builtin_amdgcn_exp2f(st.m[n] - m);
-            st.m[n] = m;
+            const float f = mx > st.m[n] ? __builtin_amdgcn_exp2f((st.m[n] - mx) * a.c2) : 1.0f;
+            st.m[n] = fmaxf(st.m[n], mx);
+            st.mm[n] = st.m[n] * a.c2 - (float)st.u;
             st.l[n] *= f;
 #pragma unroll
             for (int b = 0; b < R; ++b)
@@ -323,30 +444,30 @@ __device__ __forceinline__ void advance(State<D, NT> &st, Step<D> &s, const Attn
         float w[8], sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            w[j] = __builtin_amdgcn_exp2f(sc[n][j >> 2][j & 3] - st.m[n]);
+            w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][j >> 2][j & 3], a.c2, -st.mm[n]));
             sum += w[j];
         }
         st.l[n] += sum;
 #pragma unroll
         for (int b = 0; b < R; ++b)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float x = w[j] * (scale_of<R>(s.vs[j >> 2], j & 3, b) * st.up);
-                if (MASKED && !(seen[n] >> j & 1)) x = 0.0f;  // the scale may be infinite or NaN
-                p[n][b][j] = (_Float16)x;
-            }
+            for (int j = 0; j < 8; ++j) p[n][b][j] = (_Float16)__builtin_fmaf(w[j], half_at(d[j >> 2], R * (j & 3) + b), 0.0f);
     }
 
+    keep_order();
     // values
     const uint32_t sel = r < 8 ? 0x05040100u : 0x07060302u;  // even (low) or odd (high) elements of a token pair
 #pragma unroll
     for (int b = 0; b < R; ++b) {
+        uint32_t v[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            read_words(v[i], from + G::kV + i * G::kTile + 16 * (g * (D / 8) + 8 * b + (r & 7)));
         half8_t va[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const uint32_t *w = &s.v[u >> 1][b][2 * (u & 1)];
             half2_t e[4];
-            Unpack<1>::run(__builtin_amdgcn_perm(w[1], w[0], sel), e);
+            Unpack<1>::run(__builtin_amdgcn_perm(v[u >> 1][2 * (u & 1) + 1], v[u >> 1][2 * (u & 1)], sel), e);
 #pragma unroll
             for (int i = 0; i < 4; ++i) va[i][2 * u] = e[i][0], va[i][2 * u + 1] = e[i][1];
         }
@@ -355,225 +476,305 @@ __device__ __forceinline__ void advance(State<D, NT> &st, Step<D> &s, const Attn
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 st.o[n][b][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(va[i], p[n][b], st.o[n][b][i], 0, 0, 0);
+        keep_order();
     }
 }
 
-// Element of the head that row `row` of product i of block b computes.
-__device__ __forceinline__ int element(int b, int i, int row) { return 64 * b + 8 * (row & 7) + 2 * i + (row >> 3); }
+// Lane (r, g) holds x[j] = element 64 b + 8 (4 (g & 1) + j) + 2 i + (g >> 1)
+// of row r; store it as fp16 pairs.
+__device__ __forceinline__ void store_row(uint16_t *out, const float4_t &x, int b, int i, int g)
+{
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        // lanes below 32 take x[j], those above x[j + 2], both elements of the pair
+        auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x[j]), __float_as_uint(x[j + 2]), false, false);
+        const uint32_t lo = __builtin_bit_cast(uint16_t, (_Float16)__uint_as_float(s[0]));
+        const uint32_t hi = __builtin_bit_cast(uint16_t, (_Float16)__uint_as_float(s[1]));
+        const int word = 4 * (g & 1) + j + (g & 2);
+        if (out) *(uint32_t *)(out + 64 * b + 8 * word + 2 * i) = lo | hi << 16;
+    }
+}
 
-// Grid: x = split + splits * row tile, y = key-value head, z = request.
-template <int D, int NT, int KW>
+// Floats of a part's fragments, [n][4 b + i][lane][4]; (m, l) of its rows are
+// apart, [part][row][2], so that the join reads them together.
+template <int D, int NT> constexpr int part_floats() { return NT * 4 * (D / 64) * 256; }
+
+template <int D, int NT>
 __global__ __launch_bounds__(kThreads) void kv4_attn(AttnArgs a)
 {
-    constexpr int R = D / 64;
-    constexpr int kRows = 16 * NT;                            // of a wave
-    constexpr int kTileRows = kRows * (kWaves / KW);          // of the workgroup
-    constexpr int kPad = D + 4;
-    __shared__ float buf[KW == 1 ? 1 : kRows * kPad];
-    __shared__ float ml[KW == 1 ? 1 : kWaves][KW == 1 ? 1 : kRows][2];
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    using G = Ring<D>;
+    constexpr int R = G::R, kRows = 16 * NT;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // the ring, then the queries
+    __shared__ float ml[kWaves][kRows][2];
+    __shared__ int64_t scan[kWaves];
+    __shared__ int64_t at_shared[2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
-    const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits, head = blockIdx.y, b = blockIdx.z;
+    uint8_t *ring = lds + wave * (G::kStages * G::kStage);
+    half8_t *q = (half8_t *)(lds + G::kBytes);  // [16-row group][32 elements][lane]: operands as the products take them
 
-    Work w = request(a, b);
-    const int row0 = tile * kTileRows + (KW == 1 ? wave * kRows : 0);  // of qn * group
-    const int rows = w.qn * a.group;
-    if (KW == 1 ? row0 >= rows : tile * kTileRows >= rows) return;  // KW > 1: the whole workgroup
-    const int last = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
-    const int i0 = row0 / a.group, i1 = last / a.group;
-    span(a, w, i0, i1);
-    const int e0 = split * a.chunk, e1 = a.splits == 1 ? w.steps : e0 + a.chunk < w.steps ? e0 + a.chunk : w.steps;
-    if (split > 0 && e0 >= w.steps) return;  // the merge knows
-
-    State<D, NT> st;
-    int32_t pos[NT];
+    // this workgroup's part of the line
+    const int per = (a.B + kThreads - 1) / kThreads;
+    int64_t mine = 0;
+    for (int b = tid * per; b < (tid + 1) * per && b < a.B; ++b) mine += length(a, cost(a, b, kRows));
+    int64_t sum = mine;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int row = row0 + 16 * n + r, i = row / a.group;
-        const bool live = row < rows;
-        pos[n] = live ? w.first + i : -1;
-        const uint16_t *q = a.q + (w.q0 + (live ? i : 0)) * a.ldq + (head * a.group + (live ? row - i * a.group : 0)) * D;
-#pragma unroll
-        for (int x = 0; x < 2 * R; ++x) {
-            st.q[n][x] = *(const half8_t *)(q + 32 * x + 8 * g);
-            if (!live) st.q[n][x] = (half8_t)(_Float16)0.0f;
-        }
-#pragma unroll
-        for (int x = 0; x < R; ++x)
-#pragma unroll
-            for (int i2 = 0; i2 < 4; ++i2) st.o[n][x][i2] = (float4_t){0, 0, 0, 0};
-        st.m[n] = kLowest;
-        st.l[n] = 0.0f;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t x = __shfl_up(sum, d, 64);
+        if (lane >= d) sum += x;
     }
-    st.up = 1.0f;
-    st.cap = 0;
-
-    const int32_t *row = a.table + b * a.ld_table;
-    const int32_t p0 = w.first + i0, p1 = w.first + i1;
-    auto place = [&](int e) { return e < w.sink_steps ? e : e - w.sink_steps + w.lo; };
-    auto work = [&](Step<D> &s, const Tiles &t, int step) {
-        const int token0 = step * kStep;
-        const bool whole = t.page[0] >= 0 && t.page[1] >= 0 && token0 + kStep <= w.len && token0 + kStep - 1 <= p0 &&
-                           (a.window <= 0 || (int64_t)token0 + a.window > p1 || token0 + kStep <= a.sinks);
-        if (whole) advance<D, NT, false>(st, s, a, t, token0, pos, w.len, lane);
-        else advance<D, NT, true>(st, s, a, t, token0, pos, w.len, lane);
-    };
-    int e = e0 + (KW == 1 ? 0 : wave);
-    if (e < e1) {
-        Tiles t = tiles(a, row, place(e));
-        Step<D> s;
-        fetch<D>(s, a, t, place(e), head, lane);
-        for (;;) {
-            const int next = e + KW;
-            Tiles tn = t;
-            Step<D> sn;
-            if (next < e1) {
-                tn = tiles(a, row, place(next));
-                fetch<D>(sn, a, tn, place(next), head, lane);
-            }
-            work(s, t, place(e));
-            if (next >= e1) break;
-            s = sn;
-            t = tn;
-            e = next;
-        }
+    if (lane == 63) scan[wave] = sum;
+    __syncthreads();
+    int64_t total = 0, before = sum - mine;
+    for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) before += scan[w];
+        total += scan[w];
     }
+    int64_t share = (total + a.workers - 1) / a.workers;
+    if (share < kShare && !a.whole) share = kShare;
+    const int64_t lo = blockIdx.x * share, hi = lo + share < total ? lo + share : total;
+    if (lo >= total) return;  // the whole workgroup
+    if (lo >= before && lo < before + mine) {  // one thread
+        int b = tid * per;
+        for (;; ++b) {
+            const int64_t n = length(a, cost(a, b, kRows));
+            if (lo < before + n) break;
+            before += n;
+        }
+        at_shared[0] = b;
+        at_shared[1] = before;
+    }
+    __syncthreads();
+    int b = uniform((int)at_shared[0]);
+    int64_t start = at_shared[1];  // of request b on the line
+    Offsets<D> off;
+    off.set(lane, 1 << a.c.shift);
 
-    const float down = 1.0f / st.up;
-    const int64_t call_rows = a.total_q * a.q_heads;
-    if constexpr (KW == 1) {
+    for (int64_t x = lo; x < hi;) {
+        const Cost c = cost(a, b, kRows);
+        const int64_t all = length(a, c);
+        if (x >= start + all) {
+            start += all;
+            ++b;
+            continue;
+        }
+        const int one = c.steps + kOver;  // an item's length on the line
+        const int item = uniform((int)((x - start) / one));
+        const int64_t first = start + (int64_t)item * one;  // of the item on the line
+        int s0 = (int)(x - first), s1 = (int)(hi - first < one ? hi - first : one);
+        x = first + s1;
+        if (a.whole) {  // items are taken whole, by the workgroup they start in
+            if (s0 > 0) continue;
+            s1 = one;
+        }
+        s0 = s0 > kOver ? s0 - kOver : 0;
+        s1 -= kOver;
+        if (s1 <= s0) continue;
+        s0 = uniform(s0), s1 = uniform(s1);
+        const bool cut = s0 > 0 || s1 < c.steps;
+        const int head = item / c.tiles, turn = item - head * c.tiles;
+        const int tile = turn & 1 ? c.tiles - 1 - (turn >> 1) : turn >> 1;
+        if (s0 == 0 && tid == 0 && !a.whole)
+            a.cuts[((int64_t)b * a.c.heads + head) * a.tiles + tile] =
+                make_int2((int)((first + kOver) / share), (int)((first + one - 1) / share));
+
+        const int row0 = tile * kRows, rows = c.w.qn * a.group;
+        const int last = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
+        Work w = c.w;
+        span(a, w, row0 / a.group, last / a.group);
+        const int32_t p0 = w.first + row0 / a.group, p1 = w.first + last / a.group;
+
+        // the queries into LDS
+        for (int y = tid; y < NT * 2 * R * 64; y += kThreads) {
+            const int at = row0 + 16 * (y / (2 * R * 64)) + (y & 15), i = at / a.group;
+            const int e = 32 * (y / 64 % (2 * R)) + 8 * (y >> 4 & 3);
+            half8_t v = (half8_t)(_Float16)0.0f;
+            if (at < rows) v = *(const half8_t *)(a.q + (w.q0 + i) * a.ldq + (head * a.group + at - i * a.group) * D + e);
+            q[y] = a.negate ? -v : v;
+        }
+        State<D, NT> st;
+        int32_t pos[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float l = group_sum(st.l[n]);
             const int at = row0 + 16 * n + r;
-            if (at >= rows) continue;  // no exchange below
-            const int i = at / a.group;
-            const int64_t q = w.q0 + i;
-            const int h = head * a.group + at - i * a.group;
-            const float f = l > 0.0f ? down / l : 0.0f;
-            if (a.splits > 1) {
-                const int64_t to = split * call_rows + q * a.q_heads + h;
-                if (g == 0) a.lse[to] = l > 0.0f ? st.m[n] + __builtin_amdgcn_logf(l) : -__builtin_inff();
+            pos[n] = at < rows ? w.first + at / a.group : -1;
 #pragma unroll
-                for (int x = 0; x < R; ++x)
+            for (int y = 0; y < R; ++y)
 #pragma unroll
-                    for (int i2 = 0; i2 < 4; ++i2)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) a.part[to * D + element(x, i2, 4 * g + j)] = st.o[n][x][i2][j] * f;
-            } else {
-                uint16_t *o = a.out + q * a.ldo + h * D;
-#pragma unroll
-                for (int x = 0; x < R; ++x)
-#pragma unroll
-                    for (int i2 = 0; i2 < 4; ++i2)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            o[element(x, i2, 4 * g + j)] =
-                                __builtin_bit_cast(uint16_t, (_Float16)(st.o[n][x][i2][j] * f));
-            }
+                for (int i2 = 0; i2 < 4; ++i2) st.o[n][y][i2] = (float4_t){0, 0, 0, 0};
+            st.m[n] = kLowest;
+            st.mm[n] = 0.0f;
+            st.l[n] = 0.0f;
         }
-    } else {
-        // join the waves: common maximum, then one wave after another adds
-        float f[NT];
+        st.u = 0;
+        st.cap = 0;
+
+        // The same part of the steps that this tile has.
+        auto place = [&](int e) { return e < w.sink_steps ? e : e - w.sink_steps + w.lo; };
+        const int e1 = uniform((int)((int64_t)s1 * w.steps / c.steps));
+        int e = uniform((int)((int64_t)s0 * w.steps / c.steps)) + wave;
+        const int32_t *row = a.table + (int64_t)b * a.ld_table;
+        // pages of the steps in the ring, and of the next to be staged
+        Pages held[G::kStages + 1];
+#pragma unroll
+        for (int i = 0; i <= G::kStages; ++i) held[i] = pages_of(a, row, e + kWaves * i < e1 ? place(e + kWaves * i) : 0);
+#pragma unroll
+        for (int i = 0; i < G::kStages; ++i) {
+            const int s = e + kWaves * i;
+            stage<D>(a, ring + i * G::kStage, off, held[i], place(s), head, s < e1);
+        }
+        // the queries are there; a bare barrier, so that the loads fly on
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        for (int at = 0; e < e1; e += kWaves) {
+            wait_loads<(G::kStages - 1) * G::kLoads>();
+            const int step = place(e), token0 = step * kStep;
+            uint8_t *from = ring + at * G::kStage;
+            at = at + 1 < G::kStages ? at + 1 : 0;
+            Mask mask;
+            mask.page[0] = valid(a, held[0].p[0]) >= 0;
+            mask.page[1] = valid(a, held[0].p[1]) >= 0;
+            mask.token0 = token0;
+            mask.end = w.len;
+            mask.low = p0;
+            mask.high = p1;
+            mask.some = !(mask.page[0] && mask.page[1] && token0 + kStep <= w.len && token0 + kStep - 1 <= p0 &&
+                          (a.window <= 0 || (int64_t)token0 + a.window > p1 || token0 + kStep <= a.sinks));
+            advance<D, NT>(st, from, q, a, mask, pos, lane);
+            __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the stage has been read
+            asm volatile("" ::: "memory");
+            const int s = e + kWaves * G::kStages, s2 = s + kWaves;
+            stage<D>(a, from, off, held[G::kStages], place(s), head, s < e1);
+#pragma unroll
+            for (int y = 0; y < G::kStages; ++y) held[y] = held[y + 1];
+            held[G::kStages] = pages_of(a, row, s2 < e1 ? place(s2) : 0);
+        }
+        wait_loads<0>();  // nothing is written into the ring any more
+
+        // Join the waves: the rows' maxima and sums, then each wave adds its
+        // share of the fragments of all eight.
+        float l[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float l = group_sum(st.l[n]);
-            if (g == 0) ml[wave][16 * n + r][0] = st.m[n], ml[wave][16 * n + r][1] = l;
+            l[n] = __builtin_ldexpf(group_sum(st.l[n]), -st.u);
+            if (g == 0) ml[wave][16 * n + r][0] = st.m[n], ml[wave][16 * n + r][1] = l[n];
+        }
+        float4_t *frag = (float4_t *)lds;  // [wave][4 b + i][lane]
+        // A share goes on with at most one item, its first (part 0), and
+        // leaves at most one unfinished, its last (part 1).
+        const int part_at = 2 * (int)blockIdx.x + (s0 == 0 ? 1 : 0);
+        float *part = a.part + (int64_t)part_at * part_floats<D, NT>();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            __syncthreads();
+            float m = kLowest, all_l = 0.0f;
+            for (int y = 0; y < kWaves; ++y) m = fmaxf(m, ml[y][16 * n + r][0]);
+            for (int y = 0; y < kWaves; ++y)
+                all_l += ml[y][16 * n + r][1] * __builtin_amdgcn_exp2f((ml[y][16 * n + r][0] - m) * a.c2);
+            float f = __builtin_ldexpf(__builtin_amdgcn_exp2f((st.m[n] - m) * a.c2), -st.u);
+            if (!cut) f = all_l > 0.0f ? f / all_l : 0.0f;
+#pragma unroll
+            for (int y = 0; y < 4 * R; ++y) frag[(wave * 4 * R + y) * 64 + lane] = st.o[n][y >> 2][y & 3] * f;
+            __syncthreads();
+            const int at = row0 + 16 * n + r, i = at / a.group;
+            const bool live = at < rows;
+            uint16_t *out = a.out + (w.q0 + i) * a.ldo + (int64_t)(head * a.group + at - i * a.group) * D;
+#pragma unroll
+            for (int y = wave >> 2; y < R; y += kWaves / 4) {  // block y, product wave & 3
+                const int f4 = 4 * y + (wave & 3);
+                float4_t v = frag[f4 * 64 + lane];
+#pragma unroll
+                for (int z = 1; z < kWaves; ++z) v += frag[(z * 4 * R + f4) * 64 + lane];
+                if (cut) {
+                    if (live) ((float4_t *)part)[(n * 4 * R + f4) * 64 + lane] = v;
+                } else {
+                    store_row(live ? out : nullptr, v, y, wave & 3, g);
+                }
+            }
+            if (cut && wave == 0 && g == 0) {
+                a.part_ml[(int64_t)part_at * kRows + 16 * n + r] = make_float2(m, all_l);
+            }
         }
         __syncthreads();
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float m = kLowest, l = 0.0f;
-            for (int x = 0; x < kWaves; ++x) m = fmaxf(m, ml[x][16 * n + r][0]);
-            for (int x = 0; x < kWaves; ++x)
-                l += ml[x][16 * n + r][1] * __builtin_amdgcn_exp2f(ml[x][16 * n + r][0] - m);
-            f[n] = l > 0.0f ? __builtin_amdgcn_exp2f(st.m[n] - m) * down / l : 0.0f;
-            const int at = row0 + 16 * n + r;
-            if (wave == 0 && g == 0 && a.splits > 1 && at < rows) {
-                const int i = at / a.group;
-                const int64_t to = split * call_rows + (w.q0 + i) * a.q_heads + head * a.group + at - i * a.group;
-                a.lse[to] = l > 0.0f ? m + __builtin_amdgcn_logf(l) : -__builtin_inff();
-            }
-        }
-        for (int x = 0; x < kWaves; ++x) {
-            if (wave == x) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int y = 0; y < R; ++y)
-#pragma unroll
-                        for (int i2 = 0; i2 < 4; ++i2)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                float *to = buf + (16 * n + r) * kPad + element(y, i2, 4 * g + j);
-                                const float v = st.o[n][y][i2][j] * f[n];
-                                *to = x == 0 ? v : *to + v;
-                            }
-            }
-            __syncthreads();
-        }
-        const int n = last - row0 + 1;  // live rows
-        for (int x = threadIdx.x; x < n * (D / 4); x += kThreads) {
-            const int at = row0 + x / (D / 4), c = x % (D / 4) * 4, i = at / a.group;
-            const float4_t v = *(const float4_t *)(buf + (at - row0) * kPad + c);
-            const int64_t q = w.q0 + i;
-            const int h = head * a.group + at - i * a.group;
-            if (a.splits > 1) {
-                *(float4_t *)(a.part + (split * call_rows + q * a.q_heads + h) * D + c) = v;
-            } else {
-                uint32_t u[2];
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-                    u[y] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v[2 * y]) |
-                           (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v[2 * y + 1]) << 16;
-                *(uint2 *)(a.out + q * a.ldo + h * D + c) = make_uint2(u[0], u[1]);
-            }
-        }
     }
 }
 
-// Join the splits of each row: one wave a row (query, head).  tile_rows: rows
-// of a wave of kv4_attn, whose span says how many splits there are.
-template <int D>
-__global__ __launch_bounds__(kThreads) void kv4_merge(AttnArgs a, int tile_rows)
+// Add the parts of items that were cut.  Grid: x = block + R * row tile, y =
+// key-value head, z = request; 16 waves: product i = wave & 3 of the block,
+// a fourth of the parts each.
+template <int D, int NT>
+__global__ __launch_bounds__(1024) void kv4_join(AttnArgs a)
 {
-    const int lane = threadIdx.x & 63, b = blockIdx.z, h = blockIdx.y;
-    Work w = request(a, b);
-    const int head = h / a.group;
-    const int i = blockIdx.x * kWaves + (int)(threadIdx.x >> 6);
-    if (i >= w.qn) return;
-    const int row = i * a.group + h - head * a.group, rows = w.qn * a.group;
-    const int row0 = row / tile_rows * tile_rows, last = (row0 + tile_rows < rows ? row0 + tile_rows : rows) - 1;
-    span(a, w, row0 / a.group, last / a.group);
-    const int n = (w.steps + a.chunk - 1) / a.chunk;
-    const int64_t call_rows = a.total_q * a.q_heads, at = (w.q0 + i) * a.q_heads + h;
-
-    float m = -__builtin_inff();
-    for (int s = lane; s < n; s += 64) m = fmaxf(m, a.lse[s * call_rows + at]);
+    constexpr int R = D / 64, kRows = 16 * NT, kDeep = 8;
+    __shared__ float4_t frag[16][64];
+    __shared__ float2 ml[64][16];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+    const int tile = blockIdx.x / R, y = blockIdx.x % R, head = blockIdx.y, b = blockIdx.z;
+    const Work w = request(a, b);
+    const int row0 = tile * kRows, rows = w.qn * a.group;
+    if (row0 >= rows) return;  // the whole workgroup, as below
+    const int2 c = a.cuts[((int64_t)b * a.c.heads + head) * a.tiles + tile];
+    const int parts = uniform(c.y - c.x + 1);
+    if (parts < 2) return;
+    // The first workgroup has the item's start (its part 1), the others go on with it (their part 0).
+    auto part = [&](int j) { return 2 * ((int64_t)c.x + j) + (j == 0 ? 1 : 0); };
+    const int i = wave & 3;
+#pragma unroll 1
+    for (int n = 0; n < NT; ++n) {
+        // rows' (m, l) of all parts: 64 parts at a time, one a thread
+        float m = kLowest, l = 0.0f;
+        for (int j0 = 0; j0 < parts; j0 += 64) {
+            const int j = j0 + ((int)threadIdx.x >> 4);
+            const float2 x = j < parts ? a.part_ml[part(j) * kRows + 16 * n + (threadIdx.x & 15)] : make_float2(kLowest, 0.0f);
+            __syncthreads();
+            ml[threadIdx.x >> 4][threadIdx.x & 15] = x;
+            __syncthreads();
+            float top = m;
+            for (int j2 = g; j2 < 64; j2 += 4) top = fmaxf(top, ml[j2][r].x);
+            top = group_max(top);
+            l *= __builtin_amdgcn_exp2f((m - top) * a.c2);
+            for (int j2 = g; j2 < 64; j2 += 4) l += ml[j2][r].y * __builtin_amdgcn_exp2f((ml[j2][r].x - top) * a.c2);
+            m = top;
+        }
+        l = group_sum(l);
+        float4_t o = {0, 0, 0, 0};
+        for (int j0 = wave >> 2; j0 < parts; j0 += 4 * kDeep) {
+            float4_t v[kDeep];
+            float f[kDeep];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
-    constexpr int kEach = D / 64;
-    float o[kEach] = {}, l = 0.0f;
-    if (m > -__builtin_inff()) {
-        for (int s = 0; s < n; ++s) {
-            const float x = __builtin_amdgcn_exp2f(a.lse[s * call_rows + at] - m);
-            l += x;
-            const float *p = a.part + (s * call_rows + at) * D + lane * kEach;
+            for (int x = 0; x < kDeep; ++x) {
+                const int j = j0 + 4 * x < parts ? j0 + 4 * x : parts - 1;
+                v[x] = ((const float4_t *)a.part)[part(j) * (part_floats<D, NT>() / 4) + (n * 4 * R + 4 * y + i) * 64 + lane];
+                f[x] = a.part_ml[part(j) * kRows + 16 * n + r].x;
+            }
 #pragma unroll
-            for (int j = 0; j < kEach; ++j) o[j] = __builtin_fmaf(x, p[j], o[j]);
+            for (int x = 0; x < kDeep; ++x)
+                if (j0 + 4 * x < parts) o += v[x] * __builtin_amdgcn_exp2f((f[x] - m) * a.c2);
+        }
+        __syncthreads();
+        frag[wave][lane] = o;
+        __syncthreads();
+        if (wave < 4) {
+            const int at = row0 + 16 * n + r, q = at / a.group;
+            o = frag[wave][lane];
+#pragma unroll
+            for (int x = 1; x < 4; ++x) o += frag[4 * x + wave][lane];
+            const float f = l > 0.0f ? 1.0f / l : 0.0f;
+            uint16_t *out = a.out + (w.q0 + q) * a.ldo + (int64_t)(head * a.group + at - q * a.group) * D;
+            store_row(at < rows ? out : nullptr, o * f, y, wave, g);
         }
     }
-    const float f = l > 0.0f ? 1.0f / l : 0.0f;
-    uint16_t *out = a.out + (w.q0 + i) * a.ldo + (int64_t)h * D + lane * kEach;
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) out[j] = __builtin_bit_cast(uint16_t, (_Float16)(o[j] * f));
 }
 
 // How a call is cut.
 struct Cut {
-    int nt, kw;        // row tiles of a wave, waves along the keys
-    int64_t row_tiles; // of a request
-    int splits, chunk;
+    int nt;               // 16-row groups of a wave
+    int64_t tiles;        // row tiles of a request at most
+    int workers;
+    bool whole;
+    size_t part, cuts;    // bytes of one workgroup's parts, of the items' records
 };
 
 Cut cut(const pn_kv4_cache *c, int q_heads, int B, int64_t max_q, int64_t max_kv, int window, int sinks)
@@ -581,58 +782,60 @@ Cut cut(const pn_kv4_cache *c, int q_heads, int B, int64_t max_q, int64_t max_kv
     Cut t;
     const int group = q_heads / c->heads;
     const int64_t rows = max_q * group;
-    const int most = c->dim == 256 ? 1 : c->dim == 128 ? 2 : 4;  // rows of a wave that its registers hold
-    const int64_t per = 16 * most;
-    // Rows for four waves each: a wave takes rows of its own.
-    t.kw = rows > 2 * per ? 1 : 4;
-    t.nt = 1;
-    while (t.nt < most && 16 * t.nt < rows) t.nt *= 2;
-    const int64_t tile_rows = 16 * t.nt * (kWaves / t.kw);
-    t.row_tiles = (rows + tile_rows - 1) / tile_rows;
+    const int most = c->dim == 256 ? 2 : 4;  // that the registers hold
+    t.nt = rows >= 16 * most ? most : (int)((rows + 15) / 16);
+    t.tiles = (rows + 16 * t.nt - 1) / (16 * t.nt);
     int64_t keys = max_kv;
     if (window > 0) {
         const int64_t reach = (int64_t)window + max_q + sinks + 2 * kStep;
         if (reach < keys) keys = reach;
     }
-    const int64_t steps = (keys + kStep - 1) / kStep + 1;
-    const int64_t groups = t.row_tiles * c->heads * B;
-    // Enough workgroups for several on every compute unit; at least 8 steps
-    // for a wave, so that its start and the merge stay small beside them.
-    int64_t splits = (8 * (int64_t)device_cus() + groups - 1) / groups;
-    const int64_t least = 8 * t.kw;
-    if (splits > (steps + least - 1) / least) splits = (steps + least - 1) / least;
-    if (splits < 1) splits = 1;
-    if (splits > 1024) splits = 1024;
-    t.chunk = (int)((steps + splits - 1) / splits);
-    t.splits = (int)((steps + t.chunk - 1) / t.chunk);
+    t.workers = device_cus();
+    t.whole = keys <= 2 * kShare * kStep;
+    t.part = 2 * sizeof(float) * t.nt * (c->dim * 16 + 32);
+    t.cuts = (size_t)B * c->heads * t.tiles * sizeof(int2);
     return t;
 }
 
-template <int D, int NT>
-void attn_launch(const AttnArgs &a, const Cut &t, hipStream_t s)
+// The ring and the queries.
+template <int D, int NT> constexpr int lds_bytes() { return Ring<D>::kBytes + NT * 2 * (D / 64) * 1024; }
+
+template <int D, int NT> bool raise_one()
 {
-    const dim3 grid((unsigned)(t.row_tiles * t.splits), (unsigned)a.c.heads, (unsigned)a.B);
-    if (t.kw == 4)
-        hipLaunchKernelGGL((kv4_attn<D, NT, 4>), grid, dim3(kThreads), 0, s, a);
-    else
-        hipLaunchKernelGGL((kv4_attn<D, NT, 1>), grid, dim3(kThreads), 0, s, a);
+    return hipFuncSetAttribute((const void *)kv4_attn<D, NT>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                               lds_bytes<D, NT>()) == hipSuccess;
 }
 
-template <int D>
-pn_status launch(const AttnArgs &a, const Cut &t, hipStream_t s)
+bool raise_lds()
 {
-    if constexpr (D == 64)
-        if (t.nt == 4) attn_launch<D, 4>(a, t, s);
-    if constexpr (D <= 128)
-        if (t.nt == 2) attn_launch<D, 2>(a, t, s);
-    if (t.nt == 1) attn_launch<D, 1>(a, t, s);
+    return raise_one<64, 1>() && raise_one<64, 2>() && raise_one<64, 3>() && raise_one<64, 4>() && raise_one<128, 1>() &&
+           raise_one<128, 2>() && raise_one<128, 3>() && raise_one<128, 4>() && raise_one<256, 1>() && raise_one<256, 2>();
+}
+
+template <int D, int NT>
+pn_status launch(const AttnArgs &a, hipStream_t s)
+{
+    if (!once_per_device(kAttrKv4, raise_lds)) return PN_ELAUNCH;
+    hipLaunchKernelGGL((kv4_attn<D, NT>), dim3((unsigned)a.workers), dim3(kThreads), (lds_bytes<D, NT>()), s, a);
     if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
-    if (t.splits > 1) {
-        const dim3 grid((unsigned)((a.max_q + kWaves - 1) / kWaves), (unsigned)a.q_heads, (unsigned)a.B);
-        hipLaunchKernelGGL((kv4_merge<D>), grid, dim3(kThreads), 0, s, a, 16 * t.nt);
+    if (!a.whole) {
+        hipLaunchKernelGGL((kv4_join<D, NT>), dim3((unsigned)(a.tiles * (D / 64)), (unsigned)a.c.heads, (unsigned)a.B),
+                           dim3(1024), 0, s, a);
         if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
     }
     return PN_OK;
+}
+
+template <int D>
+pn_status launch_rows(const AttnArgs &a, int nt, hipStream_t s)
+{
+    if (nt == 1) return launch<D, 1>(a, s);
+    if (nt == 2) return launch<D, 2>(a, s);
+    if constexpr (D <= 128) {
+        if (nt == 3) return launch<D, 3>(a, s);
+        if (nt == 4) return launch<D, 4>(a, s);
+    }
+    return PN_EUNSUPPORTED;
 }
 
 bool sizes_ok(const pn_kv4_cache *c, int q_heads, int B, int64_t total_q, int64_t max_q, int64_t max_kv, int sinks)
@@ -647,23 +850,17 @@ bool sizes_fit(const pn_kv4_cache *c, int q_heads, int B, int64_t total_q, int64
            max_q * (q_heads / c->heads) <= INT32_MAX / 4;
 }
 
-size_t split_bytes(const pn_kv4_cache *c, int q_heads, int64_t total_q)
-{
-    return (size_t)total_q * q_heads * (c->dim + 4) * sizeof(float);
-}
-
 }  // namespace
 
 extern "C" size_t pn_kv4_attn_workspace(const pn_kv4_cache *cache, int q_heads, int B, int64_t total_q, int64_t max_q,
                                         int64_t max_kv, int window, int sinks)
 {
     Kv4 c;
-    if (check_cache(cache, &c) || !sizes_ok(cache, q_heads, B, total_q, max_q, max_kv, sinks) ||
-        !sizes_fit(cache, q_heads, B, total_q, max_q < total_q ? max_q : total_q, max_kv))
-        return 0;
-    if (total_q == 0) return 0;
-    const Cut t = cut(cache, q_heads, B, max_q < total_q ? max_q : total_q, max_kv, window, sinks);
-    return t.splits > 1 ? t.splits * split_bytes(cache, q_heads, total_q) : 0;
+    if (check_cache(cache, &c) || !sizes_ok(cache, q_heads, B, total_q, max_q, max_kv, sinks) || total_q == 0) return 0;
+    if (max_q > total_q) max_q = total_q;
+    if (!sizes_fit(cache, q_heads, B, total_q, max_q, max_kv)) return 0;
+    const Cut t = cut(cache, q_heads, B, max_q, max_kv, window, sinks);
+    return t.whole ? 0 : t.workers * t.part + t.cuts;
 }
 
 extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, int64_t ldq, int q_heads,
@@ -686,28 +883,22 @@ extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, i
     if (!sizes_fit(cache, q_heads, B, total_q, max_q, max_kv)) return PN_EUNSUPPORTED;
     if (total_q == 0) return PN_OK;
     Cut t = cut(cache, q_heads, B, max_q, max_kv, window, sinks);
-    if (t.splits > 1) {
-        const size_t one = split_bytes(cache, q_heads, total_q);
-        if (ws_bytes / one < (size_t)t.splits) {  // as many splits as there is room for
-            const int fit = (int)(ws_bytes / one);
-            const int64_t steps = (int64_t)t.chunk * t.splits;
-            if (fit < 2) {
-                t.chunk = (int)steps;
-                t.splits = 1;
-            } else {
-                t.chunk = (int)((steps + fit - 1) / fit);
-                t.splits = (int)((steps + t.chunk - 1) / t.chunk);
-            }
-        }
+    if (t.tiles * 4 > INT32_MAX) return PN_EUNSUPPORTED;
+    if (!t.whole && ws_bytes < t.workers * t.part + t.cuts) {
+        // As many workgroups as there is room for, while that leaves most of
+        // the device at work; else every item is one workgroup's.
+        const int fit = ws_bytes > t.cuts ? (int)((ws_bytes - t.cuts) / t.part) : 0;
+        if (fit >= t.workers / 4) t.workers = fit;
+        else t.whole = true;
     }
-    if (t.row_tiles * t.splits > INT32_MAX) return PN_EUNSUPPORTED;
     a.q = q;
     a.q_start = q_start;
     a.kv_len = kv_len;
     a.table = table;
     a.out = out;
     a.part = (float *)ws;
-    a.lse = (float *)ws + (size_t)t.splits * total_q * q_heads * cache->dim;
+    a.part_ml = (float2 *)(a.part + (size_t)t.workers * 2 * t.nt * cache->dim * 16);
+    a.cuts = (int2 *)((char *)ws + t.workers * t.part);
     a.ldq = ldq;
     a.ldo = ldo;
     a.ld_table = ld_table;
@@ -720,13 +911,16 @@ extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, i
     a.max_pages = (int)pages;
     a.window = window;
     a.sinks = sinks;
-    a.splits = t.splits;
-    a.chunk = t.chunk;
-    a.scale2 = scale * 1.4426950408889634f;
+    a.workers = t.workers;
+    a.whole = t.whole;
+    a.tiles = (int)t.tiles;
+    a.negate = scale < 0.0f;
+    // Not 0: a masked score is -inf, whose product with c2 has to stay so.
+    a.c2 = __builtin_fmaxf(__builtin_fabsf(scale) * 1.4426950408889634f, 0x1p-100f);
     const hipStream_t s = (hipStream_t)stream;
-    const pn_status st = cache->dim == 64    ? launch<64>(a, t, s)
-                         : cache->dim == 128 ? launch<128>(a, t, s)
-                                             : launch<256>(a, t, s);
+    const pn_status st = cache->dim == 64    ? launch_rows<64>(a, t.nt, s)
+                         : cache->dim == 128 ? launch_rows<128>(a, t.nt, s)
+                                             : launch_rows<256>(a, t.nt, s);
     if (st == PN_OK) g_last_variant = kVarKv4Attn;
     return st;
 }

@@ -121,7 +121,7 @@ def test_attn_checks(kw, status):
 def test_attn_workspace_sizes():
     c = cache(heads=4, dim=128, num=1000)
     one = B.pn_kv4_attn_workspace(c, 24, 1, 1, 1, 16384)
-    assert one > 0 and one % (24 * 132 * 4) == 0
+    assert 0 < one < 64 << 20
     assert B.pn_kv4_attn_workspace(c, 24, 1, 1, 1, 16) == 0  # nothing to split
     assert B.pn_kv4_attn_workspace(c, 25, 1, 1, 1, 16384) == 0  # refused sizes
     assert B.pn_kv4_attn_workspace(c, 24, 1, 0, 1, 16384) == 0
