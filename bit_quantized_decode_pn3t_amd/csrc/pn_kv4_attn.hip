@@ -52,6 +52,7 @@ namespace {
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float4_t __attribute__((ext_vector_type(4)));
 typedef unsigned short ushort2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 
 constexpr int kThreads = 512;
@@ -172,19 +173,20 @@ template <int D> struct Ring {
     }
 };
 
-// A lane's offsets within a head's part of a page.
+// A lane's offsets within a head's part of a page (k[1] less the 1024 that
+// its instruction adds).
 template <int D> struct Offsets {
-    int k[Ring<D>::kEach], v, s;
+    int k[D == 256 ? 2 : 1], v, s;
     __device__ __forceinline__ void set(int lane, int P)
     {
         using G = Ring<D>;
         using L = Kv4Layout<D>;
 #pragma unroll
-        for (int j = 0; j < G::kEach; ++j) {
+        for (int j = 0; j < (D == 256 ? 2 : 1); ++j) {
             const int x = 64 * j + lane;
             if (D == 64) k[j] = 4 * x;
             else if (D == 128) k[j] = 64 * (x >> 2) + 16 * ((x & 3) ^ (x >> 4));
-            else k[j] = 128 * (x >> 3) + 16 * ((x & 7) ^ (x >> 4 & 7));
+            else k[j] = 128 * (x >> 3) + 16 * ((x & 7) ^ (x >> 4 & 7)) - 1024 * j;
         }
         v = L::v_codes(P) + G::kWide * lane;
         s = lane < 8 * G::R ? L::k_scales(P) + 4 * lane
@@ -192,7 +194,10 @@ template <int D> struct Offsets {
     }
 };
 
-// The pages of a step's two 16-token tiles (-1: not of the cache).
+// The pages of a step's two 16-token tiles (-1: not of the cache).  Scalar
+// loads: a vector load here would be the youngest behind the ring's, and
+// waiting for it would wait for all of those.
+#define PN_CONST __attribute__((address_space(4)))
 struct Pages {
     int32_t p[2];
 };
@@ -203,7 +208,7 @@ __device__ __forceinline__ Pages pages_of(const AttnArgs &a, const int32_t *row,
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int at = (step * kStep + 16 * i) >> a.c.shift;
-        t.p[i] = at < a.max_pages ? row[at] : -1;
+        t.p[i] = at < a.max_pages ? ((const PN_CONST int32_t *)row)[uniform(at)] : -1;
     }
     return t;
 }
@@ -213,12 +218,50 @@ __device__ __forceinline__ int32_t valid(const AttnArgs &a, int32_t p)
     return uniform((uint32_t)p < (uint32_t)a.c.num_pages ? p : -1);
 }
 
-// Loads of 4 or 16 bytes a lane into LDS.
-template <int BYTES>
-__device__ __forceinline__ void load_lds(const __amdgpu_buffer_rsrc_t &rs, uint8_t *to, int lane_off, int off)
+// One tile's loads into LDS: K codes to m_k on, V codes to m_v on, scales to
+// m_s, from page offsets o_k, o_v, o_s and the lane's own.  The compiler does
+// not see these loads, so that it does not wait for all of them before any
+// LDS read (it cannot tell the stages of a ring apart); they have no register
+// results, and wait_loads counts them.  An offset in the instruction moves
+// both addresses.  s_nop 4: a scalar register that a vector instruction
+// wrote must not be read by a load for five states; s_nop 0: nor M0 for one.
+// (M0 is the compiler's to use, but nothing else here uses it.)
+template <int D>
+__device__ __forceinline__ void load_tile(u32x4_t rs, const Offsets<D> &off, uint32_t m_k, uint32_t m_v, uint32_t m_s,
+                                          int o_k, int o_v, int o_s)
 {
-    if constexpr (BYTES == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)to, 16, lane_off, off, 0, 0);
-    else __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)to, 4, lane_off, off, 0, 0);
+    if constexpr (D == 64) {
+        asm volatile("s_nop 4\n\ts_mov_b32 m0, %4\n\ts_nop 0\n\t"
+                     "buffer_load_dword %0, %3, %7 offen lds\n\t"
+                     "buffer_load_dword %0, %3, %7 offen offset:256 lds\n\t"
+                     "s_mov_b32 m0, %5\n\ts_nop 0\n\t"
+                     "buffer_load_dword %1, %3, %8 offen lds\n\t"
+                     "buffer_load_dword %1, %3, %8 offen offset:256 lds\n\t"
+                     "s_mov_b32 m0, %6\n\ts_nop 0\n\t"
+                     "buffer_load_dword %2, %3, %9 offen lds"
+                     :: "v"(off.k[0]), "v"(off.v), "v"(off.s), "s"(rs), "s"(m_k), "s"(m_v), "s"(m_s), "s"(o_k), "s"(o_v),
+                     "s"(o_s) : "memory");
+    } else if constexpr (D == 128) {
+        asm volatile("s_nop 4\n\ts_mov_b32 m0, %4\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %0, %3, %7 offen lds\n\t"
+                     "s_mov_b32 m0, %5\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %1, %3, %8 offen lds\n\t"
+                     "s_mov_b32 m0, %6\n\ts_nop 0\n\t"
+                     "buffer_load_dword %2, %3, %9 offen lds"
+                     :: "v"(off.k[0]), "v"(off.v), "v"(off.s), "s"(rs), "s"(m_k), "s"(m_v), "s"(m_s), "s"(o_k), "s"(o_v),
+                     "s"(o_s) : "memory");
+    } else {
+        asm volatile("s_nop 4\n\ts_mov_b32 m0, %5\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %0, %4, %8 offen lds\n\t"
+                     "buffer_load_dwordx4 %1, %4, %8 offen offset:1024 lds\n\t"
+                     "s_mov_b32 m0, %6\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %2, %4, %9 offen lds\n\t"
+                     "buffer_load_dwordx4 %2, %4, %9 offen offset:1024 lds\n\t"
+                     "s_mov_b32 m0, %7\n\ts_nop 0\n\t"
+                     "buffer_load_dword %3, %4, %10 offen lds"
+                     :: "v"(off.k[0]), "v"(off.k[1]), "v"(off.v), "v"(off.s), "s"(rs), "s"(m_k), "s"(m_v), "s"(m_s),
+                     "s"(o_k), "s"(o_v), "s"(o_s) : "memory");
+    }
 }
 
 // Start the loads of a step (none: `there` false; the count stays the same).
@@ -228,20 +271,18 @@ __device__ __forceinline__ void stage(const AttnArgs &a, uint8_t *to, const Offs
 {
     using G = Ring<D>;
     using L = Kv4Layout<D>;
+    const uint32_t m = uniform((int)(uint32_t)(size_t)(lds_void *)to);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int32_t page = valid(a, t.p[i]);
         const int o = (step * kStep + 16 * i) & ((1 << a.c.shift) - 1);
         const bool some = there && page >= 0;
-        const uint8_t *base = a.c.pages + ((int64_t)(some ? page : 0) * a.c.heads + head) * a.c.chunk;
-        const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, some ? (uint32_t)a.c.chunk : 0u);
-#pragma unroll
-        for (int j = 0; j < G::kEach; ++j)
-            load_lds<G::kWide>(rs, to + i * G::kTile + 64 * G::kWide * j, off.k[j], o * L::kRow);
-#pragma unroll
-        for (int j = 0; j < G::kEach; ++j)
-            load_lds<G::kWide>(rs, to + G::kV + i * G::kTile + 64 * G::kWide * j, off.v, o * L::kRow + 64 * G::kWide * j);
-        load_lds<4>(rs, to + G::kScales + 256 * i, off.s, o * 2 * G::R);
+        const uint64_t base = (uint64_t)(a.c.pages + ((int64_t)(some ? page : 0) * a.c.heads + head) * a.c.chunk);
+        // raw buffer: 48-bit base, no stride, the head's part of the page (or nothing) in range
+        const u32x4_t rs = {(uint32_t)uniform((int)base), (uint32_t)uniform((int)(base >> 32) & 0xffff),
+                            some ? (uint32_t)a.c.chunk : 0u, 0x00020000u};
+        load_tile<D>(rs, off, m + i * G::kTile, m + G::kV + i * G::kTile, m + G::kScales + 256 * i, o * L::kRow, o * L::kRow,
+                     o * 2 * G::R);
     }
 }
 
@@ -613,7 +654,7 @@ __global__ __launch_bounds__(kThreads) void kv4_attn(AttnArgs a)
         auto place = [&](int e) { return e < w.sink_steps ? e : e - w.sink_steps + w.lo; };
         const int e1 = uniform((int)((int64_t)s1 * w.steps / c.steps));
         int e = uniform((int)((int64_t)s0 * w.steps / c.steps)) + wave;
-        const int32_t *row = a.table + (int64_t)b * a.ld_table;
+        const int32_t *row = uniform_ptr(a.table + (int64_t)b * a.ld_table);
         // pages of the steps in the ring, and of the next to be staged
         Pages held[G::kStages + 1];
 #pragma unroll
