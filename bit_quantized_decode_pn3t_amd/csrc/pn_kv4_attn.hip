@@ -149,9 +149,26 @@ __device__ __forceinline__ int64_t length(const AttnArgs &a, const Cost &c)
     return (int64_t)(c.steps + kOver) * c.tiles * a.c.heads;
 }
 
+// The same in every lane: into scalar registers.
+__device__ __forceinline__ Cost scalar(const Cost &m)
+{
+    Cost c;
+    c.w.q0 = (int64_t)(((uint64_t)(uint32_t)uniform((int)(m.w.q0 >> 32)) << 32) | (uint32_t)uniform((int)m.w.q0));
+    c.w.qn = uniform(m.w.qn);
+    c.w.first = uniform(m.w.first);
+    c.w.len = uniform(m.w.len);
+    c.steps = uniform(m.steps);
+    c.tiles = uniform(m.tiles);
+    c.w.sink_steps = c.w.lo = c.w.steps = 0;  // the row tile's, to be filled in
+    return c;
+}
+
 // ---------------------------------------------------------------------------
 // A wave's ring of staged steps.
 // ---------------------------------------------------------------------------
+// Two workgroups share a compute unit where registers and LDS allow it.
+template <int D, int NT> constexpr int waves_per_simd() { return D < 256 && NT == 1 ? 4 : 2; }
+
 template <int D> struct Ring {
     using L = Kv4Layout<D>;
     static constexpr int R = L::R;
@@ -159,7 +176,7 @@ template <int D> struct Ring {
     static constexpr int kV = 2 * kTile;               // K of both tiles, then V, then the scales
     static constexpr int kScales = 4 * kTile;          // of a tile: K's, V's (32 R bytes each), 256 bytes kept
     static constexpr int kStage = kScales + 512;
-    static constexpr int kStages = D == 256 ? 2 : D == 128 ? 3 : 4;
+    static constexpr int kStages = D == 64 ? 3 : 2;
     static constexpr int kWide = D == 64 ? 4 : 16;     // bytes of a lane's DMA
     static constexpr int kEach = kTile / (64 * kWide); // DMA instructions of a tile's codes
     static constexpr int kLoads = 2 * (2 * kEach + 1); // of a step
@@ -202,13 +219,13 @@ struct Pages {
     int32_t p[2];
 };
 
-__device__ __forceinline__ Pages pages_of(const AttnArgs &a, const int32_t *row, int step)
+__device__ __forceinline__ Pages pages_of(const AttnArgs &a, const int32_t *row, int step, bool there)
 {
     Pages t;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int at = (step * kStep + 16 * i) >> a.c.shift;
-        t.p[i] = at < a.max_pages ? ((const PN_CONST int32_t *)row)[uniform(at)] : -1;
+        t.p[i] = there && at < a.max_pages ? ((const PN_CONST int32_t *)row)[uniform(at)] : -1;
     }
     return t;
 }
@@ -264,10 +281,11 @@ __device__ __forceinline__ void load_tile(u32x4_t rs, const Offsets<D> &off, uin
     }
 }
 
-// Start the loads of a step (none: `there` false; the count stays the same).
+// Start the loads of a step (pages of -1 load nothing; the count stays the
+// same).  head_base: the head's part of page 0.
 template <int D>
 __device__ __forceinline__ void stage(const AttnArgs &a, uint8_t *to, const Offsets<D> &off, const Pages &t, int step,
-                                      int head, bool there)
+                                      uint64_t head_base, int32_t page_bytes)
 {
     using G = Ring<D>;
     using L = Kv4Layout<D>;
@@ -276,11 +294,10 @@ __device__ __forceinline__ void stage(const AttnArgs &a, uint8_t *to, const Offs
     for (int i = 0; i < 2; ++i) {
         const int32_t page = valid(a, t.p[i]);
         const int o = (step * kStep + 16 * i) & ((1 << a.c.shift) - 1);
-        const bool some = there && page >= 0;
-        const uint64_t base = (uint64_t)(a.c.pages + ((int64_t)(some ? page : 0) * a.c.heads + head) * a.c.chunk);
+        const uint64_t base = head_base + (uint64_t)(uint32_t)(page < 0 ? 0 : page) * (uint32_t)page_bytes;
         // raw buffer: 48-bit base, no stride, the head's part of the page (or nothing) in range
         const u32x4_t rs = {(uint32_t)uniform((int)base), (uint32_t)uniform((int)(base >> 32) & 0xffff),
-                            some ? (uint32_t)a.c.chunk : 0u, 0x00020000u};
+                            page < 0 ? 0u : (uint32_t)a.c.chunk, 0x00020000u};
         load_tile<D>(rs, off, m + i * G::kTile, m + G::kV + i * G::kTile, m + G::kScales + 256 * i, o * L::kRow, o * L::kRow,
                      o * 2 * G::R);
     }
@@ -327,13 +344,28 @@ template <int N> __device__ __forceinline__ float half_at(const uint32_t (&w)[N]
     return (float)as_half2(w[h >> 1])[h & 1];
 }
 
+// The larger of two, of three.  (fmaxf first quiets NaNs, one instruction an
+// operand; there are none here, and one would come through.)
+__device__ __forceinline__ float max2(float a, float b)
+{
+    float r;
+    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
 // Largest over, or sum of, the four 16-lane groups, in all of them.
 __device__ __forceinline__ float group_max(float v)
 {
     auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    v = max2(__uint_as_float(a[0]), __uint_as_float(a[1]));
     auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+    return max2(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 __device__ __forceinline__ float group_sum(float v)
 {
@@ -433,17 +465,31 @@ __device__ __forceinline__ void advance(State<D, NT> &st, const uint8_t *from, c
         }
     }
 
-    // the scales against the cap
-    ushort2_t most = {0, 0};
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 2 * R; ++j)
-            most = __builtin_elementwise_max(most, __builtin_bit_cast(ushort2_t, d[i][j] & 0x7fff7fffu));
-    uint32_t big = most[0] > most[1] ? most[0] : most[1];
+        for (int j = 0; j < 2 * R; ++j) asm("" : "+v"(d[i][j]));  // words, not halves
+
+    // The scales against the cap: lane r looks at one word of its group's 4 R.
+    uint32_t big;
+    {
+        const int x = r & (4 * R - 1), i = x / (2 * R), h = x % (2 * R);
+        uint32_t w = *(const uint32_t *)(from + G::kScales + 256 * i + 32 * R + 8 * R * g + 4 * h) & 0x7fff7fffu;
+        if (mask.some) {  // as above
+            const int32_t under = a.window > 0 ? mask.low - a.window : -1;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int key = mask.token0 + 16 * i + 4 * g + (2 * h + y) / R;
+                const bool ok = (i ? mask.page[1] : mask.page[0]) && key < mask.end && key <= mask.high &&
+                                (key > under || key < a.sinks);
+                if (!ok) w &= y ? 0x0000ffffu : 0xffff0000u;
+            }
+        }
+        big = (w >> 16) > (w & 0xffffu) ? w >> 16 : w & 0xffffu;
+    }
     if (__ballot(big > st.cap)) {
 #pragma unroll
-        for (int x = 16; x < 64; x <<= 1) {
+        for (int x = 1; x < 64; x <<= 1) {
             const uint32_t y = __shfl_xor(big, x, 64);
             big = y > big ? y : big;
         }
@@ -468,10 +514,10 @@ __device__ __forceinline__ void advance(State<D, NT> &st, const uint8_t *from, c
     half8_t p[NT][R];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        float mx = fmaxf(fmaxf(sc[n][0][0], sc[n][0][1]), sc[n][0][2]);
-        mx = fmaxf(fmaxf(mx, sc[n][0][3]), sc[n][1][0]);
-        mx = fmaxf(fmaxf(mx, sc[n][1][1]), sc[n][1][2]);
-        mx = group_max(fmaxf(mx, sc[n][1][3]));
+        float mx = max3(sc[n][0][0], sc[n][0][1], sc[n][0][2]);
+        mx = max3(mx, sc[n][0][3], sc[n][1][0]);
+        mx = max3(mx, sc[n][1][1], sc[n][1][2]);
+        mx = group_max(max2(mx, sc[n][1][3]));
         if (__ballot(mx > st.m[n])) {
             const float f = mx > st.m[n] ? __builtin_amdgcn_exp2f((st.m[n] - mx) * a.c2) : 1.0f;
             st.m[n] = fmaxf(st.m[n], mx);
@@ -541,7 +587,7 @@ __device__ __forceinline__ void store_row(uint16_t *out, const float4_t &x, int 
 template <int D, int NT> constexpr int part_floats() { return NT * 4 * (D / 64) * 256; }
 
 template <int D, int NT>
-__global__ __launch_bounds__(kThreads) void kv4_attn(AttnArgs a)
+__global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT>())) void kv4_attn(AttnArgs a)
 {
     using G = Ring<D>;
     constexpr int R = G::R, kRows = 16 * NT;
@@ -549,50 +595,74 @@ __global__ __launch_bounds__(kThreads) void kv4_attn(AttnArgs a)
     __shared__ float ml[kWaves][kRows][2];
     __shared__ int64_t scan[kWaves];
     __shared__ int64_t at_shared[2];
+    __shared__ Cost known[64];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
     uint8_t *ring = lds + wave * (G::kStages * G::kStage);
     half8_t *q = (half8_t *)(lds + G::kBytes);  // [16-row group][32 elements][lane]: operands as the products take them
 
-    // this workgroup's part of the line
-    const int per = (a.B + kThreads - 1) / kThreads;
-    int64_t mine = 0;
-    for (int b = tid * per; b < (tid + 1) * per && b < a.B; ++b) mine += length(a, cost(a, b, kRows));
+    // This workgroup's part of the line.  Up to 64 requests are summed by
+    // every wave for itself and kept in LDS; more are summed by the workgroup
+    // and read again as they come.
+    const bool few = a.B <= 64;
+    int64_t mine = 0, total = 0, before = 0;
+    if (few) {
+        const Cost c = cost(a, lane < a.B ? lane : 0, kRows);
+        mine = lane < a.B ? length(a, c) : 0;
+        if (wave == 0) known[lane] = c;
+    } else {
+        const int per = (a.B + kThreads - 1) / kThreads;
+        for (int b = tid * per; b < (tid + 1) * per && b < a.B; ++b) mine += length(a, cost(a, b, kRows));
+    }
     int64_t sum = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const int64_t x = __shfl_up(sum, d, 64);
         if (lane >= d) sum += x;
     }
-    if (lane == 63) scan[wave] = sum;
-    __syncthreads();
-    int64_t total = 0, before = sum - mine;
-    for (int w = 0; w < kWaves; ++w) {
-        if (w < wave) before += scan[w];
-        total += scan[w];
+    if (few) {
+        total = __shfl(sum, 63, 64);
+        before = sum - mine;
+    } else {
+        if (lane == 63) scan[wave] = sum;
+        __syncthreads();
+        before = sum - mine;
+        for (int w = 0; w < kWaves; ++w) {
+            if (w < wave) before += scan[w];
+            total += scan[w];
+        }
     }
     int64_t share = (total + a.workers - 1) / a.workers;
     if (share < kShare && !a.whole) share = kShare;
     const int64_t lo = blockIdx.x * share, hi = lo + share < total ? lo + share : total;
     if (lo >= total) return;  // the whole workgroup
-    if (lo >= before && lo < before + mine) {  // one thread
-        int b = tid * per;
-        for (;; ++b) {
-            const int64_t n = length(a, cost(a, b, kRows));
-            if (lo < before + n) break;
-            before += n;
+    if (few) __syncthreads();
+    const bool here = lo >= before && lo < before + mine;  // one lane of each wave, or one thread
+    int b;
+    int64_t start;  // of request b on the line
+    if (few) {
+        b = __builtin_ctzll(__ballot(here));
+        start = __shfl(before, b, 64);
+    } else {
+        if (here) {
+            int x = tid * ((a.B + kThreads - 1) / kThreads);
+            for (;; ++x) {
+                const int64_t n = length(a, cost(a, x, kRows));
+                if (lo < before + n) break;
+                before += n;
+            }
+            at_shared[0] = x;
+            at_shared[1] = before;
         }
-        at_shared[0] = b;
-        at_shared[1] = before;
+        __syncthreads();
+        b = uniform((int)at_shared[0]);
+        start = at_shared[1];
     }
-    __syncthreads();
-    int b = uniform((int)at_shared[0]);
-    int64_t start = at_shared[1];  // of request b on the line
     Offsets<D> off;
     off.set(lane, 1 << a.c.shift);
 
     for (int64_t x = lo; x < hi;) {
-        const Cost c = cost(a, b, kRows);
+        const Cost c = scalar(few ? known[b] : cost(a, b, kRows));
         const int64_t all = length(a, c);
         if (x >= start + all) {
             start += all;
@@ -655,14 +725,16 @@ __global__ __launch_bounds__(kThreads) void kv4_attn(AttnArgs a)
         const int e1 = uniform((int)((int64_t)s1 * w.steps / c.steps));
         int e = uniform((int)((int64_t)s0 * w.steps / c.steps)) + wave;
         const int32_t *row = uniform_ptr(a.table + (int64_t)b * a.ld_table);
+        const uint64_t head_base = (uint64_t)a.c.pages + (uint64_t)head * a.c.chunk;
+        const int32_t page_bytes = a.c.heads * a.c.chunk;
         // pages of the steps in the ring, and of the next to be staged
         Pages held[G::kStages + 1];
 #pragma unroll
-        for (int i = 0; i <= G::kStages; ++i) held[i] = pages_of(a, row, e + kWaves * i < e1 ? place(e + kWaves * i) : 0);
+        for (int i = 0; i <= G::kStages; ++i) held[i] = pages_of(a, row, place(e + kWaves * i), e + kWaves * i < e1);
 #pragma unroll
         for (int i = 0; i < G::kStages; ++i) {
             const int s = e + kWaves * i;
-            stage<D>(a, ring + i * G::kStage, off, held[i], place(s), head, s < e1);
+            stage<D>(a, ring + i * G::kStage, off, held[i], place(s), head_base, page_bytes);
         }
         // the queries are there; a bare barrier, so that the loads fly on
         __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
@@ -687,10 +759,10 @@ __global__ __launch_bounds__(kThreads) void kv4_attn(AttnArgs a)
             __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the stage has been read
             asm volatile("" ::: "memory");
             const int s = e + kWaves * G::kStages, s2 = s + kWaves;
-            stage<D>(a, from, off, held[G::kStages], place(s), head, s < e1);
+            stage<D>(a, from, off, held[G::kStages], place(s), head_base, page_bytes);
 #pragma unroll
             for (int y = 0; y < G::kStages; ++y) held[y] = held[y + 1];
-            held[G::kStages] = pages_of(a, row, s2 < e1 ? place(s2) : 0);
+            held[G::kStages] = pages_of(a, row, place(s2), s2 < e1);
         }
         wait_loads<0>();  // nothing is written into the ring any more
 
@@ -748,25 +820,33 @@ __global__ __launch_bounds__(kThreads) void kv4_attn(AttnArgs a)
 template <int D, int NT>
 __global__ __launch_bounds__(1024) void kv4_join(AttnArgs a)
 {
-    constexpr int R = D / 64, kRows = 16 * NT, kDeep = 8;
+    constexpr int R = D / 64, kRows = 16 * NT;
     __shared__ float4_t frag[16][64];
     __shared__ float2 ml[64][16];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
     const int tile = blockIdx.x / R, y = blockIdx.x % R, head = blockIdx.y, b = blockIdx.z;
+    const int2 c = a.cuts[((int64_t)b * a.c.heads + head) * a.tiles + tile];
     const Work w = request(a, b);
     const int row0 = tile * kRows, rows = w.qn * a.group;
-    if (row0 >= rows) return;  // the whole workgroup, as below
-    const int2 c = a.cuts[((int64_t)b * a.c.heads + head) * a.tiles + tile];
     const int parts = uniform(c.y - c.x + 1);
-    if (parts < 2) return;
+    if (row0 >= rows || parts < 2) return;  // the whole workgroup; without rows the record is not one
     // The first workgroup has the item's start (its part 1), the others go on with it (their part 0).
     auto part = [&](int j) { return 2 * ((int64_t)c.x + j) + (j == 0 ? 1 : 0); };
     const int i = wave & 3;
 #pragma unroll 1
     for (int n = 0; n < NT; ++n) {
-        // rows' (m, l) of all parts: 64 parts at a time, one a thread
         float m = kLowest, l = 0.0f;
+        float4_t o = {0, 0, 0, 0};
+        // 64 parts at a time: each wave takes a fourth of them for its
+        // product, and the rows' (m, l) come one a thread
         for (int j0 = 0; j0 < parts; j0 += 64) {
+            float4_t v[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                const int j = j0 + (wave >> 2) + 4 * x;
+                v[x] = (float4_t){0, 0, 0, 0};
+                if (j < parts) v[x] = ((const float4_t *)a.part)[part(j) * (part_floats<D, NT>() / 4) + (n * 4 * R + 4 * y + i) * 64 + lane];
+            }
             const int j = j0 + ((int)threadIdx.x >> 4);
             const float2 x = j < parts ? a.part_ml[part(j) * kRows + 16 * n + (threadIdx.x & 15)] : make_float2(kLowest, 0.0f);
             __syncthreads();
@@ -775,25 +855,17 @@ __global__ __launch_bounds__(1024) void kv4_join(AttnArgs a)
             float top = m;
             for (int j2 = g; j2 < 64; j2 += 4) top = fmaxf(top, ml[j2][r].x);
             top = group_max(top);
-            l *= __builtin_amdgcn_exp2f((m - top) * a.c2);
+            const float f = __builtin_amdgcn_exp2f((m - top) * a.c2);
+            l *= f;
+            o *= f;
             for (int j2 = g; j2 < 64; j2 += 4) l += ml[j2][r].y * __builtin_amdgcn_exp2f((ml[j2][r].x - top) * a.c2);
+#pragma unroll
+            for (int x2 = 0; x2 < 16; ++x2)
+                if (j0 + (wave >> 2) + 4 * x2 < parts)
+                    o += v[x2] * __builtin_amdgcn_exp2f((ml[(wave >> 2) + 4 * x2][r].x - top) * a.c2);
             m = top;
         }
         l = group_sum(l);
-        float4_t o = {0, 0, 0, 0};
-        for (int j0 = wave >> 2; j0 < parts; j0 += 4 * kDeep) {
-            float4_t v[kDeep];
-            float f[kDeep];
-#pragma unroll
-            for (int x = 0; x < kDeep; ++x) {
-                const int j = j0 + 4 * x < parts ? j0 + 4 * x : parts - 1;
-                v[x] = ((const float4_t *)a.part)[part(j) * (part_floats<D, NT>() / 4) + (n * 4 * R + 4 * y + i) * 64 + lane];
-                f[x] = a.part_ml[part(j) * kRows + 16 * n + r].x;
-            }
-#pragma unroll
-            for (int x = 0; x < kDeep; ++x)
-                if (j0 + 4 * x < parts) o += v[x] * __builtin_amdgcn_exp2f((f[x] - m) * a.c2);
-        }
         __syncthreads();
         frag[wave][lane] = o;
         __syncthreads();
@@ -831,7 +903,7 @@ Cut cut(const pn_kv4_cache *c, int q_heads, int B, int64_t max_q, int64_t max_kv
         const int64_t reach = (int64_t)window + max_q + sinks + 2 * kStep;
         if (reach < keys) keys = reach;
     }
-    t.workers = device_cus();
+    t.workers = device_cus() * (c->dim < 256 && t.nt == 1 ? 2 : 1);
     t.whole = keys <= 2 * kShare * kStep;
     t.part = 2 * sizeof(float) * t.nt * (c->dim * 16 + 32);
     t.cuts = (size_t)B * c->heads * t.tiles * sizeof(int2);
