@@ -1,7 +1,7 @@
 // pn_kv4_attn.hip - attention over the paged pn4t cache (pn_kv4_attn), for
 // AMD Instinct MI355X (gfx950).
 //
-//   out = sum_t w_t v_t / sum_t w_t,   w_t = exp2(c s_t - m),  c = scale log2(e)
+//   out = sum_t w_t v_t / sum_t w_t,   w_t = exp2(c (s_t - m)),  c = scale log2(e)
 //   s_t = sum_b dk[t][b] * (sum over block b of q . (n_k - 8))
 //
 // One pass over the keys with a running maximum and sum for each row (rows:
@@ -18,11 +18,13 @@
 //                 4 g .. 4 g + 3 of both 16-token tiles.  V's codes enter
 //                 exactly too; the scale of a token's block multiplies the
 //                 weight, and that product is the one rounding to fp16 (half a
-//                 step, 2^-11 relative).  Weights are <= 1 and scales may have
-//                 any fp16 size, so each wave keeps a power of two 2^u that
-//                 puts the scales it has met below 2^11, inside the exponent
-//                 of w: with fp32 sums nothing overflows, and products down to
-//                 2^-25 of the largest keep full precision.
+//                 step, 2^-11 relative).  The running maximum m follows only
+//                 scores that pass it by 4 (in log2), so that O is rarely
+//                 scaled; weights are <= 2^4.  Scales may have any fp16 size,
+//                 so each wave keeps a power of two 2^u, inside the exponent
+//                 of w, that puts the scales it has met below 2^7 first and
+//                 2^11 at most: with fp32 sums nothing overflows, and products
+//                 down to 2^-20 of the largest keep full precision.
 // A row of A is element 2 i + (r >> 3) of word r & 7 of a block (r = lane &
 // 15, product i < 4), so that one product stays in one block; two v_perm-ed
 // words give the token pairs.
@@ -37,10 +39,12 @@
 // into equal parts.  Every workgroup sums the requests for itself.  Later row
 // tiles of a prompt see more keys than earlier ones: a part of an item is a
 // part of the steps it really has, and the tiles are taken from both ends in
-// turn, so that neighbours make up for each other.  A workgroup's eight waves
-// take every eighth step and are joined through LDS; an item cut between
-// workgroups leaves parts in the workspace, which kv4_join adds.  All sums
-// have a fixed order.
+// turn, so that neighbours make up for each other.  With few rows (RG = 1)
+// a workgroup's eight waves take every eighth step of the same rows; with
+// many (RG = 4) four groups of two waves take rows of their own and share the
+// staged steps, one of two each.  The waves of the same rows are joined
+// through LDS; an item cut between workgroups leaves parts in the workspace,
+// which kv4_join adds.  All sums have a fixed order.
 #include "pn_kv4.h"
 #include "pn_device.h"
 
@@ -70,14 +74,22 @@ struct AttnArgs {
     uint16_t *out;
     float *part;      // fragments of a workgroup's first and last cut item
     float2 *part_ml;  // their rows' maxima and sums
-    int2 *cuts;       // [item]: first and last workgroup of the item
+    struct Cutoff *cuts;  // [workgroup]: the item that it leaves unfinished
     int64_t ldq, ldo, ld_table, total_q;
     int64_t max_q, max_kv;
     int32_t q_heads, group, B, max_pages, window, sinks;
     int32_t workers, whole;  // workgroups; whole: items are not cut
-    int32_t tiles;           // row tiles of a request at most
     int32_t negate;          // scale < 0: the queries are negated
     float c2;                // |scale| log2(e), above 0
+    float slack;             // 4 / c2
+};
+
+// An item whose steps go on in the workgroups behind this one.
+struct Cutoff {
+    int64_t q0;          // the request's first query
+    int32_t row0, rows;  // of the tile, of the request
+    int32_t head;
+    int32_t parts;       // workgroups that work on it; 0: none is unfinished
 };
 
 // The part of a request that a row tile works on.
@@ -166,9 +178,6 @@ __device__ __forceinline__ Cost scalar(const Cost &m)
 // ---------------------------------------------------------------------------
 // A wave's ring of staged steps.
 // ---------------------------------------------------------------------------
-// Two workgroups share a compute unit where registers and LDS allow it.
-template <int D, int NT> constexpr int waves_per_simd() { return D < 256 && NT == 1 ? 4 : 2; }
-
 template <int D> struct Ring {
     using L = Kv4Layout<D>;
     static constexpr int R = L::R;
@@ -176,12 +185,8 @@ template <int D> struct Ring {
     static constexpr int kV = 2 * kTile;               // K of both tiles, then V, then the scales
     static constexpr int kScales = 4 * kTile;          // of a tile: K's, V's (32 R bytes each), 256 bytes kept
     static constexpr int kStage = kScales + 512;
-    static constexpr int kStages = D == 64 ? 3 : 2;
     static constexpr int kWide = D == 64 ? 4 : 16;     // bytes of a lane's DMA
     static constexpr int kEach = kTile / (64 * kWide); // DMA instructions of a tile's codes
-    static constexpr int kLoads = 2 * (2 * kEach + 1); // of a step
-    static constexpr int kBytes = kWaves * kStages * kStage;
-    static_assert((kStages - 1) * kLoads < 64, "vmcnt");
 
     // 16-byte piece u (of a key row's D / 32) of row r
     __device__ static constexpr int piece(int r, int u)
@@ -235,71 +240,80 @@ __device__ __forceinline__ int32_t valid(const AttnArgs &a, int32_t p)
     return uniform((uint32_t)p < (uint32_t)a.c.num_pages ? p : -1);
 }
 
-// One tile's loads into LDS: K codes to m_k on, V codes to m_v on, scales to
-// m_s, from page offsets o_k, o_v, o_s and the lane's own.  The compiler does
-// not see these loads, so that it does not wait for all of them before any
-// LDS read (it cannot tell the stages of a ring apart); they have no register
+// One tile's loads into LDS: K codes to m on; V codes to m on and the scales
+// to m_s, from page offsets o, o_s and the lane's own.  The compiler does not
+// see these loads, so that it does not wait for all of them before any LDS
+// read (it cannot tell the stages of a ring apart); they have no register
 // results, and wait_loads counts them.  An offset in the instruction moves
-// both addresses.  s_nop 4: a scalar register that a vector instruction
-// wrote must not be read by a load for five states; s_nop 0: nor M0 for one.
-// (M0 is the compiler's to use, but nothing else here uses it.)
+// both addresses.  s_nop 4: a scalar register that a vector instruction wrote
+// must not be read by a load for five states; s_nop 0: nor M0 for one.  (M0 is
+// the compiler's to use, but nothing else here uses it.)
 template <int D>
-__device__ __forceinline__ void load_tile(u32x4_t rs, const Offsets<D> &off, uint32_t m_k, uint32_t m_v, uint32_t m_s,
-                                          int o_k, int o_v, int o_s)
+__device__ __forceinline__ void load_k(u32x4_t rs, const Offsets<D> &off, uint32_t m, int o)
 {
-    if constexpr (D == 64) {
-        asm volatile("s_nop 4\n\ts_mov_b32 m0, %4\n\ts_nop 0\n\t"
-                     "buffer_load_dword %0, %3, %7 offen lds\n\t"
-                     "buffer_load_dword %0, %3, %7 offen offset:256 lds\n\t"
+    if constexpr (D == 64)
+        asm volatile("s_nop 4\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\t"
+                     "buffer_load_dword %0, %1, %3 offen lds\n\t"
+                     "buffer_load_dword %0, %1, %3 offen offset:256 lds"
+                     :: "v"(off.k[0]), "s"(rs), "s"(m), "s"(o) : "memory");
+    else if constexpr (D == 128)
+        asm volatile("s_nop 4\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %0, %1, %3 offen lds"
+                     :: "v"(off.k[0]), "s"(rs), "s"(m), "s"(o) : "memory");
+    else
+        asm volatile("s_nop 4\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %0, %2, %4 offen lds\n\t"
+                     "buffer_load_dwordx4 %1, %2, %4 offen offset:1024 lds"
+                     :: "v"(off.k[0]), "v"(off.k[1]), "s"(rs), "s"(m), "s"(o) : "memory");
+}
+
+template <int D>
+__device__ __forceinline__ void load_v(u32x4_t rs, const Offsets<D> &off, uint32_t m, int o, uint32_t m_s, int o_s)
+{
+    if constexpr (D == 64)
+        asm volatile("s_nop 4\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\t"
+                     "buffer_load_dword %0, %2, %4 offen lds\n\t"
+                     "buffer_load_dword %0, %2, %4 offen offset:256 lds\n\t"
                      "s_mov_b32 m0, %5\n\ts_nop 0\n\t"
-                     "buffer_load_dword %1, %3, %8 offen lds\n\t"
-                     "buffer_load_dword %1, %3, %8 offen offset:256 lds\n\t"
-                     "s_mov_b32 m0, %6\n\ts_nop 0\n\t"
-                     "buffer_load_dword %2, %3, %9 offen lds"
-                     :: "v"(off.k[0]), "v"(off.v), "v"(off.s), "s"(rs), "s"(m_k), "s"(m_v), "s"(m_s), "s"(o_k), "s"(o_v),
-                     "s"(o_s) : "memory");
-    } else if constexpr (D == 128) {
-        asm volatile("s_nop 4\n\ts_mov_b32 m0, %4\n\ts_nop 0\n\t"
-                     "buffer_load_dwordx4 %0, %3, %7 offen lds\n\t"
+                     "buffer_load_dword %1, %2, %6 offen lds"
+                     :: "v"(off.v), "v"(off.s), "s"(rs), "s"(m), "s"(o), "s"(m_s), "s"(o_s) : "memory");
+    else if constexpr (D == 128)
+        asm volatile("s_nop 4\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %0, %2, %4 offen lds\n\t"
                      "s_mov_b32 m0, %5\n\ts_nop 0\n\t"
-                     "buffer_load_dwordx4 %1, %3, %8 offen lds\n\t"
-                     "s_mov_b32 m0, %6\n\ts_nop 0\n\t"
-                     "buffer_load_dword %2, %3, %9 offen lds"
-                     :: "v"(off.k[0]), "v"(off.v), "v"(off.s), "s"(rs), "s"(m_k), "s"(m_v), "s"(m_s), "s"(o_k), "s"(o_v),
-                     "s"(o_s) : "memory");
-    } else {
-        asm volatile("s_nop 4\n\ts_mov_b32 m0, %5\n\ts_nop 0\n\t"
-                     "buffer_load_dwordx4 %0, %4, %8 offen lds\n\t"
-                     "buffer_load_dwordx4 %1, %4, %8 offen offset:1024 lds\n\t"
-                     "s_mov_b32 m0, %6\n\ts_nop 0\n\t"
-                     "buffer_load_dwordx4 %2, %4, %9 offen lds\n\t"
-                     "buffer_load_dwordx4 %2, %4, %9 offen offset:1024 lds\n\t"
-                     "s_mov_b32 m0, %7\n\ts_nop 0\n\t"
-                     "buffer_load_dword %3, %4, %10 offen lds"
-                     :: "v"(off.k[0]), "v"(off.k[1]), "v"(off.v), "v"(off.s), "s"(rs), "s"(m_k), "s"(m_v), "s"(m_s),
-                     "s"(o_k), "s"(o_v), "s"(o_s) : "memory");
-    }
+                     "buffer_load_dword %1, %2, %6 offen lds"
+                     :: "v"(off.v), "v"(off.s), "s"(rs), "s"(m), "s"(o), "s"(m_s), "s"(o_s) : "memory");
+    else
+        asm volatile("s_nop 4\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %0, %2, %4 offen lds\n\t"
+                     "buffer_load_dwordx4 %0, %2, %4 offen offset:1024 lds\n\t"
+                     "s_mov_b32 m0, %5\n\ts_nop 0\n\t"
+                     "buffer_load_dword %1, %2, %6 offen lds"
+                     :: "v"(off.v), "v"(off.s), "s"(rs), "s"(m), "s"(o), "s"(m_s), "s"(o_s) : "memory");
 }
 
 // Start the loads of a step (pages of -1 load nothing; the count stays the
-// same).  head_base: the head's part of page 0.
-template <int D>
+// same).  head_base: the head's part of page 0.  RG = 1: a wave loads its
+// step whole; RG = 4: row group rg loads K or V of one of the tiles.
+template <int D, int RG>
 __device__ __forceinline__ void stage(const AttnArgs &a, uint8_t *to, const Offsets<D> &off, const Pages &t, int step,
-                                      uint64_t head_base, int32_t page_bytes)
+                                      uint64_t head_base, int32_t page_bytes, int rg)
 {
     using G = Ring<D>;
     using L = Kv4Layout<D>;
     const uint32_t m = uniform((int)(uint32_t)(size_t)(lds_void *)to);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int32_t page = valid(a, t.p[i]);
+    for (int i0 = 0; i0 < (RG == 1 ? 2 : 1); ++i0) {
+        const int i = RG == 1 ? i0 : rg >> 1;
+        const int32_t page = valid(a, i ? t.p[1] : t.p[0]);
         const int o = (step * kStep + 16 * i) & ((1 << a.c.shift) - 1);
         const uint64_t base = head_base + (uint64_t)(uint32_t)(page < 0 ? 0 : page) * (uint32_t)page_bytes;
         // raw buffer: 48-bit base, no stride, the head's part of the page (or nothing) in range
         const u32x4_t rs = {(uint32_t)uniform((int)base), (uint32_t)uniform((int)(base >> 32) & 0xffff),
                             page < 0 ? 0u : (uint32_t)a.c.chunk, 0x00020000u};
-        load_tile<D>(rs, off, m + i * G::kTile, m + G::kV + i * G::kTile, m + G::kScales + 256 * i, o * L::kRow, o * L::kRow,
-                     o * 2 * G::R);
+        if (RG == 1 || !(rg & 1)) load_k<D>(rs, off, m + i * G::kTile, o * L::kRow);
+        if (RG == 1 || (rg & 1))
+            load_v<D>(rs, off, m + G::kV + i * G::kTile, o * L::kRow, m + G::kScales + 256 * i, o * 2 * G::R);
     }
 }
 
@@ -380,11 +394,12 @@ __device__ __forceinline__ float group_sum(float v)
 template <int D, int NT> struct State {
     static constexpr int R = D / 64;
     float4_t o[NT][R][4];
-    float m[NT];   // largest score (before c2), kLowest if none
+    float m[NT];   // the score (before c2) that weights are relative to, kLowest if none
+    float lim[NT]; // score above which m has to follow
     float mm[NT];  // m c2 - u
     float l[NT];   // this lane's share of the sum of exp2(c2 s - mm)
     int u;         // the power of two on the value scales
-    uint32_t cap;  // largest scale (fp16 bits) that 2^u leaves below 2^15
+    uint32_t cap;  // largest scale (fp16 bits) that 2^u leaves below 2^11
 };
 
 // What a step that is not visible as a whole needs to know.
@@ -494,7 +509,7 @@ __device__ __forceinline__ void advance(State<D, NT> &st, const uint8_t *from, c
             big = y > big ? y : big;
         }
         const int e = (int)(big >> 10) < 30 ? (int)(big >> 10) : 30;  // scales < 2^(e - 14)
-        const int u = 25 - e;
+        const int u = 21 - e;
         const float f = __builtin_ldexpf(1.0f, u - st.u);  // the first time l and O are 0
         st.cap = e + 5 > 30 ? 0xffffu : (uint32_t)((e + 5) << 10) - 1;
 #pragma unroll
@@ -518,9 +533,10 @@ __device__ __forceinline__ void advance(State<D, NT> &st, const uint8_t *from, c
         mx = max3(mx, sc[n][0][3], sc[n][1][0]);
         mx = max3(mx, sc[n][1][1], sc[n][1][2]);
         mx = group_max(max2(mx, sc[n][1][3]));
-        if (__ballot(mx > st.m[n])) {
+        if (__ballot(mx > st.lim[n])) {
             const float f = mx > st.m[n] ? __builtin_amdgcn_exp2f((st.m[n] - mx) * a.c2) : 1.0f;
-            st.m[n] = fmaxf(st.m[n], mx);
+            st.m[n] = max2(st.m[n], mx);
+            st.lim[n] = st.m[n] > kLowest ? st.m[n] + a.slack : kLowest;
             st.mm[n] = st.m[n] * a.c2 - (float)st.u;
             st.l[n] *= f;
 #pragma unroll
@@ -582,24 +598,45 @@ __device__ __forceinline__ void store_row(uint16_t *out, const float4_t &x, int 
     }
 }
 
-// Floats of a part's fragments, [n][4 b + i][lane][4]; (m, l) of its rows are
-// apart, [part][row][2], so that the join reads them together.
-template <int D, int NT> constexpr int part_floats() { return NT * 4 * (D / 64) * 256; }
+// How a workgroup's waves are used.
+template <int D, int NT, int RG> struct Shape {
+    using G = Ring<D>;
+    static constexpr int KW = kWaves / RG;             // waves along the keys
+    static constexpr int kRows = 16 * NT * RG;         // of a workgroup
+    static constexpr int kStages = RG > 1 ? 3 : D == 64 ? 3 : 2;
+    static constexpr int kRing = (RG == 1 ? kWaves : KW) * kStages * G::kStage;
+    static constexpr int kLds = kRing + RG * NT * 2 * G::R * 1024;  // and the queries
+    // Steps staged ahead of the one at work.  A wave with a ring of its own
+    // refills a stage when it has read it; a shared stage is refilled one
+    // step later, when a barrier has shown that all have.
+    static constexpr int kAhead = RG == 1 ? kStages : kStages - 1;
+    // Fragments of the join: RG = 1: all waves'; else those of all but the first along the keys.
+    static_assert((RG == 1 ? kWaves : RG * (KW - 1)) * 4 * G::R * 1024 <= kLds, "room for the join");
+    // Floats of a part, [row group][n][4 b + i][lane][4]; (m, l) of its rows
+    // are apart, [part][row][2], so that the join reads them together.
+    static constexpr int kPart = RG * NT * 4 * G::R * 256;
+};
 
-template <int D, int NT>
-__global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT>())) void kv4_attn(AttnArgs a)
+// Two workgroups share a compute unit where registers and LDS allow it.
+template <int D, int NT, int RG> constexpr int waves_per_simd() { return D < 256 && NT == 1 && RG == 1 ? 4 : 2; }
+
+template <int D, int NT, int RG>
+__global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_attn(AttnArgs a)
 {
     using G = Ring<D>;
-    constexpr int R = G::R, kRows = 16 * NT;
+    using S = Shape<D, NT, RG>;
+    constexpr int R = G::R, kRows = S::kRows, KW = S::KW;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // the ring, then the queries
-    __shared__ float ml[kWaves][kRows][2];
+    __shared__ float ml[kWaves][16 * NT][2];
     __shared__ int64_t scan[kWaves];
     __shared__ int64_t at_shared[2];
     __shared__ Cost known[64];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
-    uint8_t *ring = lds + wave * (G::kStages * G::kStage);
-    half8_t *q = (half8_t *)(lds + G::kBytes);  // [16-row group][32 elements][lane]: operands as the products take them
+    const int rg = wave / KW, kg = wave % KW;
+    uint8_t *ring = lds + (RG == 1 ? wave : kg) * (S::kStages * G::kStage);
+    // operands as the products take them: [16-row group][32 elements][lane]
+    half8_t *queries = (half8_t *)(lds + S::kRing), *q = queries + rg * NT * 2 * R * 64;
 
     // This workgroup's part of the line.  Up to 64 requests are summed by
     // every wave for itself and kept in LDS; more are summed by the workgroup
@@ -635,6 +672,7 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT>())) void kv4_attn(
     int64_t share = (total + a.workers - 1) / a.workers;
     if (share < kShare && !a.whole) share = kShare;
     const int64_t lo = blockIdx.x * share, hi = lo + share < total ? lo + share : total;
+    if (tid == 0 && !a.whole) a.cuts[blockIdx.x].parts = 0;
     if (lo >= total) return;  // the whole workgroup
     if (few) __syncthreads();
     const bool here = lo >= before && lo < before + mine;  // one lane of each wave, or one thread
@@ -685,23 +723,24 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT>())) void kv4_attn(
         const bool cut = s0 > 0 || s1 < c.steps;
         const int head = item / c.tiles, turn = item - head * c.tiles;
         const int tile = turn & 1 ? c.tiles - 1 - (turn >> 1) : turn >> 1;
-        if (s0 == 0 && tid == 0 && !a.whole)
-            a.cuts[((int64_t)b * a.c.heads + head) * a.tiles + tile] =
-                make_int2((int)((first + kOver) / share), (int)((first + one - 1) / share));
+        const int tile0 = tile * kRows, rows = c.w.qn * a.group;  // the workgroup's first row, the request's rows
+        if (s0 == 0 && cut && tid == 0)
+            a.cuts[blockIdx.x] = {c.w.q0, tile0, rows, head, (int)((first + one - 1) / share) - (int)blockIdx.x + 1};
 
-        const int row0 = tile * kRows, rows = c.w.qn * a.group;
-        const int last = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
         Work w = c.w;
-        span(a, w, row0 / a.group, last / a.group);
-        const int32_t p0 = w.first + row0 / a.group, p1 = w.first + last / a.group;
+        span(a, w, tile0 / a.group, ((tile0 + kRows < rows ? tile0 + kRows : rows) - 1) / a.group);
+        // the wave's own rows (none: nothing is visible)
+        const int row0 = tile0 + rg * 16 * NT;
+        const int last = (row0 + 16 * NT < rows ? row0 + 16 * NT : rows) - 1;
+        const int32_t p0 = row0 < rows ? w.first + row0 / a.group : -1, p1 = row0 < rows ? w.first + last / a.group : -1;
 
         // the queries into LDS
-        for (int y = tid; y < NT * 2 * R * 64; y += kThreads) {
-            const int at = row0 + 16 * (y / (2 * R * 64)) + (y & 15), i = at / a.group;
+        for (int y = tid; y < RG * NT * 2 * R * 64; y += kThreads) {
+            const int at = tile0 + 16 * (y / (2 * R * 64)) + (y & 15), i = at / a.group;
             const int e = 32 * (y / 64 % (2 * R)) + 8 * (y >> 4 & 3);
             half8_t v = (half8_t)(_Float16)0.0f;
             if (at < rows) v = *(const half8_t *)(a.q + (w.q0 + i) * a.ldq + (head * a.group + at - i * a.group) * D + e);
-            q[y] = a.negate ? -v : v;
+            queries[y] = a.negate ? -v : v;
         }
         State<D, NT> st;
         int32_t pos[NT];
@@ -713,7 +752,7 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT>())) void kv4_attn(
             for (int y = 0; y < R; ++y)
 #pragma unroll
                 for (int i2 = 0; i2 < 4; ++i2) st.o[n][y][i2] = (float4_t){0, 0, 0, 0};
-            st.m[n] = kLowest;
+            st.m[n] = st.lim[n] = kLowest;
             st.mm[n] = 0.0f;
             st.l[n] = 0.0f;
         }
@@ -723,29 +762,42 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT>())) void kv4_attn(
         // The same part of the steps that this tile has.
         auto place = [&](int e) { return e < w.sink_steps ? e : e - w.sink_steps + w.lo; };
         const int e1 = uniform((int)((int64_t)s1 * w.steps / c.steps));
-        int e = uniform((int)((int64_t)s0 * w.steps / c.steps)) + wave;
+        int e = uniform((int)((int64_t)s0 * w.steps / c.steps));
+        const int turns = (e1 - e + KW - 1) / KW;  // the same for all waves
+        e += kg;
         const int32_t *row = uniform_ptr(a.table + (int64_t)b * a.ld_table);
         const uint64_t head_base = (uint64_t)a.c.pages + (uint64_t)head * a.c.chunk;
         const int32_t page_bytes = a.c.heads * a.c.chunk;
         // pages of the steps in the ring, and of the next to be staged
-        Pages held[G::kStages + 1];
+        Pages held[S::kAhead + 1];
 #pragma unroll
-        for (int i = 0; i <= G::kStages; ++i) held[i] = pages_of(a, row, place(e + kWaves * i), e + kWaves * i < e1);
+        for (int i = 0; i <= S::kAhead; ++i) held[i] = pages_of(a, row, place(e + KW * i), e + KW * i < e1);
 #pragma unroll
-        for (int i = 0; i < G::kStages; ++i) {
-            const int s = e + kWaves * i;
-            stage<D>(a, ring + i * G::kStage, off, held[i], place(s), head_base, page_bytes);
-        }
+        for (int i = 0; i < S::kAhead; ++i)
+            stage<D, RG>(a, ring + i * G::kStage, off, held[i], place(e + KW * i), head_base, page_bytes, rg);
         // the queries are there; a bare barrier, so that the loads fly on
         __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        for (int at = 0; e < e1; e += kWaves) {
-            wait_loads<(G::kStages - 1) * G::kLoads>();
-            const int step = place(e), token0 = step * kStep;
+        int at = 0;  // stage of the step at work
+        for (int turn2 = 0; turn2 < turns && (RG > 1 || e < e1); ++turn2, e += KW) {
+            if constexpr (RG == 1) {
+                wait_loads<(S::kStages - 1) * 2 * (2 * G::kEach + 1)>();
+            } else {
+                // this wave's loads of the step have landed; after the
+                // barrier all have, and no wave reads the stage before it
+                if (rg & 1) wait_loads<(S::kStages - 2) * (G::kEach + 1)>();
+                else wait_loads<(S::kStages - 2) * G::kEach>();
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+                const int to = at > 0 ? at - 1 : S::kStages - 1;
+                stage<D, RG>(a, ring + to * G::kStage, off, held[S::kAhead], place(e + KW * S::kAhead), head_base, page_bytes,
+                             rg);
+            }
+            const int token0 = place(e) * kStep;
             uint8_t *from = ring + at * G::kStage;
-            at = at + 1 < G::kStages ? at + 1 : 0;
+            at = at + 1 < S::kStages ? at + 1 : 0;
             Mask mask;
             mask.page[0] = valid(a, held[0].p[0]) >= 0;
             mask.page[1] = valid(a, held[0].p[1]) >= 0;
@@ -755,149 +807,162 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT>())) void kv4_attn(
             mask.high = p1;
             mask.some = !(mask.page[0] && mask.page[1] && token0 + kStep <= w.len && token0 + kStep - 1 <= p0 &&
                           (a.window <= 0 || (int64_t)token0 + a.window > p1 || token0 + kStep <= a.sinks));
-            advance<D, NT>(st, from, q, a, mask, pos, lane);
+            // A row group sees less than its workgroup's tile.
+            const bool none = RG > 1 && (e >= e1 || token0 > p1 ||
+                                         (a.window > 0 && (int64_t)token0 + kStep - 1 + a.window <= p0 && token0 >= a.sinks));
+            if (!none) advance<D, NT>(st, from, q, a, mask, pos, lane);
             __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the stage has been read
             asm volatile("" ::: "memory");
-            const int s = e + kWaves * G::kStages, s2 = s + kWaves;
-            stage<D>(a, from, off, held[G::kStages], place(s), head_base, page_bytes);
+            if constexpr (RG == 1)
+                stage<D, RG>(a, from, off, held[S::kAhead], place(e + KW * S::kAhead), head_base, page_bytes, rg);
 #pragma unroll
-            for (int y = 0; y < G::kStages; ++y) held[y] = held[y + 1];
-            held[G::kStages] = pages_of(a, row, place(s2), s2 < e1);
+            for (int y = 0; y < S::kAhead; ++y) held[y] = held[y + 1];
+            const int s = e + KW * (S::kAhead + 1);
+            held[S::kAhead] = pages_of(a, row, place(s), s < e1);
         }
         wait_loads<0>();  // nothing is written into the ring any more
 
-        // Join the waves: the rows' maxima and sums, then each wave adds its
-        // share of the fragments of all eight.
-        float l[NT];
+        // Join the waves of the same rows: the rows' maxima and sums, then
+        // the fragments.
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            l[n] = __builtin_ldexpf(group_sum(st.l[n]), -st.u);
-            if (g == 0) ml[wave][16 * n + r][0] = st.m[n], ml[wave][16 * n + r][1] = l[n];
+            const float l = __builtin_ldexpf(group_sum(st.l[n]), -st.u);
+            if (g == 0) ml[wave][16 * n + r][0] = st.m[n], ml[wave][16 * n + r][1] = l;
         }
         float4_t *frag = (float4_t *)lds;  // [wave][4 b + i][lane]
         // A share goes on with at most one item, its first (part 0), and
         // leaves at most one unfinished, its last (part 1).
         const int part_at = 2 * (int)blockIdx.x + (s0 == 0 ? 1 : 0);
-        float *part = a.part + (int64_t)part_at * part_floats<D, NT>();
+        float4_t *part = (float4_t *)(a.part + (int64_t)part_at * S::kPart);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             __syncthreads();
             float m = kLowest, all_l = 0.0f;
-            for (int y = 0; y < kWaves; ++y) m = fmaxf(m, ml[y][16 * n + r][0]);
-            for (int y = 0; y < kWaves; ++y)
-                all_l += ml[y][16 * n + r][1] * __builtin_amdgcn_exp2f((ml[y][16 * n + r][0] - m) * a.c2);
+            for (int y = 0; y < KW; ++y) m = max2(m, ml[rg * KW + y][16 * n + r][0]);
+            for (int y = 0; y < KW; ++y)
+                all_l += ml[rg * KW + y][16 * n + r][1] * __builtin_amdgcn_exp2f((ml[rg * KW + y][16 * n + r][0] - m) * a.c2);
             float f = __builtin_ldexpf(__builtin_amdgcn_exp2f((st.m[n] - m) * a.c2), -st.u);
             if (!cut) f = all_l > 0.0f ? f / all_l : 0.0f;
-#pragma unroll
-            for (int y = 0; y < 4 * R; ++y) frag[(wave * 4 * R + y) * 64 + lane] = st.o[n][y >> 2][y & 3] * f;
-            __syncthreads();
-            const int at = row0 + 16 * n + r, i = at / a.group;
-            const bool live = at < rows;
-            uint16_t *out = a.out + (w.q0 + i) * a.ldo + (int64_t)(head * a.group + at - i * a.group) * D;
-#pragma unroll
-            for (int y = wave >> 2; y < R; y += kWaves / 4) {  // block y, product wave & 3
-                const int f4 = 4 * y + (wave & 3);
-                float4_t v = frag[f4 * 64 + lane];
-#pragma unroll
-                for (int z = 1; z < kWaves; ++z) v += frag[(z * 4 * R + f4) * 64 + lane];
+            const int row_at = row0 + 16 * n + r, i = row_at / a.group;
+            const bool live = row_at < rows;
+            uint16_t *out = a.out + (w.q0 + i) * a.ldo + (int64_t)(head * a.group + row_at - i * a.group) * D;
+            auto give = [&](float4_t v, int y, int i4) {  // block y, product i4
                 if (cut) {
-                    if (live) ((float4_t *)part)[(n * 4 * R + f4) * 64 + lane] = v;
+                    if (live) part[((rg * NT + n) * 4 * R + 4 * y + i4) * 64 + lane] = v;
                 } else {
-                    store_row(live ? out : nullptr, v, y, wave & 3, g);
+                    store_row(live ? out : nullptr, v, y, i4, g);
+                }
+            };
+            if constexpr (RG == 1) {  // each wave adds its share of all waves' fragments
+#pragma unroll
+                for (int y = 0; y < 4 * R; ++y) frag[(wave * 4 * R + y) * 64 + lane] = st.o[n][y >> 2][y & 3] * f;
+                __syncthreads();
+#pragma unroll
+                for (int y = wave >> 2; y < R; y += kWaves / 4) {
+                    const int f4 = 4 * y + (wave & 3);
+                    float4_t v = frag[f4 * 64 + lane];
+#pragma unroll
+                    for (int z = 1; z < kWaves; ++z) v += frag[(z * 4 * R + f4) * 64 + lane];
+                    give(v, y, wave & 3);
+                }
+            } else {  // the first along the keys adds the others'
+                if (kg > 0) {
+#pragma unroll
+                    for (int y = 0; y < 4 * R; ++y)
+                        frag[((rg * (KW - 1) + kg - 1) * 4 * R + y) * 64 + lane] = st.o[n][y >> 2][y & 3] * f;
+                }
+                __syncthreads();
+                if (kg == 0) {
+#pragma unroll
+                    for (int y = 0; y < 4 * R; ++y) {
+                        float4_t v = st.o[n][y >> 2][y & 3] * f;
+#pragma unroll
+                        for (int z = 0; z < KW - 1; ++z) v += frag[((rg * (KW - 1) + z) * 4 * R + y) * 64 + lane];
+                        give(v, y >> 2, y & 3);
+                    }
                 }
             }
-            if (cut && wave == 0 && g == 0) {
-                a.part_ml[(int64_t)part_at * kRows + 16 * n + r] = make_float2(m, all_l);
-            }
+            if (cut && kg == 0 && g == 0) a.part_ml[(int64_t)part_at * kRows + (rg * NT + n) * 16 + r] = make_float2(m, all_l);
         }
         __syncthreads();
     }
 }
 
-// Add the parts of items that were cut.  Grid: x = block + R * row tile, y =
-// key-value head, z = request; 16 waves: product i = wave & 3 of the block,
-// a fourth of the parts each.
-template <int D, int NT>
-__global__ __launch_bounds__(1024) void kv4_join(AttnArgs a)
+// Add the parts of an item that a workgroup left unfinished.  Grid: x =
+// workgroup, y = block, z = 16-row group; 16 waves: product i = wave & 3, a
+// fourth of the parts each.
+template <int D>
+__global__ __launch_bounds__(1024) void kv4_join(AttnArgs a, int groups)
 {
-    constexpr int R = D / 64, kRows = 16 * NT;
+    constexpr int R = D / 64;
     __shared__ float4_t frag[16][64];
     __shared__ float2 ml[64][16];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-    const int tile = blockIdx.x / R, y = blockIdx.x % R, head = blockIdx.y, b = blockIdx.z;
-    const int2 c = a.cuts[((int64_t)b * a.c.heads + head) * a.tiles + tile];
-    const Work w = request(a, b);
-    const int row0 = tile * kRows, rows = w.qn * a.group;
-    const int parts = uniform(c.y - c.x + 1);
-    if (row0 >= rows || parts < 2) return;  // the whole workgroup; without rows the record is not one
+    const int y = blockIdx.y, n = blockIdx.z, i = wave & 3;
+    const Cutoff c = a.cuts[blockIdx.x];
+    const int parts = c.parts;
+    if (parts < 2 || c.row0 + 16 * n >= c.rows) return;  // the whole workgroup
     // The first workgroup has the item's start (its part 1), the others go on with it (their part 0).
-    auto part = [&](int j) { return 2 * ((int64_t)c.x + j) + (j == 0 ? 1 : 0); };
-    const int i = wave & 3;
-#pragma unroll 1
-    for (int n = 0; n < NT; ++n) {
-        float m = kLowest, l = 0.0f;
-        float4_t o = {0, 0, 0, 0};
-        // 64 parts at a time: each wave takes a fourth of them for its
-        // product, and the rows' (m, l) come one a thread
-        for (int j0 = 0; j0 < parts; j0 += 64) {
-            float4_t v[16];
+    auto part = [&](int j) { return 2 * ((int64_t)blockIdx.x + j) + (j == 0 ? 1 : 0); };
+    float m = kLowest, l = 0.0f;
+    float4_t o = {0, 0, 0, 0};
+    // 64 parts at a time: each wave takes a fourth of them for its product,
+    // and the rows' (m, l) come one a thread
+    for (int j0 = 0; j0 < parts; j0 += 64) {
+        float4_t v[16];
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                const int j = j0 + (wave >> 2) + 4 * x;
-                v[x] = (float4_t){0, 0, 0, 0};
-                if (j < parts) v[x] = ((const float4_t *)a.part)[part(j) * (part_floats<D, NT>() / 4) + (n * 4 * R + 4 * y + i) * 64 + lane];
-            }
-            const int j = j0 + ((int)threadIdx.x >> 4);
-            const float2 x = j < parts ? a.part_ml[part(j) * kRows + 16 * n + (threadIdx.x & 15)] : make_float2(kLowest, 0.0f);
-            __syncthreads();
-            ml[threadIdx.x >> 4][threadIdx.x & 15] = x;
-            __syncthreads();
-            float top = m;
-            for (int j2 = g; j2 < 64; j2 += 4) top = fmaxf(top, ml[j2][r].x);
-            top = group_max(top);
-            const float f = __builtin_amdgcn_exp2f((m - top) * a.c2);
-            l *= f;
-            o *= f;
-            for (int j2 = g; j2 < 64; j2 += 4) l += ml[j2][r].y * __builtin_amdgcn_exp2f((ml[j2][r].x - top) * a.c2);
-#pragma unroll
-            for (int x2 = 0; x2 < 16; ++x2)
-                if (j0 + (wave >> 2) + 4 * x2 < parts)
-                    o += v[x2] * __builtin_amdgcn_exp2f((ml[(wave >> 2) + 4 * x2][r].x - top) * a.c2);
-            m = top;
+        for (int x = 0; x < 16; ++x) {
+            const int j = j0 + (wave >> 2) + 4 * x;
+            v[x] = (float4_t){0, 0, 0, 0};
+            if (j < parts) v[x] = ((const float4_t *)a.part)[(part(j) * groups + n) * 4 * R * 64 + (4 * y + i) * 64 + lane];
         }
-        l = group_sum(l);
+        const int j = j0 + ((int)threadIdx.x >> 4);
+        const float2 x = j < parts ? a.part_ml[(part(j) * groups + n) * 16 + (threadIdx.x & 15)] : make_float2(kLowest, 0.0f);
         __syncthreads();
-        frag[wave][lane] = o;
+        ml[threadIdx.x >> 4][threadIdx.x & 15] = x;
         __syncthreads();
-        if (wave < 4) {
-            const int at = row0 + 16 * n + r, q = at / a.group;
-            o = frag[wave][lane];
+        float top = m;
+        for (int j2 = g; j2 < 64; j2 += 4) top = max2(top, ml[j2][r].x);
+        top = group_max(top);
+        const float f = __builtin_amdgcn_exp2f((m - top) * a.c2);
+        l *= f;
+        o *= f;
+        for (int j2 = g; j2 < 64; j2 += 4) l += ml[j2][r].y * __builtin_amdgcn_exp2f((ml[j2][r].x - top) * a.c2);
 #pragma unroll
-            for (int x = 1; x < 4; ++x) o += frag[4 * x + wave][lane];
-            const float f = l > 0.0f ? 1.0f / l : 0.0f;
-            uint16_t *out = a.out + (w.q0 + q) * a.ldo + (int64_t)(head * a.group + at - q * a.group) * D;
-            store_row(at < rows ? out : nullptr, o * f, y, wave, g);
-        }
+        for (int x2 = 0; x2 < 16; ++x2)
+            if (j0 + (wave >> 2) + 4 * x2 < parts)
+                o += v[x2] * __builtin_amdgcn_exp2f((ml[(wave >> 2) + 4 * x2][r].x - top) * a.c2);
+        m = top;
+    }
+    l = group_sum(l);
+    frag[wave][lane] = o;
+    __syncthreads();
+    if (wave < 4) {
+        const int at = c.row0 + 16 * n + r, q = at / a.group;
+        o = frag[wave][lane];
+#pragma unroll
+        for (int x = 1; x < 4; ++x) o += frag[4 * x + wave][lane];
+        const float f = l > 0.0f ? 1.0f / l : 0.0f;
+        uint16_t *out = a.out + (c.q0 + q) * a.ldo + (int64_t)(c.head * a.group + at - q * a.group) * D;
+        store_row(at < c.rows ? out : nullptr, o * f, y, wave, g);
     }
 }
 
 // How a call is cut.
 struct Cut {
-    int nt;               // 16-row groups of a wave
-    int64_t tiles;        // row tiles of a request at most
+    int nt, rg;   // 16-row groups of a wave, row groups of a workgroup
     int workers;
     bool whole;
-    size_t part, cuts;    // bytes of one workgroup's parts, of the items' records
+    size_t part;  // bytes that one workgroup's parts and record need
 };
 
-Cut cut(const pn_kv4_cache *c, int q_heads, int B, int64_t max_q, int64_t max_kv, int window, int sinks)
+Cut cut(const pn_kv4_cache *c, int q_heads, int64_t max_q, int64_t max_kv, int window, int sinks)
 {
     Cut t;
-    const int group = q_heads / c->heads;
-    const int64_t rows = max_q * group;
+    const int64_t rows = max_q * (q_heads / c->heads);
     const int most = c->dim == 256 ? 2 : 4;  // that the registers hold
     t.nt = rows >= 16 * most ? most : (int)((rows + 15) / 16);
-    t.tiles = (rows + 16 * t.nt - 1) / (16 * t.nt);
+    t.rg = rows > 32 * most ? 4 : 1;
     int64_t keys = max_kv;
     if (window > 0) {
         const int64_t reach = (int64_t)window + max_q + sinks + 2 * kStep;
@@ -905,48 +970,48 @@ Cut cut(const pn_kv4_cache *c, int q_heads, int B, int64_t max_q, int64_t max_kv
     }
     t.workers = device_cus() * (c->dim < 256 && t.nt == 1 ? 2 : 1);
     t.whole = keys <= 2 * kShare * kStep;
-    t.part = 2 * sizeof(float) * t.nt * (c->dim * 16 + 32);
-    t.cuts = (size_t)B * c->heads * t.tiles * sizeof(int2);
+    const size_t groups = t.rg * t.nt;
+    t.part = 2 * groups * (c->dim * 16 * sizeof(float) + 16 * sizeof(float2)) + sizeof(Cutoff);
     return t;
 }
 
-// The ring and the queries.
-template <int D, int NT> constexpr int lds_bytes() { return Ring<D>::kBytes + NT * 2 * (D / 64) * 1024; }
-
-template <int D, int NT> bool raise_one()
+template <int D, int NT, int RG> bool raise_one()
 {
-    return hipFuncSetAttribute((const void *)kv4_attn<D, NT>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                               lds_bytes<D, NT>()) == hipSuccess;
+    return hipFuncSetAttribute((const void *)kv4_attn<D, NT, RG>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                               Shape<D, NT, RG>::kLds) == hipSuccess;
 }
 
 bool raise_lds()
 {
-    return raise_one<64, 1>() && raise_one<64, 2>() && raise_one<64, 3>() && raise_one<64, 4>() && raise_one<128, 1>() &&
-           raise_one<128, 2>() && raise_one<128, 3>() && raise_one<128, 4>() && raise_one<256, 1>() && raise_one<256, 2>();
+    return raise_one<64, 1, 1>() && raise_one<64, 2, 1>() && raise_one<64, 3, 1>() && raise_one<64, 4, 1>() &&
+           raise_one<64, 4, 4>() && raise_one<128, 1, 1>() && raise_one<128, 2, 1>() && raise_one<128, 3, 1>() &&
+           raise_one<128, 4, 1>() && raise_one<128, 4, 4>() && raise_one<256, 1, 1>() && raise_one<256, 2, 1>() &&
+           raise_one<256, 2, 4>();
 }
 
-template <int D, int NT>
+template <int D, int NT, int RG>
 pn_status launch(const AttnArgs &a, hipStream_t s)
 {
     if (!once_per_device(kAttrKv4, raise_lds)) return PN_ELAUNCH;
-    hipLaunchKernelGGL((kv4_attn<D, NT>), dim3((unsigned)a.workers), dim3(kThreads), (lds_bytes<D, NT>()), s, a);
+    hipLaunchKernelGGL((kv4_attn<D, NT, RG>), dim3((unsigned)a.workers), dim3(kThreads), (Shape<D, NT, RG>::kLds), s, a);
     if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
     if (!a.whole) {
-        hipLaunchKernelGGL((kv4_join<D, NT>), dim3((unsigned)(a.tiles * (D / 64)), (unsigned)a.c.heads, (unsigned)a.B),
-                           dim3(1024), 0, s, a);
+        hipLaunchKernelGGL(kv4_join<D>, dim3((unsigned)a.workers, D / 64, NT * RG), dim3(1024), 0, s, a, NT * RG);
         if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
     }
     return PN_OK;
 }
 
 template <int D>
-pn_status launch_rows(const AttnArgs &a, int nt, hipStream_t s)
+pn_status launch_rows(const AttnArgs &a, const Cut &t, hipStream_t s)
 {
-    if (nt == 1) return launch<D, 1>(a, s);
-    if (nt == 2) return launch<D, 2>(a, s);
+    constexpr int most = D == 256 ? 2 : 4;
+    if (t.rg == 4) return launch<D, most, 4>(a, s);
+    if (t.nt == 1) return launch<D, 1, 1>(a, s);
+    if (t.nt == 2) return launch<D, 2, 1>(a, s);
     if constexpr (D <= 128) {
-        if (nt == 3) return launch<D, 3>(a, s);
-        if (nt == 4) return launch<D, 4>(a, s);
+        if (t.nt == 3) return launch<D, 3, 1>(a, s);
+        if (t.nt == 4) return launch<D, 4, 1>(a, s);
     }
     return PN_EUNSUPPORTED;
 }
@@ -972,8 +1037,8 @@ extern "C" size_t pn_kv4_attn_workspace(const pn_kv4_cache *cache, int q_heads, 
     if (check_cache(cache, &c) || !sizes_ok(cache, q_heads, B, total_q, max_q, max_kv, sinks) || total_q == 0) return 0;
     if (max_q > total_q) max_q = total_q;
     if (!sizes_fit(cache, q_heads, B, total_q, max_q, max_kv)) return 0;
-    const Cut t = cut(cache, q_heads, B, max_q, max_kv, window, sinks);
-    return t.whole ? 0 : t.workers * t.part + t.cuts;
+    const Cut t = cut(cache, q_heads, max_q, max_kv, window, sinks);
+    return t.whole ? 0 : t.workers * t.part;
 }
 
 extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, int64_t ldq, int q_heads,
@@ -995,12 +1060,11 @@ extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, i
     if (max_q > total_q) max_q = total_q;  // no request has more
     if (!sizes_fit(cache, q_heads, B, total_q, max_q, max_kv)) return PN_EUNSUPPORTED;
     if (total_q == 0) return PN_OK;
-    Cut t = cut(cache, q_heads, B, max_q, max_kv, window, sinks);
-    if (t.tiles * 4 > INT32_MAX) return PN_EUNSUPPORTED;
-    if (!t.whole && ws_bytes < t.workers * t.part + t.cuts) {
+    Cut t = cut(cache, q_heads, max_q, max_kv, window, sinks);
+    if (!t.whole && ws_bytes < t.workers * t.part) {
         // As many workgroups as there is room for, while that leaves most of
         // the device at work; else every item is one workgroup's.
-        const int fit = ws_bytes > t.cuts ? (int)((ws_bytes - t.cuts) / t.part) : 0;
+        const int fit = (int)(ws_bytes / t.part);
         if (fit >= t.workers / 4) t.workers = fit;
         else t.whole = true;
     }
@@ -1010,8 +1074,9 @@ extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, i
     a.table = table;
     a.out = out;
     a.part = (float *)ws;
-    a.part_ml = (float2 *)(a.part + (size_t)t.workers * 2 * t.nt * cache->dim * 16);
-    a.cuts = (int2 *)((char *)ws + t.workers * t.part);
+    const size_t groups = 2 * (size_t)t.workers * t.nt * t.rg;
+    a.part_ml = (float2 *)(a.part + groups * cache->dim * 16);
+    a.cuts = (Cutoff *)(a.part_ml + groups * 16);
     a.ldq = ldq;
     a.ldo = ldo;
     a.ld_table = ld_table;
@@ -1026,14 +1091,14 @@ extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, i
     a.sinks = sinks;
     a.workers = t.workers;
     a.whole = t.whole;
-    a.tiles = (int)t.tiles;
     a.negate = scale < 0.0f;
     // Not 0: a masked score is -inf, whose product with c2 has to stay so.
     a.c2 = __builtin_fmaxf(__builtin_fabsf(scale) * 1.4426950408889634f, 0x1p-100f);
+    a.slack = 4.0f / a.c2;
     const hipStream_t s = (hipStream_t)stream;
-    const pn_status st = cache->dim == 64    ? launch_rows<64>(a, t.nt, s)
-                         : cache->dim == 128 ? launch_rows<128>(a, t.nt, s)
-                                             : launch_rows<256>(a, t.nt, s);
+    const pn_status st = cache->dim == 64    ? launch_rows<64>(a, t, s)
+                         : cache->dim == 128 ? launch_rows<128>(a, t, s)
+                                             : launch_rows<256>(a, t, s);
     if (st == PN_OK) g_last_variant = kVarKv4Attn;
     return st;
 }
