@@ -15,16 +15,19 @@
 //                 scale multiplies the fp32 sum.
 //   O^T += V^T P  A = 16 elements x 32 tokens, B = P^T.  A score's place after
 //                 the first product is already a lane's place of B: tokens
-//                 4 g .. 4 g + 3 of both 16-token tiles.  V's codes enter
-//                 exactly too; the scale of a token's block multiplies the
-//                 weight, and that product is the one rounding to fp16 (half a
-//                 step, 2^-11 relative).  The running maximum m follows only
-//                 scores that pass it by 4 (in log2), so that O is rarely
-//                 scaled; weights are <= 2^4.  Scales may have any fp16 size,
-//                 so each wave keeps a power of two 2^u, inside the exponent
-//                 of w, that puts the scales it has met below 2^7 first and
-//                 2^11 at most: with fp32 sums nothing overflows, and products
-//                 down to 2^-20 of the largest keep full precision.
+//                 4 g .. 4 g + 3 of both 16-token tiles.  Weights and values
+//                 (scale times code) are rounded once each to fp16, half a
+//                 step, 2^-11 relative: with the scale in the weights instead
+//                 the codes would be exact, but each block of the head then
+//                 needs weights of its own, and 64 rows of two blocks spend a
+//                 sixth more instructions on that than on 32 products.
+//                 Neither factor leaves fp16's full precision: the running
+//                 maximum m follows only scores that pass it by 4 (in log2),
+//                 so that O is rarely scaled, and weights carry 2^10: they
+//                 stay below 2^14, normal down to 2^-24 of the largest.
+//                 Scales may have any fp16 size, so each wave keeps a power of
+//                 two 2^u that puts the scales it has met below 2^7 at first
+//                 and 2^11 at most, values below 2^14.
 // A row of A is element 2 i + (r >> 3) of word r & 7 of a block (r = lane &
 // 15, product i < 4), so that one product stays in one block; two v_perm-ed
 // words give the token pairs.
@@ -63,6 +66,7 @@ constexpr int kThreads = 512;
 constexpr int kWaves = 8;
 constexpr int kStep = 32;          // tokens of a step
 constexpr float kLowest = -1e30f;  // a maximum before any score
+constexpr float kBias = 10.0f;     // weights carry 2^kBias
 constexpr int kShare = 16;         // steps of a workgroup at least
 constexpr int kOver = 32;          // what an item's start and end cost, in steps
 constexpr int kNothing = (int)0x80000000;  // an offset past every buffer: reads zero
@@ -395,10 +399,8 @@ template <int D, int NT> struct State {
     static constexpr int R = D / 64;
     float4_t o[NT][R][4];
     float m[NT];   // the score (before c2) that weights are relative to, kLowest if none
-    float lim[NT]; // score above which m has to follow
-    float mm[NT];  // m c2 - u
-    float l[NT];   // this lane's share of the sum of exp2(c2 s - mm)
-    int u;         // the power of two on the value scales
+    float l[NT];   // this lane's share of the sum of the weights exp2(c2 (s - m) + kBias)
+    float up;      // 2^u, the power of two on the value scales
     uint32_t cap;  // largest scale (fp16 bits) that 2^u leaves below 2^11
 };
 
@@ -409,11 +411,12 @@ struct Mask {
     int32_t token0;    // of the step
     int32_t end;       // keys of the request
     int32_t low, high; // positions of the wave's first and last query
+    int32_t row0, rows, first;  // the wave's first row, the request's rows, the position of query 0
 };
 
 template <int D, int NT>
 __device__ __forceinline__ void advance(State<D, NT> &st, const uint8_t *from, const half8_t *q, const AttnArgs &a,
-                                        const Mask &mask, const int32_t (&pos)[NT], int lane)
+                                        const Mask &mask, int lane)
 {
     using G = Ring<D>;
     constexpr int R = G::R;
@@ -470,11 +473,13 @@ __device__ __forceinline__ void advance(State<D, NT> &st, const uint8_t *from, c
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int32_t below = a.window > 0 ? pos[n] - a.window : -1;  // >= INT32_MIN: pos >= -1
+            const int at = mask.row0 + 16 * n + r;
+            const int32_t pos = at < mask.rows ? mask.first + at / a.group : -1;
+            const int32_t below = a.window > 0 && pos >= 0 ? pos - a.window : -1;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int key = mask.token0 + 16 * (j >> 2) + 4 * g + (j & 3);
-                const bool ok = mask.page[j >> 2] && key < mask.end && key <= pos[n] && (key > below || key < a.sinks);
+                const bool ok = mask.page[j >> 2] && key < mask.end && key <= pos && (key > below || key < a.sinks);
                 sc[n][j >> 2][j & 3] = ok ? sc[n][j >> 2][j & 3] : -__builtin_inff();
             }
         }
@@ -509,57 +514,50 @@ __device__ __forceinline__ void advance(State<D, NT> &st, const uint8_t *from, c
             big = y > big ? y : big;
         }
         const int e = (int)(big >> 10) < 30 ? (int)(big >> 10) : 30;  // scales < 2^(e - 14)
-        const int u = 21 - e;
-        const float f = __builtin_ldexpf(1.0f, u - st.u);  // the first time l and O are 0
+        const float up = __builtin_ldexpf(1.0f, 21 - e), f = up / st.up;  // the first time O is 0
+        st.up = up;
         st.cap = e + 5 > 30 ? 0xffffu : (uint32_t)((e + 5) << 10) - 1;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            st.mm[n] -= (float)(u - st.u);
-            st.l[n] *= f;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int b = 0; b < R; ++b)
 #pragma unroll
                 for (int i2 = 0; i2 < 4; ++i2) st.o[n][b][i2] *= f;
-        }
-        st.u = u;
     }
 
     keep_order();
     // weights
-    half8_t p[NT][R];
+    half8_t p[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         float mx = max3(sc[n][0][0], sc[n][0][1], sc[n][0][2]);
         mx = max3(mx, sc[n][0][3], sc[n][1][0]);
         mx = max3(mx, sc[n][1][1], sc[n][1][2]);
         mx = group_max(max2(mx, sc[n][1][3]));
-        if (__ballot(mx > st.lim[n])) {
+        if (__ballot(mx > st.m[n] + a.slack)) {
             const float f = mx > st.m[n] ? __builtin_amdgcn_exp2f((st.m[n] - mx) * a.c2) : 1.0f;
             st.m[n] = max2(st.m[n], mx);
-            st.lim[n] = st.m[n] > kLowest ? st.m[n] + a.slack : kLowest;
-            st.mm[n] = st.m[n] * a.c2 - (float)st.u;
             st.l[n] *= f;
 #pragma unroll
             for (int b = 0; b < R; ++b)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) st.o[n][b][i] *= f;
         }
+        const float mm = kBias - st.m[n] * a.c2;
         float w[8], sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][j >> 2][j & 3], a.c2, -st.mm[n]));
+            w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][j >> 2][j & 3], a.c2, mm));
             sum += w[j];
+            p[n][j] = (_Float16)w[j];
         }
         st.l[n] += sum;
-#pragma unroll
-        for (int b = 0; b < R; ++b)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) p[n][b][j] = (_Float16)__builtin_fmaf(w[j], half_at(d[j >> 2], R * (j & 3) + b), 0.0f);
     }
 
     keep_order();
     // values
     const uint32_t sel = r < 8 ? 0x05040100u : 0x07060302u;  // even (low) or odd (high) elements of a token pair
+    const half2_t up2 = {(_Float16)st.up, (_Float16)st.up};
 #pragma unroll
     for (int b = 0; b < R; ++b) {
         uint32_t v[2][4];
@@ -569,16 +567,24 @@ __device__ __forceinline__ void advance(State<D, NT> &st, const uint8_t *from, c
         half8_t va[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
+            // the scales of the token pair for this block
+            const int i2 = u >> 1, t = 2 * (u & 1), word = R * t / 2 + b / 2, next = R / 2;
+            const half2_t sc2 = up2 * as_half2(R == 1 ? d[i2][u & 1]
+                                                      : __builtin_amdgcn_perm(d[i2][word + next], d[i2][word],
+                                                                              b & 1 ? 0x07060302u : 0x05040100u));
             half2_t e[4];
-            Unpack<1>::run(__builtin_amdgcn_perm(v[u >> 1][2 * (u & 1) + 1], v[u >> 1][2 * (u & 1)], sel), e);
+            Unpack<1>::run(__builtin_amdgcn_perm(v[i2][t + 1], v[i2][t], sel), e);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) va[i][2 * u] = e[i][0], va[i][2 * u + 1] = e[i][1];
+            for (int i = 0; i < 4; ++i) {
+                e[i] *= sc2;
+                va[i][2 * u] = e[i][0], va[i][2 * u + 1] = e[i][1];
+            }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                st.o[n][b][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(va[i], p[n][b], st.o[n][b][i], 0, 0, 0);
+                st.o[n][b][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(va[i], p[n], st.o[n][b][i], 0, 0, 0);
         keep_order();
     }
 }
@@ -743,20 +749,16 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
             queries[y] = a.negate ? -v : v;
         }
         State<D, NT> st;
-        int32_t pos[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int at = row0 + 16 * n + r;
-            pos[n] = at < rows ? w.first + at / a.group : -1;
 #pragma unroll
             for (int y = 0; y < R; ++y)
 #pragma unroll
                 for (int i2 = 0; i2 < 4; ++i2) st.o[n][y][i2] = (float4_t){0, 0, 0, 0};
-            st.m[n] = st.lim[n] = kLowest;
-            st.mm[n] = 0.0f;
+            st.m[n] = kLowest;
             st.l[n] = 0.0f;
         }
-        st.u = 0;
+        st.up = 1.0f;
         st.cap = 0;
 
         // The same part of the steps that this tile has.
@@ -805,12 +807,15 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
             mask.end = w.len;
             mask.low = p0;
             mask.high = p1;
+            mask.row0 = row0;
+            mask.rows = rows;
+            mask.first = w.first;
             mask.some = !(mask.page[0] && mask.page[1] && token0 + kStep <= w.len && token0 + kStep - 1 <= p0 &&
                           (a.window <= 0 || (int64_t)token0 + a.window > p1 || token0 + kStep <= a.sinks));
             // A row group sees less than its workgroup's tile.
             const bool none = RG > 1 && (e >= e1 || token0 > p1 ||
                                          (a.window > 0 && (int64_t)token0 + kStep - 1 + a.window <= p0 && token0 >= a.sinks));
-            if (!none) advance<D, NT>(st, from, q, a, mask, pos, lane);
+            if (!none) advance<D, NT>(st, from, q, a, mask, lane);
             __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the stage has been read
             asm volatile("" ::: "memory");
             if constexpr (RG == 1)
@@ -826,10 +831,11 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
         // the fragments.
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float l = __builtin_ldexpf(group_sum(st.l[n]), -st.u);
+            const float l = group_sum(st.l[n]);
             if (g == 0) ml[wave][16 * n + r][0] = st.m[n], ml[wave][16 * n + r][1] = l;
         }
         float4_t *frag = (float4_t *)lds;  // [wave][4 b + i][lane]
+        const float down = 1.0f / st.up;
         // A share goes on with at most one item, its first (part 0), and
         // leaves at most one unfinished, its last (part 1).
         const int part_at = 2 * (int)blockIdx.x + (s0 == 0 ? 1 : 0);
@@ -841,7 +847,7 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
             for (int y = 0; y < KW; ++y) m = max2(m, ml[rg * KW + y][16 * n + r][0]);
             for (int y = 0; y < KW; ++y)
                 all_l += ml[rg * KW + y][16 * n + r][1] * __builtin_amdgcn_exp2f((ml[rg * KW + y][16 * n + r][0] - m) * a.c2);
-            float f = __builtin_ldexpf(__builtin_amdgcn_exp2f((st.m[n] - m) * a.c2), -st.u);
+            float f = __builtin_amdgcn_exp2f((st.m[n] - m) * a.c2) * down;
             if (!cut) f = all_l > 0.0f ? f / all_l : 0.0f;
             const int row_at = row0 + 16 * n + r, i = row_at / a.group;
             const bool live = row_at < rows;

@@ -433,8 +433,8 @@ pn_status pn_kv4_load(const pn_kv4_cache *cache, const int64_t *slots, int64_t T
  * t < sinks.  A token whose table entry is not a page of the cache is not
  * visible; a query that sees nothing gives zeros.  Masked places may hold any
  * bytes.
- * Scores and sums are fp32; codes enter the products exactly; a weight times
- * the value's scale is rounded once to fp16.
+ * Scores (from exact codes) and sums are fp32; weights and values are rounded
+ * once each to fp16.
  *   q, out   : fp16, total_q rows, 16-byte aligned, ld >= q_heads * dim and a
  *              multiple of 8; must not overlap
  *   table    : int32, B rows of ld_table >= ceil(max_kv / page_size)

@@ -115,8 +115,8 @@ def store(x, heads_of, gains, eps, inv_freq, rot, pairs, positions, dim):
 
 def attend(q, pages, page, heads, dim, q_start, kv_len, table, scale, window, sinks, num_pages):
     """q [T, q_heads, dim] -> (out, bound): fp64 outputs, and for each what an
-    fp32 pass with one fp16 rounding of a weight times its value's scale, and
-    one of the output, may be off by."""
+    fp32 pass with one fp16 rounding of each weight, of each value and of the
+    output may be off by."""
     T, q_heads, _ = q.shape
     group = q_heads // heads
     out, bound = np.zeros(q.shape), np.zeros(q.shape)
@@ -145,7 +145,7 @@ def attend(q, pages, page, heads, dim, q_start, kv_len, table, scale, window, si
                 a = w @ np.abs(vv) / w.sum()
                 # scores: dim products and a few scalings in fp32; exp2 of a difference of two scores
                 eta = 2 * ((dim + 8) * 2.0 ** -24 * mag.max() + 8 * 2.0 ** -24)
-                e = a * (2.0 ** -11 + 2 * eta + (see.sum() + 64) * 2.0 ** -24)
+                e = a * (2 * 2.0 ** -11 + 2 * eta + (see.sum() + 64) * 2.0 ** -24)
                 e += see.sum() * np.abs(vv).max() * 2.0 ** -34  # weights below fp16's normal range
                 bound[i, h] = e + 2.0 ** -11 * (np.abs(out[i, h]) + e) + 2.0 ** -25
     return out, bound
