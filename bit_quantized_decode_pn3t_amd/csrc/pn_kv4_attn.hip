@@ -68,7 +68,6 @@ constexpr int kStep = 32;          // tokens of a step
 constexpr float kLowest = -1e30f;  // a maximum before any score
 constexpr float kBias = 10.0f;     // weights carry 2^kBias
 constexpr int kShare = 16;         // steps of a workgroup at least
-constexpr int kOver = 32;          // what an item's start and end cost, in steps
 constexpr int kNothing = (int)0x80000000;  // an offset past every buffer: reads zero
 
 struct AttnArgs {
@@ -83,6 +82,7 @@ struct AttnArgs {
     int64_t max_q, max_kv;
     int32_t q_heads, group, B, max_pages, window, sinks;
     int32_t workers, whole;  // workgroups; whole: items are not cut
+    int32_t over;            // what an item's start and end cost, in steps
     int32_t negate;          // scale < 0: the queries are negated
     float c2;                // |scale| log2(e), above 0
     float slack;             // 4 / c2
@@ -120,19 +120,20 @@ __device__ __forceinline__ Work request(const AttnArgs &a, int b)
     return w;
 }
 
-// The steps that queries i0 .. i1 of the request can see.
+// The steps of STEP tokens that queries i0 .. i1 of the request can see.
+template <int STEP>
 __device__ __forceinline__ void span(const AttnArgs &a, Work &w, int i0, int i1)
 {
     int32_t hi = w.first + i1 + 1;
     hi = hi < 0 ? 0 : hi < w.len ? hi : w.len;
-    const int32_t end = (hi + kStep - 1) / kStep;
+    const int32_t end = (hi + STEP - 1) / STEP;
     w.sink_steps = 0;
     w.lo = 0;
     if (a.window > 0) {
         const int64_t from = (int64_t)w.first + i0 - a.window + 1;
-        const int32_t lo = from < 0 ? 0 : from < hi ? (int32_t)(from / kStep) : end;
+        const int32_t lo = from < 0 ? 0 : from < hi ? (int32_t)(from / STEP) : end;
         const int32_t s = a.sinks < hi ? a.sinks : hi;
-        const int32_t ss = (s + kStep - 1) / kStep;
+        const int32_t ss = (s + STEP - 1) / STEP;
         w.sink_steps = ss < lo ? ss : 0;  // sinks that meet the window are one stretch
         w.lo = ss < lo ? lo : 0;
     }
@@ -147,6 +148,7 @@ struct Cost {
     int32_t steps, tiles;
 };
 
+template <int STEP>
 __device__ __forceinline__ Cost cost(const AttnArgs &a, int b, int tile_rows)
 {
     Cost c;
@@ -154,7 +156,7 @@ __device__ __forceinline__ Cost cost(const AttnArgs &a, int b, int tile_rows)
     c.steps = c.tiles = 0;
     if (c.w.qn < 1) return c;
     Work all = c.w;
-    span(a, all, 0, c.w.qn - 1);
+    span<STEP>(a, all, 0, c.w.qn - 1);
     c.steps = all.steps < 1 ? 1 : all.steps;
     c.tiles = (c.w.qn * a.group + tile_rows - 1) / tile_rows;
     return c;
@@ -162,14 +164,18 @@ __device__ __forceinline__ Cost cost(const AttnArgs &a, int b, int tile_rows)
 
 __device__ __forceinline__ int64_t length(const AttnArgs &a, const Cost &c)
 {
-    return (int64_t)(c.steps + kOver) * c.tiles * a.c.heads;
+    return (int64_t)(c.steps + a.over) * c.tiles * a.c.heads;
 }
 
 // The same in every lane: into scalar registers.
+__device__ __forceinline__ int64_t uniform64(int64_t v)
+{
+    return (int64_t)(((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32) | (uint32_t)uniform((int)v));
+}
 __device__ __forceinline__ Cost scalar(const Cost &m)
 {
     Cost c;
-    c.w.q0 = (int64_t)(((uint64_t)(uint32_t)uniform((int)(m.w.q0 >> 32)) << 32) | (uint32_t)uniform((int)m.w.q0));
+    c.w.q0 = uniform64(m.w.q0);
     c.w.qn = uniform(m.w.qn);
     c.w.first = uniform(m.w.first);
     c.w.len = uniform(m.w.len);
@@ -177,6 +183,128 @@ __device__ __forceinline__ Cost scalar(const Cost &m)
     c.tiles = uniform(m.tiles);
     c.w.sink_steps = c.w.lo = c.w.steps = 0;  // the row tile's, to be filled in
     return c;
+}
+
+// ---------------------------------------------------------------------------
+// A workgroup's part of the line.
+// ---------------------------------------------------------------------------
+struct LineLds {
+    int64_t scan[kWaves];
+    int64_t at[2];
+    Cost known[64];
+};
+
+struct Line {
+    int64_t lo, hi, share;
+    int64_t start;  // of request b on the line
+    int32_t b;
+    bool few;
+};
+
+// Up to 64 requests are summed by every wave for itself and kept in LDS; more
+// are summed by the workgroup and read again as they come.  False: nothing is
+// left for this workgroup.
+template <int STEP>
+__device__ __forceinline__ bool line_part(const AttnArgs &a, LineLds &s, Line &t, int tile_rows)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    t.few = a.B <= 64;
+    const int per = (a.B + kThreads - 1) / kThreads;
+    int64_t mine = 0, total = 0, before = 0;
+    if (t.few) {
+        const Cost c = cost<STEP>(a, lane < a.B ? lane : 0, tile_rows);
+        mine = lane < a.B ? length(a, c) : 0;
+        if (wave == 0) s.known[lane] = c;
+    } else {
+        for (int b = tid * per; b < (tid + 1) * per && b < a.B; ++b) mine += length(a, cost<STEP>(a, b, tile_rows));
+    }
+    int64_t sum = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t x = __shfl_up(sum, d, 64);
+        if (lane >= d) sum += x;
+    }
+    before = sum - mine;
+    if (t.few) {
+        total = __shfl(sum, 63, 64);
+    } else {
+        if (lane == 63) s.scan[wave] = sum;
+        __syncthreads();
+        for (int w = 0; w < kWaves; ++w) {
+            if (w < wave) before += s.scan[w];
+            total += s.scan[w];
+        }
+    }
+    total = uniform64(total);
+    t.share = (total + a.workers - 1) / a.workers;
+    if (t.share < kShare && !a.whole) t.share = kShare;
+    t.lo = blockIdx.x * t.share;
+    t.hi = t.lo + t.share < total ? t.lo + t.share : total;
+    if (tid == 0 && !a.whole) a.cuts[blockIdx.x].parts = 0;
+    if (t.lo >= total) return false;  // the whole workgroup
+    const bool here = t.lo >= before && t.lo < before + mine;  // one lane of each wave, or one thread
+    if (t.few) {
+        __syncthreads();
+        t.b = __builtin_ctzll(__ballot(here));
+        t.start = uniform64(__shfl(before, t.b, 64));
+    } else {
+        if (here) {
+            int x = tid * per;
+            for (;; ++x) {
+                const int64_t n = length(a, cost<STEP>(a, x, tile_rows));
+                if (t.lo < before + n) break;
+                before += n;
+            }
+            s.at[0] = x;
+            s.at[1] = before;
+        }
+        __syncthreads();
+        t.b = uniform((int)s.at[0]);
+        t.start = uniform64(s.at[1]);
+    }
+    return true;
+}
+
+// The next item of the part.
+struct Item {
+    Cost c;
+    int32_t s0, s1;  // steps of those the line counts
+    int32_t head, tile0, rows;  // the tile's first row, the request's rows
+    bool cut;
+};
+
+// Step x on along the line; false: a stretch without an item's steps.
+template <int STEP>
+__device__ __forceinline__ bool next_item(const AttnArgs &a, const LineLds &s, Line &t, int64_t &x, Item &m, int tile_rows)
+{
+    m.c = scalar(t.few ? s.known[t.b] : cost<STEP>(a, t.b, tile_rows));
+    const int64_t all = length(a, m.c);
+    if (x >= t.start + all) {
+        t.start += all;
+        ++t.b;
+        return false;
+    }
+    const int one = m.c.steps + a.over;  // an item's length on the line
+    const int item = uniform((int)((x - t.start) / one));
+    const int64_t first = t.start + (int64_t)item * one;  // of the item on the line
+    int s0 = (int)(x - first), s1 = (int)(t.hi - first < one ? t.hi - first : one);
+    x = first + s1;
+    if (a.whole) {  // items are taken whole, by the workgroup they start in
+        if (s0 > 0) return false;
+        s1 = one;
+    }
+    s0 = s0 > a.over ? s0 - a.over : 0;
+    s1 -= a.over;
+    if (s1 <= s0) return false;
+    m.s0 = uniform(s0), m.s1 = uniform(s1);
+    m.cut = s0 > 0 || s1 < m.c.steps;
+    m.head = item / m.c.tiles;
+    const int turn = item - m.head * m.c.tiles;
+    m.tile0 = (turn & 1 ? m.c.tiles - 1 - (turn >> 1) : turn >> 1) * tile_rows;
+    m.rows = m.c.w.qn * a.group;
+    if (m.s0 == 0 && m.cut && threadIdx.x == 0)
+        a.cuts[blockIdx.x] = {m.c.w.q0, m.tile0, m.rows, m.head, (int)((first + one - 1) / t.share) - (int)blockIdx.x + 1};
+    return true;
 }
 
 // ---------------------------------------------------------------------------
@@ -634,9 +762,7 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
     constexpr int R = G::R, kRows = S::kRows, KW = S::KW;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // the ring, then the queries
     __shared__ float ml[kWaves][16 * NT][2];
-    __shared__ int64_t scan[kWaves];
-    __shared__ int64_t at_shared[2];
-    __shared__ Cost known[64];
+    __shared__ LineLds line_lds;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int rg = wave / KW, kg = wave % KW;
@@ -644,97 +770,20 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
     // operands as the products take them: [16-row group][32 elements][lane]
     half8_t *queries = (half8_t *)(lds + S::kRing), *q = queries + rg * NT * 2 * R * 64;
 
-    // This workgroup's part of the line.  Up to 64 requests are summed by
-    // every wave for itself and kept in LDS; more are summed by the workgroup
-    // and read again as they come.
-    const bool few = a.B <= 64;
-    int64_t mine = 0, total = 0, before = 0;
-    if (few) {
-        const Cost c = cost(a, lane < a.B ? lane : 0, kRows);
-        mine = lane < a.B ? length(a, c) : 0;
-        if (wave == 0) known[lane] = c;
-    } else {
-        const int per = (a.B + kThreads - 1) / kThreads;
-        for (int b = tid * per; b < (tid + 1) * per && b < a.B; ++b) mine += length(a, cost(a, b, kRows));
-    }
-    int64_t sum = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int64_t x = __shfl_up(sum, d, 64);
-        if (lane >= d) sum += x;
-    }
-    if (few) {
-        total = __shfl(sum, 63, 64);
-        before = sum - mine;
-    } else {
-        if (lane == 63) scan[wave] = sum;
-        __syncthreads();
-        before = sum - mine;
-        for (int w = 0; w < kWaves; ++w) {
-            if (w < wave) before += scan[w];
-            total += scan[w];
-        }
-    }
-    int64_t share = (total + a.workers - 1) / a.workers;
-    if (share < kShare && !a.whole) share = kShare;
-    const int64_t lo = blockIdx.x * share, hi = lo + share < total ? lo + share : total;
-    if (tid == 0 && !a.whole) a.cuts[blockIdx.x].parts = 0;
-    if (lo >= total) return;  // the whole workgroup
-    if (few) __syncthreads();
-    const bool here = lo >= before && lo < before + mine;  // one lane of each wave, or one thread
-    int b;
-    int64_t start;  // of request b on the line
-    if (few) {
-        b = __builtin_ctzll(__ballot(here));
-        start = __shfl(before, b, 64);
-    } else {
-        if (here) {
-            int x = tid * ((a.B + kThreads - 1) / kThreads);
-            for (;; ++x) {
-                const int64_t n = length(a, cost(a, x, kRows));
-                if (lo < before + n) break;
-                before += n;
-            }
-            at_shared[0] = x;
-            at_shared[1] = before;
-        }
-        __syncthreads();
-        b = uniform((int)at_shared[0]);
-        start = at_shared[1];
-    }
+    Line line;
+    if (!line_part<kStep>(a, line_lds, line, kRows)) return;
     Offsets<D> off;
     off.set(lane, 1 << a.c.shift);
 
-    for (int64_t x = lo; x < hi;) {
-        const Cost c = scalar(few ? known[b] : cost(a, b, kRows));
-        const int64_t all = length(a, c);
-        if (x >= start + all) {
-            start += all;
-            ++b;
-            continue;
-        }
-        const int one = c.steps + kOver;  // an item's length on the line
-        const int item = uniform((int)((x - start) / one));
-        const int64_t first = start + (int64_t)item * one;  // of the item on the line
-        int s0 = (int)(x - first), s1 = (int)(hi - first < one ? hi - first : one);
-        x = first + s1;
-        if (a.whole) {  // items are taken whole, by the workgroup they start in
-            if (s0 > 0) continue;
-            s1 = one;
-        }
-        s0 = s0 > kOver ? s0 - kOver : 0;
-        s1 -= kOver;
-        if (s1 <= s0) continue;
-        s0 = uniform(s0), s1 = uniform(s1);
-        const bool cut = s0 > 0 || s1 < c.steps;
-        const int head = item / c.tiles, turn = item - head * c.tiles;
-        const int tile = turn & 1 ? c.tiles - 1 - (turn >> 1) : turn >> 1;
-        const int tile0 = tile * kRows, rows = c.w.qn * a.group;  // the workgroup's first row, the request's rows
-        if (s0 == 0 && cut && tid == 0)
-            a.cuts[blockIdx.x] = {c.w.q0, tile0, rows, head, (int)((first + one - 1) / share) - (int)blockIdx.x + 1};
+    for (int64_t x = line.lo; x < line.hi;) {
+        Item item;
+        if (!next_item<kStep>(a, line_lds, line, x, item, kRows)) continue;
+        const Cost &c = item.c;
+        const int s0 = item.s0, s1 = item.s1, head = item.head, tile0 = item.tile0, rows = item.rows, b = line.b;
+        const bool cut = item.cut;
 
         Work w = c.w;
-        span(a, w, tile0 / a.group, ((tile0 + kRows < rows ? tile0 + kRows : rows) - 1) / a.group);
+        span<kStep>(a, w, tile0 / a.group, ((tile0 + kRows < rows ? tile0 + kRows : rows) - 1) / a.group);
         // the wave's own rows (none: nothing is visible)
         const int row0 = tile0 + rg * 16 * NT;
         const int last = (row0 + 16 * NT < rows ? row0 + 16 * NT : rows) - 1;
@@ -894,15 +943,419 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
     }
 }
 
-// Add the parts of an item that a workgroup left unfinished.  Grid: x =
-// workgroup, y = block, z = 16-row group; 16 waves: product i = wave & 3, a
-// fourth of the parts each.
-template <int D>
-__global__ __launch_bounds__(1024) void kv4_join(AttnArgs a, int groups)
+// ---------------------------------------------------------------------------
+// Prompts: eight waves with 16 NT rows each share every step's keys and
+// values, which they unpack together.  Half of the waves turn a step's key
+// words into A operands of the first product, half its value words, scaled,
+// into those of the second, both as fp16 fragments in LDS that all waves then
+// read; the words come straight into registers two steps ahead.  64 tokens a
+// step, one barrier: while it is worked on, the next one is unpacked.
+// Unpacking costs a wave an eighth of what it would alone; what is left bounds
+// the kernel: exp2 and the arithmetic around it, about as long as the products
+// they go with.
+// ---------------------------------------------------------------------------
+constexpr int kWide = 64;  // tokens of a prompt's step
+
+template <int D, int NT> struct Prompt {
+    static constexpr int R = D / 64;
+    static constexpr int kRows = kWaves * 16 * NT;
+    static constexpr int kFrags = kWide / 16 * 2 * R;       // of K: [tile][block][h]; of V: [32 tokens][block][product], as many
+    static constexpr int kBuf = 2 * kFrags * 1024;          // one step's K and V
+    static constexpr int kScale = kWide * R * 2;            // K's scales of a step: [token][block] fp16
+    static constexpr int kLds = 2 * kBuf + 3 * kScale;
+    static constexpr int kPart = kWaves * NT * 4 * R * 256; // floats of a part
+    static constexpr int kPairs = kWide * (D / 16) / 256;   // key word pairs of a thread
+};
+
+// What a thread has of a step to come: key word pairs and its token's scales,
+// or four tokens' value words and scales.
+template <int D> struct Raw {
+    uint2 k[Prompt<D, 1>::kPairs];
+    uint32_t ks;
+    uint4 v;
+    uint32_t vs[2 * (D / 64)];
+};
+
+template <int D, int NT>
+__global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
 {
-    constexpr int R = D / 64;
-    __shared__ float4_t frag[16][64];
-    __shared__ float2 ml[64][16];
+    using P = Prompt<D, NT>;
+    using L = Kv4Layout<D>;
+    constexpr int R = P::R, kRows = P::kRows;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // two steps' fragments, three steps' key scales
+    __shared__ LineLds line_lds;
+    // A step's largest value scale past the cap, read one step ahead of it;
+    // whether it misses a page, read with it.  Cleared in the step after.
+    __shared__ uint32_t most[3], bad[4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const bool keys = wave >= 4;       // unpacks keys; else values
+    const int half_tid = tid & 255;
+    const int T = 1 << a.c.shift;      // tokens of a page
+    // A key thread: pairs (row, 2 words); a value thread: four tokens of one word.
+    constexpr int kPer = D / 16;       // pairs of a row
+    const int k_row = half_tid / kPer, k_pair = half_tid % kPer;
+    const int v_t4 = half_tid / (D / 8), v_word = half_tid % (D / 8);
+    const bool v_on = !keys && v_t4 < kWide / 4;
+
+    Line line;
+    if (!line_part<kWide>(a, line_lds, line, kRows)) return;
+    for (int64_t x = line.lo; x < line.hi;) {
+        Item item;
+        if (!next_item<kWide>(a, line_lds, line, x, item, kRows)) continue;
+        const int head = item.head, tile0 = item.tile0, rows = item.rows, b = line.b;
+        Work w = item.c.w;
+        const int tile_last = (tile0 + kRows < rows ? tile0 + kRows : rows) - 1;
+        span<kWide>(a, w, tile0 / a.group, tile_last / a.group);
+        const int32_t t_low = w.first + tile0 / a.group, t_high = w.first + tile_last / a.group;  // the tile's positions
+        const int row0 = tile0 + wave * 16 * NT;
+        const int last = (row0 + 16 * NT < rows ? row0 + 16 * NT : rows) - 1;
+        const int32_t p0 = row0 < rows ? w.first + row0 / a.group : -1, p1 = row0 < rows ? w.first + last / a.group : -1;
+
+        half8_t q[NT][2 * R];
+        float4_t o[NT][R][4];
+        float m[NT], l[NT];
+        int32_t pos[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int at = row0 + 16 * n + r, i = at / a.group;
+            const bool live = at < rows;
+            pos[n] = live ? w.first + i : -1;
+            const uint16_t *from = a.q + (w.q0 + (live ? i : 0)) * a.ldq + (head * a.group + (live ? at - i * a.group : 0)) * D;
+#pragma unroll
+            for (int y = 0; y < 2 * R; ++y) {
+                q[n][y] = *(const half8_t *)(from + 32 * y + 8 * g);
+                if (!live) q[n][y] = (half8_t)(_Float16)0.0f;
+                if (a.negate) q[n][y] = -q[n][y];
+            }
+#pragma unroll
+            for (int y = 0; y < R; ++y)
+#pragma unroll
+                for (int i2 = 0; i2 < 4; ++i2) o[n][y][i2] = (float4_t){0, 0, 0, 0};
+            m[n] = kLowest;
+            l[n] = 0.0f;
+        }
+        float up = 1.0f;   // 2^u on the values being added
+        uint32_t cap = 0;  // largest scale (fp16 bits) that the next step's u leaves below 2^11
+
+        const int e0 = uniform((int)((int64_t)item.s0 * w.steps / item.c.steps));
+        const int count = uniform((int)((int64_t)item.s1 * w.steps / item.c.steps)) - e0;
+        auto token_of = [&](int i) {
+            const int e = e0 + i;
+            return (e < w.sink_steps ? e : e - w.sink_steps + w.lo) * kWide;
+        };
+        const int32_t *row = a.table + (int64_t)b * a.ld_table;
+        // Page of token t, -1 if it is none of the cache.
+        auto page_at = [&](int t) {
+            const int at = t >> a.c.shift;
+            return at < a.max_pages ? row[at] : -1;
+        };
+        struct Ids {
+            int32_t p[P::kPairs];
+        };
+        // The pages of the thread's tokens in step i.
+        auto ids_of = [&](int i) {
+            Ids d;
+#pragma unroll
+            for (int y = 0; y < P::kPairs; ++y) d.p[y] = -1;
+            if (i < count) {
+                const int t0 = token_of(i);
+                if (keys) {
+#pragma unroll
+                    for (int y = 0; y < P::kPairs; ++y) d.p[y] = page_at(t0 + k_row + 256 / kPer * y);
+                } else if (v_on) {
+                    d.p[0] = page_at(t0 + 4 * v_t4);
+                }
+            }
+            return d;
+        };
+        auto base_of = [&](int32_t page) { return a.c.pages + ((int64_t)page * a.c.heads + head) * a.c.chunk; };
+        auto ok_page = [&](int32_t page) { return (uint32_t)page < (uint32_t)a.c.num_pages; };
+        // Start the loads of step i.
+        auto fetch = [&](Raw<D> &raw, const Ids &d, int i) {
+            if (i >= count) return;
+            const int t0 = token_of(i);
+            if (keys) {
+#pragma unroll
+                for (int y = 0; y < P::kPairs; ++y) {
+                    const int o = (t0 + k_row + 256 / kPer * y) & (T - 1);
+                    raw.k[y] = make_uint2(0x88888888u, 0x88888888u);
+                    if (ok_page(d.p[y])) raw.k[y] = *(const uint2 *)(base_of(d.p[y]) + o * L::kRow + 8 * k_pair);
+                }
+                // the scales of one row a thread: pair y of it (pairs 0 .. kPairs - 1 fetch rows k_row + ... y)
+                raw.ks = 0;
+#pragma unroll
+                for (int y = 0; y < P::kPairs; ++y) {
+                    if (k_pair != y) continue;
+                    const int o = (t0 + k_row + 256 / kPer * y) & (T - 1);
+                    if (ok_page(d.p[y])) {
+                        const uint8_t *s = base_of(d.p[y]) + L::k_scales(T) + 2 * R * o;
+                        raw.ks = R == 1 ? *(const uint16_t *)s : *(const uint32_t *)s;
+                    }
+                }
+            } else if (v_on) {
+                const int o = (t0 + 4 * v_t4) & (T - 1);
+                raw.v = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int y = 0; y < 2 * R; ++y) raw.vs[y] = 0;
+                if (ok_page(d.p[0])) {
+                    const uint8_t *from = base_of(d.p[0]);
+                    raw.v = *(const uint4 *)(from + L::v_codes(T) + ((o >> 2) * (D / 8) + v_word) * 16);
+                    const uint8_t *s = from + L::v_scales(T) + 2 * R * o;
+                    if constexpr (R == 1) {
+                        const uint2 y = *(const uint2 *)s;
+                        raw.vs[0] = y.x, raw.vs[1] = y.y;
+                    } else {
+                        const uint4 y = *(const uint4 *)s;
+                        raw.vs[0] = y.x, raw.vs[1] = y.y, raw.vs[2] = y.z, raw.vs[3] = y.w;
+                    }
+                }
+            }
+        };
+        // The step's words have come: value scales that no row sees become 0
+        // (they may be anything), the others are held against the cap; key
+        // scales go to LDS, NaN for a token without a page.
+        auto look = [&](Raw<D> &raw, const Ids &d, int i) {
+            if (i >= count) return;
+            const int t0 = token_of(i);
+            if (keys) {
+#pragma unroll
+                for (int y = 0; y < P::kPairs; ++y) {
+                    if (k_pair != y) continue;
+                    const int t = k_row + 256 / kPer * y;
+                    const bool gone = !ok_page(d.p[y]);
+                    uint8_t *to = lds + 2 * P::kBuf + i % 3 * P::kScale + 2 * R * t;
+                    if (R == 1) *(uint16_t *)to = gone ? 0x7e00 : (uint16_t)raw.ks;
+                    else *(uint32_t *)to = gone ? 0x7e007e00u : raw.ks;
+                    if (gone) bad[i % 4] = 1;
+                }
+            } else if (v_on) {
+                const int32_t under = a.window > 0 ? t_low - a.window : -1;
+                uint32_t any = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int t = t0 + 4 * v_t4 + j;
+                    const bool seen = t < w.len && t <= t_high && (t > under || t < a.sinks);
+#pragma unroll
+                    for (int z = 0; z < R; ++z) {
+                        const int h = R * j + z;
+                        if (!seen) raw.vs[h >> 1] &= h & 1 ? 0x0000ffffu : 0xffff0000u;
+                    }
+                }
+#pragma unroll
+                for (int y = 0; y < 2 * R; ++y) {
+                    const uint32_t s = raw.vs[y] & 0x7fff7fffu;
+                    any = (s >> 16) > any ? s >> 16 : any;
+                    any = (s & 0xffffu) > any ? s & 0xffffu : any;
+                }
+                if (any > cap) atomicMax(&most[i % 3], any);
+            }
+        };
+        // Words into fragments.
+        auto unpack = [&](const Raw<D> &raw, int i, float factor) {
+            if (i >= count) return;
+            half8_t *buf = (half8_t *)(lds + (i & 1) * P::kBuf);
+            if (keys) {
+#pragma unroll
+                for (int y = 0; y < P::kPairs; ++y) {
+                    const int t = k_row + 256 / kPer * y, kg = k_pair / R, kb = k_pair % R;
+                    half8_t *to = buf + ((t >> 4) * 2 * R + 2 * kb) * 64 + 16 * kg + (t & 15);
+                    to[0] = codes8(raw.k[y].x);
+                    to[64] = codes8(raw.k[y].y);
+                }
+            } else if (v_on) {
+                const int vb = v_word >> 3, group = v_t4 >> 3, second = v_t4 >> 2 & 1, vg = v_t4 & 3;
+                const half2_t f2 = {(_Float16)factor, (_Float16)factor};
+                const uint32_t words[4] = {raw.v.x, raw.v.y, raw.v.z, raw.v.w};
+                half2_t e[2][2][4];  // [token pair][odd element][product]
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    half2_t sc;
+                    if constexpr (R == 1) sc = as_half2(raw.vs[u]);
+                    else sc = as_half2(__builtin_amdgcn_perm(raw.vs[2 * u + 1], raw.vs[2 * u], vb ? 0x07060302u : 0x05040100u));
+                    sc *= f2;
+#pragma unroll
+                    for (int odd = 0; odd < 2; ++odd) {
+                        Unpack<1>::run(__builtin_amdgcn_perm(words[2 * u + 1], words[2 * u], odd ? 0x07060302u : 0x05040100u), e[u][odd]);
+#pragma unroll
+                        for (int i4 = 0; i4 < 4; ++i4) e[u][odd][i4] *= sc;
+                    }
+                }
+                // a lane's 16 bytes: tokens 4 g .. of the first tile, then of the second
+                uint8_t *to = (uint8_t *)(buf + (P::kFrags + (group * R + vb) * 4) * 64 + 16 * vg + (v_word & 7)) + 8 * second;
+#pragma unroll
+                for (int i4 = 0; i4 < 4; ++i4)
+#pragma unroll
+                    for (int odd = 0; odd < 2; ++odd)
+                        *(uint2 *)(to + 1024 * i4 + 128 * odd) =
+                            make_uint2(__builtin_bit_cast(uint32_t, e[0][odd][i4]), __builtin_bit_cast(uint32_t, e[1][odd][i4]));
+            }
+        };
+
+        __syncthreads();  // the last item's LDS has been read
+        if (tid < 3) most[tid] = 0;
+        if (tid < 4) bad[tid] = 0;
+        __syncthreads();
+        Raw<D> raw;
+        Ids d0 = ids_of(0), d1 = ids_of(1);
+        fetch(raw, d0, 0);
+        look(raw, d0, 0);
+        for (int it = -1; it < count; ++it) {
+            // Step it's fragments are written, step it + 1's words are looked
+            // at, and no wave reads step it - 1 any more.
+            __syncthreads();
+            float next_up = up, f = 1.0f;
+            if (it + 1 < count) {
+                const uint32_t big = uniform((int)most[(it + 1) % 3]);
+                if (big > cap) {  // the same in every wave
+                    const int e = (int)(big >> 10) < 30 ? (int)(big >> 10) : 30;  // scales < 2^(e - 14)
+                    next_up = __builtin_ldexpf(1.0f, 21 - e);
+                    f = next_up / up;
+                    cap = e + 5 > 30 ? 0xffffu : (uint32_t)((e + 5) << 10) - 1;
+                }
+            }
+            if (it >= 0 && tid == 0) {
+                most[it % 3] = 0;        // for step it + 3, looked at after the next barrier
+                bad[(it + 3) % 4] = 0;   // step it - 1's, for step it + 3
+            }
+            unpack(raw, it + 1, next_up);
+            fetch(raw, d1, it + 2);
+            d0 = d1;
+            d1 = ids_of(it + 3);
+            if (it >= 0) {
+                const half8_t *buf = (const half8_t *)(lds + (it & 1) * P::kBuf);
+                const uint8_t *scales = lds + 2 * P::kBuf + it % 3 * P::kScale;
+                const bool gone = uniform((int)bad[it % 4]) != 0;
+#pragma unroll 1
+                for (int sub = 0; sub < kWide / 32; ++sub) {
+                    const int token0 = token_of(it) + 32 * sub;
+                    // nothing of it is visible to the wave's rows
+                    if (token0 > p1 || (a.window > 0 && (int64_t)token0 + 31 + a.window <= p0 && token0 >= a.sinks)) continue;
+                    const bool some = gone || token0 + 32 > w.len || token0 + 31 > p0 ||
+                                      !(a.window <= 0 || (int64_t)token0 + a.window > p1 || token0 + 32 <= a.sinks);
+                    // scores
+                    float4_t sc[NT][2];
+                    uint32_t ks[2][2 * R];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) read_words(ks[i], scales + 2 * R * (32 * sub + 16 * i + 4 * g));
+#pragma unroll
+                    for (int y = 0; y < R; ++y) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const half8_t *k = buf + ((2 * sub + i) * 2 * R + 2 * y) * 64 + lane;
+                            const half8_t k0 = k[0], k1 = k[64];
+                            float4_t c[NT];
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                c[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, q[n][2 * y], (float4_t){0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                c[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, q[n][2 * y + 1], c[n], 0, 0, 0);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    sc[n][i][j] = __builtin_fmaf(c[n][j], half_at(ks[i], R * j + y), y == 0 ? 0.0f : sc[n][i][j]);
+                        }
+                    }
+                    if (some) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const int32_t below = a.window > 0 && pos[n] >= 0 ? pos[n] - a.window : -1;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const int key = token0 + 16 * (j >> 2) + 4 * g + (j & 3), h = R * (j & 3);
+                                const uint32_t bits = ks[j >> 2][h >> 1] >> (16 * (h & 1)) & 0x7fffu;
+                                const bool ok = bits <= 0x7c00u && key < w.len && key <= pos[n] && (key > below || key < a.sinks);
+                                sc[n][j >> 2][j & 3] = ok ? sc[n][j >> 2][j & 3] : -__builtin_inff();
+                            }
+                        }
+                    }
+                    // weights
+                    half8_t p[NT];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float mx = max3(sc[n][0][0], sc[n][0][1], sc[n][0][2]);
+                        mx = max3(mx, sc[n][0][3], sc[n][1][0]);
+                        mx = max3(mx, sc[n][1][1], sc[n][1][2]);
+                        mx = group_max(max2(mx, sc[n][1][3]));
+                        if (__ballot(mx > m[n] + a.slack)) {
+                            const float s = mx > m[n] ? __builtin_amdgcn_exp2f((m[n] - mx) * a.c2) : 1.0f;
+                            m[n] = max2(m[n], mx);
+                            l[n] *= s;
+#pragma unroll
+                            for (int y = 0; y < R; ++y)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) o[n][y][i] *= s;
+                        }
+                        const float mm = kBias - m[n] * a.c2;
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float v = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][j >> 2][j & 3], a.c2, mm));
+                            sum += v;
+                            p[n][j] = (_Float16)v;
+                        }
+                        l[n] += sum;
+                    }
+                    // values
+#pragma unroll
+                    for (int y = 0; y < R; ++y)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const half8_t v = buf[(P::kFrags + (sub * R + y) * 4 + i) * 64 + lane];
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                o[n][y][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[n], o[n][y][i], 0, 0, 0);
+                        }
+                }
+            }
+            if (f != 1.0f) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int y = 0; y < R; ++y)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[n][y][i] *= f;
+            }
+            up = next_up;
+            look(raw, d0, it + 2);
+        }
+
+        const float down = 1.0f / up;
+        const int part_at = 2 * (int)blockIdx.x + (item.s0 == 0 ? 1 : 0);
+        float4_t *part = (float4_t *)(a.part + (int64_t)part_at * P::kPart);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float all_l = group_sum(l[n]);
+            const float f = item.cut ? down : all_l > 0.0f ? down / all_l : 0.0f;
+            const int at = row0 + 16 * n + r, i = at / a.group;
+            const bool live = at < rows;
+            uint16_t *out = a.out + (w.q0 + i) * a.ldo + (int64_t)(head * a.group + at - i * a.group) * D;
+#pragma unroll
+            for (int y = 0; y < 4 * R; ++y) {
+                const float4_t v = o[n][y >> 2][y & 3] * f;
+                if (item.cut) {
+                    if (live) part[((wave * NT + n) * 4 * R + y) * 64 + lane] = v;
+                } else {
+                    store_row(live ? out : nullptr, v, y >> 2, y & 3, g);
+                }
+            }
+            if (item.cut && g == 0) a.part_ml[(int64_t)part_at * kRows + (wave * NT + n) * 16 + r] = make_float2(m[n], all_l);
+        }
+    }
+}
+
+// Add the parts of an item that a workgroup left unfinished.  Grid: x =
+// workgroup, y = block, z = 16-row group.  Product i = wave & 3; W = 16 waves
+// take a fourth of the parts each (few rows: many parts), or four all of them.
+template <int D, int W>
+__global__ __launch_bounds__(64 * W) void kv4_join(AttnArgs a, int groups)
+{
+    constexpr int R = D / 64, F = W / 4;  // F: waves that share a product's parts
+    constexpr int kAt = 4 * W;            // parts at a time
+    __shared__ float4_t frag[W][64];
+    __shared__ float2 ml[kAt][16];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
     const int y = blockIdx.y, n = blockIdx.z, i = wave & 3;
     const Cutoff c = a.cuts[blockIdx.x];
@@ -912,13 +1365,13 @@ __global__ __launch_bounds__(1024) void kv4_join(AttnArgs a, int groups)
     auto part = [&](int j) { return 2 * ((int64_t)blockIdx.x + j) + (j == 0 ? 1 : 0); };
     float m = kLowest, l = 0.0f;
     float4_t o = {0, 0, 0, 0};
-    // 64 parts at a time: each wave takes a fourth of them for its product,
-    // and the rows' (m, l) come one a thread
-    for (int j0 = 0; j0 < parts; j0 += 64) {
+    // each wave takes its share of the parts for its product, and the rows'
+    // (m, l) come one a thread
+    for (int j0 = 0; j0 < parts; j0 += kAt) {
         float4_t v[16];
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
-            const int j = j0 + (wave >> 2) + 4 * x;
+            const int j = j0 + (wave >> 2) + F * x;
             v[x] = (float4_t){0, 0, 0, 0};
             if (j < parts) v[x] = ((const float4_t *)a.part)[(part(j) * groups + n) * 4 * R * 64 + (4 * y + i) * 64 + lane];
         }
@@ -928,16 +1381,16 @@ __global__ __launch_bounds__(1024) void kv4_join(AttnArgs a, int groups)
         ml[threadIdx.x >> 4][threadIdx.x & 15] = x;
         __syncthreads();
         float top = m;
-        for (int j2 = g; j2 < 64; j2 += 4) top = max2(top, ml[j2][r].x);
+        for (int j2 = g; j2 < kAt; j2 += 4) top = max2(top, ml[j2][r].x);
         top = group_max(top);
         const float f = __builtin_amdgcn_exp2f((m - top) * a.c2);
         l *= f;
         o *= f;
-        for (int j2 = g; j2 < 64; j2 += 4) l += ml[j2][r].y * __builtin_amdgcn_exp2f((ml[j2][r].x - top) * a.c2);
+        for (int j2 = g; j2 < kAt; j2 += 4) l += ml[j2][r].y * __builtin_amdgcn_exp2f((ml[j2][r].x - top) * a.c2);
 #pragma unroll
         for (int x2 = 0; x2 < 16; ++x2)
-            if (j0 + (wave >> 2) + 4 * x2 < parts)
-                o += v[x2] * __builtin_amdgcn_exp2f((ml[(wave >> 2) + 4 * x2][r].x - top) * a.c2);
+            if (j0 + (wave >> 2) + F * x2 < parts)
+                o += v[x2] * __builtin_amdgcn_exp2f((ml[(wave >> 2) + F * x2][r].x - top) * a.c2);
         m = top;
     }
     l = group_sum(l);
@@ -947,12 +1400,15 @@ __global__ __launch_bounds__(1024) void kv4_join(AttnArgs a, int groups)
         const int at = c.row0 + 16 * n + r, q = at / a.group;
         o = frag[wave][lane];
 #pragma unroll
-        for (int x = 1; x < 4; ++x) o += frag[4 * x + wave][lane];
+        for (int x = 1; x < F; ++x) o += frag[4 * x + wave][lane];
         const float f = l > 0.0f ? 1.0f / l : 0.0f;
         uint16_t *out = a.out + (c.q0 + q) * a.ldo + (int64_t)(c.head * a.group + at - q * a.group) * D;
         store_row(at < c.rows ? out : nullptr, o * f, y, wave, g);
     }
 }
+
+// 16-row groups of a prompt's waves.
+template <int D> constexpr int kPromptRows = 2;
 
 // How a call is cut.
 struct Cut {
@@ -968,7 +1424,8 @@ Cut cut(const pn_kv4_cache *c, int q_heads, int64_t max_q, int64_t max_kv, int w
     const int64_t rows = max_q * (q_heads / c->heads);
     const int most = c->dim == 256 ? 2 : 4;  // that the registers hold
     t.nt = rows >= 16 * most ? most : (int)((rows + 15) / 16);
-    t.rg = rows > 32 * most ? 4 : 1;
+    t.rg = rows > 32 * most ? c->dim == 256 ? 4 : kWaves : 1;
+    if (t.rg == kWaves) t.nt = c->dim == 128 ? kPromptRows<128> : kPromptRows<64>;
     int64_t keys = max_kv;
     if (window > 0) {
         const int64_t reach = (int64_t)window + max_q + sinks + 2 * kStep;
@@ -987,12 +1444,18 @@ template <int D, int NT, int RG> bool raise_one()
                                Shape<D, NT, RG>::kLds) == hipSuccess;
 }
 
+template <int D> bool raise_prompt()
+{
+    return hipFuncSetAttribute((const void *)kv4_prompt<D, kPromptRows<D>>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                               Prompt<D, kPromptRows<D>>::kLds) == hipSuccess;
+}
+
 bool raise_lds()
 {
     return raise_one<64, 1, 1>() && raise_one<64, 2, 1>() && raise_one<64, 3, 1>() && raise_one<64, 4, 1>() &&
-           raise_one<64, 4, 4>() && raise_one<128, 1, 1>() && raise_one<128, 2, 1>() && raise_one<128, 3, 1>() &&
-           raise_one<128, 4, 1>() && raise_one<128, 4, 4>() && raise_one<256, 1, 1>() && raise_one<256, 2, 1>() &&
-           raise_one<256, 2, 4>();
+           raise_one<128, 1, 1>() && raise_one<128, 2, 1>() && raise_one<128, 3, 1>() &&
+           raise_one<128, 4, 1>() && raise_one<256, 1, 1>() && raise_one<256, 2, 1>() &&
+           raise_one<256, 2, 4>() && raise_prompt<64>() && raise_prompt<128>();
 }
 
 template <int D, int NT, int RG>
@@ -1002,7 +1465,21 @@ pn_status launch(const AttnArgs &a, hipStream_t s)
     hipLaunchKernelGGL((kv4_attn<D, NT, RG>), dim3((unsigned)a.workers), dim3(kThreads), (Shape<D, NT, RG>::kLds), s, a);
     if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
     if (!a.whole) {
-        hipLaunchKernelGGL(kv4_join<D>, dim3((unsigned)a.workers, D / 64, NT * RG), dim3(1024), 0, s, a, NT * RG);
+        constexpr int W = RG == 1 ? 16 : 4;
+        hipLaunchKernelGGL((kv4_join<D, W>), dim3((unsigned)a.workers, D / 64, NT * RG), dim3(64 * W), 0, s, a, NT * RG);
+        if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
+    }
+    return PN_OK;
+}
+
+template <int D, int NT>
+pn_status launch_prompt(const AttnArgs &a, hipStream_t s)
+{
+    if (!once_per_device(kAttrKv4, raise_lds)) return PN_ELAUNCH;
+    hipLaunchKernelGGL((kv4_prompt<D, NT>), dim3((unsigned)a.workers), dim3(kThreads), (Prompt<D, NT>::kLds), s, a);
+    if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
+    if (!a.whole) {
+        hipLaunchKernelGGL((kv4_join<D, 4>), dim3((unsigned)a.workers, D / 64, NT * kWaves), dim3(256), 0, s, a, NT * kWaves);
         if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
     }
     return PN_OK;
@@ -1012,7 +1489,11 @@ template <int D>
 pn_status launch_rows(const AttnArgs &a, const Cut &t, hipStream_t s)
 {
     constexpr int most = D == 256 ? 2 : 4;
-    if (t.rg == 4) return launch<D, most, 4>(a, s);
+    if constexpr (D == 256) {
+        if (t.rg > 1) return launch<D, most, 4>(a, s);
+    } else {
+        if (t.rg > 1) return launch_prompt<D, kPromptRows<D>>(a, s);
+    }
     if (t.nt == 1) return launch<D, 1, 1>(a, s);
     if (t.nt == 2) return launch<D, 2, 1>(a, s);
     if constexpr (D <= 128) {
@@ -1097,6 +1578,7 @@ extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, i
     a.sinks = sinks;
     a.workers = t.workers;
     a.whole = t.whole;
+    a.over = t.rg == kWaves ? 4 : 32;
     a.negate = scale < 0.0f;
     // Not 0: a masked score is -inf, whose product with c2 has to stay so.
     a.c2 = __builtin_fmaxf(__builtin_fabsf(scale) * 1.4426950408889634f, 0x1p-100f);
