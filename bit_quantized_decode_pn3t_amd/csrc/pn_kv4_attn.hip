@@ -37,17 +37,14 @@
 // pieces are permuted on the way so that the reads spread over the banks.
 //
 // Work is dealt in equal shares, whatever the lengths: the items (request,
-// key-value head, row tile), each as long as its request has steps to see and
-// a little more for its start and end, form one line that the workgroups cut
-// into equal parts.  Every workgroup sums the requests for itself.  Later row
-// tiles of a prompt see more keys than earlier ones: a part of an item is a
-// part of the steps it really has, and the tiles are taken from both ends in
-// turn, so that neighbours make up for each other.  With few rows (RG = 1)
-// a workgroup's eight waves take every eighth step of the same rows; with
-// many (RG = 4) four groups of two waves take rows of their own and share the
-// staged steps, one of two each.  The waves of the same rows are joined
-// through LDS; an item cut between workgroups leaves parts in the workspace,
-// which kv4_join adds.  All sums have a fixed order.
+// key-value head, row tile), each about as long as the steps it sees and what
+// its start and end cost, form one line that the workgroups cut into equal
+// parts.  Every workgroup sums the requests for itself and finds its items;
+// an item cut between workgroups leaves parts in the workspace, which
+// kv4_join adds.  With few rows (RG = 1) a workgroup's eight waves take every
+// eighth step of the same rows; with more (RG = 4) four groups of two waves
+// take rows of their own and share the staged steps, one of two each.  The
+// waves of the same rows are joined through LDS.  All sums have a fixed order.
 #include "pn_kv4.h"
 #include "pn_device.h"
 
@@ -97,17 +94,19 @@ struct Cutoff {
 };
 
 // The part of a request that a row tile works on.
-struct Work {
+struct Request {
     int64_t q0;       // first query row of the request
     int32_t qn;       // queries of the request that are computed
     int32_t first;    // position of query 0
     int32_t len;      // keys
+};
+struct Work : Request {
     int32_t sink_steps, lo, steps;  // steps [0, sink_steps), then from lo; steps in all
 };
 
-__device__ __forceinline__ Work request(const AttnArgs &a, int b)
+__device__ __forceinline__ Request request(const AttnArgs &a, int b)
 {
-    Work w;
+    Request w;
     int64_t q0 = a.q_start[b], q1 = a.q_start[b + 1];
     q0 = q0 < 0 ? 0 : q0 > a.total_q ? a.total_q : q0;
     q1 = q1 < q0 ? q0 : q1 > a.total_q ? a.total_q : q1;
@@ -116,7 +115,6 @@ __device__ __forceinline__ Work request(const AttnArgs &a, int b)
     w.first = (int32_t)(kv - (q1 - q0));
     w.qn = (int32_t)(q1 - q0 < a.max_q ? q1 - q0 : a.max_q);
     w.len = kv < a.max_kv ? kv : (int32_t)a.max_kv;
-    w.sink_steps = w.lo = w.steps = 0;
     return w;
 }
 
@@ -140,12 +138,21 @@ __device__ __forceinline__ void span(const AttnArgs &a, Work &w, int i0, int i1)
     w.steps = w.sink_steps + (end > w.lo ? end - w.lo : 0);
 }
 
-// What the line counts for request b: its row tiles and the steps that all of
-// its queries see together.  Queries without keys count one step: they have
-// zeros to write.
+// a / b for non-negative a: a 64-bit quotient takes some hundred instructions.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    if (((uint64_t)a | (uint64_t)b) >> 32 == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
+// What the line counts for request b: its row tiles, and for tile t a length
+// of min(base + t grow, top) sixteenths of a step: what its start and end
+// cost, and about the steps it sees (a later tile of a prompt more, up to the
+// window).  Only the balance depends on these lengths.
+constexpr int kUnit = 16;
 struct Cost {
-    Work w;
-    int32_t steps, tiles;
+    Request w;
+    int32_t tiles, base, grow, top;
 };
 
 template <int STEP>
@@ -153,18 +160,38 @@ __device__ __forceinline__ Cost cost(const AttnArgs &a, int b, int tile_rows)
 {
     Cost c;
     c.w = request(a, b);
-    c.steps = c.tiles = 0;
+    c.tiles = c.base = c.top = c.grow = 0;
     if (c.w.qn < 1) return c;
-    Work all = c.w;
-    span<STEP>(a, all, 0, c.w.qn - 1);
-    c.steps = all.steps < 1 ? 1 : all.steps;
     c.tiles = (c.w.qn * a.group + tile_rows - 1) / tile_rows;
+    const int queries = (tile_rows + a.group - 1) / a.group;  // of a tile
+    int32_t see = c.w.first + (c.w.qn < queries ? c.w.qn : queries);
+    see = see < 0 ? 0 : see < c.w.len ? see : c.w.len;
+    int32_t most = c.w.len;
+    if (a.window > 0 && (int64_t)a.window + a.sinks + queries < most) most = a.window + a.sinks + queries;
+    const int32_t fixed = (a.over + 1) * kUnit;
+    c.top = fixed + (int32_t)((int64_t)most * kUnit / STEP);
+    c.base = fixed + (int32_t)((int64_t)see * kUnit / STEP);
+    if (c.base > c.top) c.base = c.top;
+    c.grow = tile_rows * kUnit / (a.group * STEP);
     return c;
 }
 
+// Tiles whose length still grows, and the length of the first t tiles.
+__device__ __forceinline__ int32_t growing(const Cost &c)
+{
+    if (c.base >= c.top) return 0;
+    if (c.grow == 0) return c.tiles;
+    const int32_t n = (c.top - c.base + c.grow - 1) / c.grow;
+    return n < c.tiles ? n : c.tiles;
+}
+__device__ __forceinline__ int64_t before_tile(const Cost &c, int32_t n, int64_t t)
+{
+    const int64_t g = t < n ? t : n;
+    return g * c.base + g * (g - 1) / 2 * c.grow + (t - g) * c.top;
+}
 __device__ __forceinline__ int64_t length(const AttnArgs &a, const Cost &c)
 {
-    return (int64_t)(c.steps + a.over) * c.tiles * a.c.heads;
+    return before_tile(c, growing(c), c.tiles) * a.c.heads;
 }
 
 // The same in every lane: into scalar registers.
@@ -179,9 +206,10 @@ __device__ __forceinline__ Cost scalar(const Cost &m)
     c.w.qn = uniform(m.w.qn);
     c.w.first = uniform(m.w.first);
     c.w.len = uniform(m.w.len);
-    c.steps = uniform(m.steps);
     c.tiles = uniform(m.tiles);
-    c.w.sink_steps = c.w.lo = c.w.steps = 0;  // the row tile's, to be filled in
+    c.base = uniform(m.base);
+    c.grow = uniform(m.grow);
+    c.top = uniform(m.top);
     return c;
 }
 
@@ -193,6 +221,7 @@ struct LineLds {
     int64_t at[2];
     Cost known[64];
 };
+static_assert(sizeof(LineLds) <= 2944, "two workgroups' LDS (narrow heads, few rows)");
 
 struct Line {
     int64_t lo, hi, share;
@@ -236,8 +265,11 @@ __device__ __forceinline__ bool line_part(const AttnArgs &a, LineLds &s, Line &t
         }
     }
     total = uniform64(total);
-    t.share = (total + a.workers - 1) / a.workers;
-    if (t.share < kShare && !a.whole) t.share = kShare;
+    // A few workgroups fewer than there are: with four items or more no item
+    // then has over 64 parts, which is what the join takes at a time.
+    const int32_t dealt = a.workers - a.workers / 64;
+    t.share = quotient(total + dealt - 1, dealt);
+    if (t.share < kShare * kUnit && !a.whole) t.share = kShare * kUnit;
     t.lo = blockIdx.x * t.share;
     t.hi = t.lo + t.share < total ? t.lo + t.share : total;
     if (tid == 0 && !a.whole) a.cuts[blockIdx.x].parts = 0;
@@ -268,42 +300,63 @@ __device__ __forceinline__ bool line_part(const AttnArgs &a, LineLds &s, Line &t
 // The next item of the part.
 struct Item {
     Cost c;
-    int32_t s0, s1;  // steps of those the line counts
+    int32_t s0, s1, all;        // its part [s0, s1) of `all` (lengths on the line)
     int32_t head, tile0, rows;  // the tile's first row, the request's rows
     bool cut;
 };
 
-// Step x on along the line; false: a stretch without an item's steps.
+// Steps that a part of an item stands for: the same part of the `steps` it has.
+__device__ __forceinline__ int share_of(int32_t s, int32_t all, int steps) { return uniform((int)quotient((int64_t)s * steps, all)); }
+
+// Go on along the line from x; false: a stretch without an item's steps.
 template <int STEP>
 __device__ __forceinline__ bool next_item(const AttnArgs &a, const LineLds &s, Line &t, int64_t &x, Item &m, int tile_rows)
 {
     m.c = scalar(t.few ? s.known[t.b] : cost<STEP>(a, t.b, tile_rows));
-    const int64_t all = length(a, m.c);
-    if (x >= t.start + all) {
-        t.start += all;
+    const int32_t n = growing(m.c);
+    const int64_t head_len = before_tile(m.c, n, m.c.tiles);
+    if (x >= t.start + head_len * a.c.heads) {
+        t.start += head_len * a.c.heads;
         ++t.b;
         return false;
     }
-    const int one = m.c.steps + a.over;  // an item's length on the line
-    const int item = uniform((int)((x - t.start) / one));
-    const int64_t first = t.start + (int64_t)item * one;  // of the item on the line
+    m.head = uniform((int)quotient(x - t.start, head_len));
+    const int64_t off = x - t.start - m.head * head_len;
+    // the tile: largest with before_tile <= off
+    int32_t tile = 0;
+    const int64_t flat = before_tile(m.c, n, n);
+    if (m.c.tiles == 1) {
+    } else if (off >= flat) {
+        tile = n + (int32_t)quotient(off - flat, m.c.top);
+    } else if (m.c.grow == 0) {
+        tile = (int32_t)quotient(off, m.c.base);
+    } else {
+        const double h = m.c.base - 0.5 * m.c.grow;
+        tile = (int32_t)((__builtin_sqrt(h * h + 2.0 * m.c.grow * (double)off) - h) / m.c.grow);
+        if (tile >= n) tile = n - 1;
+        if (tile < 0) tile = 0;
+        while (tile > 0 && before_tile(m.c, n, tile) > off) --tile;
+        while (tile + 1 < n && before_tile(m.c, n, tile + 1) <= off) ++tile;
+    }
+    tile = uniform(tile);
+    const int64_t first = t.start + m.head * head_len + before_tile(m.c, n, tile);  // of the item on the line
+    const int one = (int)(before_tile(m.c, n, tile + 1) - before_tile(m.c, n, tile));
     int s0 = (int)(x - first), s1 = (int)(t.hi - first < one ? t.hi - first : one);
     x = first + s1;
     if (a.whole) {  // items are taken whole, by the workgroup they start in
         if (s0 > 0) return false;
         s1 = one;
     }
-    s0 = s0 > a.over ? s0 - a.over : 0;
-    s1 -= a.over;
+    const int over = a.over * kUnit;  // the first stretch of an item: nobody's steps
+    s0 = s0 > over ? s0 - over : 0;
+    s1 -= over;
     if (s1 <= s0) return false;
-    m.s0 = uniform(s0), m.s1 = uniform(s1);
-    m.cut = s0 > 0 || s1 < m.c.steps;
-    m.head = item / m.c.tiles;
-    const int turn = item - m.head * m.c.tiles;
-    m.tile0 = (turn & 1 ? m.c.tiles - 1 - (turn >> 1) : turn >> 1) * tile_rows;
+    m.s0 = uniform(s0), m.s1 = uniform(s1), m.all = uniform(one - over);
+    m.cut = s0 > 0 || s1 < m.all;
+    m.tile0 = tile * tile_rows;
     m.rows = m.c.w.qn * a.group;
     if (m.s0 == 0 && m.cut && threadIdx.x == 0)
-        a.cuts[blockIdx.x] = {m.c.w.q0, m.tile0, m.rows, m.head, (int)((first + one - 1) / t.share) - (int)blockIdx.x + 1};
+        a.cuts[blockIdx.x] = {m.c.w.q0, m.tile0, m.rows, m.head, (int)quotient(first + one - 1, t.share) - (int)blockIdx.x + 1};
     return true;
 }
 
@@ -467,6 +520,15 @@ __device__ __forceinline__ half8_t codes8(uint32_t word)
 #pragma unroll
     for (int i = 0; i < 4; ++i) r[2 * i] = t[i][0], r[2 * i + 1] = t[i][1];
     return r;
+}
+
+// A barrier for what is in LDS: loads in flight stay so.
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // N dwords from LDS, 8 or 16 bytes at a time.
@@ -718,17 +780,21 @@ __device__ __forceinline__ void advance(State<D, NT> &st, const uint8_t *from, c
 }
 
 // Lane (r, g) holds x[j] = element 64 b + 8 (4 (g & 1) + j) + 2 i + (g >> 1)
-// of row r; store it as fp16 pairs.
+// of row r.  As fp16 pairs: elements 2 i and 2 i + 1 of word 4 (g & 1) + j +
+// (g & 2) of the block, j < 2 (lanes below 32 take x[j], those above x[j + 2]).
+__device__ __forceinline__ uint32_t row_pair(const float4_t &x, int j)
+{
+    auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x[j]), __float_as_uint(x[j + 2]), false, false);
+    const uint32_t lo = __builtin_bit_cast(uint16_t, (_Float16)__uint_as_float(s[0]));
+    const uint32_t hi = __builtin_bit_cast(uint16_t, (_Float16)__uint_as_float(s[1]));
+    return lo | hi << 16;
+}
 __device__ __forceinline__ void store_row(uint16_t *out, const float4_t &x, int b, int i, int g)
 {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        // lanes below 32 take x[j], those above x[j + 2], both elements of the pair
-        auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x[j]), __float_as_uint(x[j + 2]), false, false);
-        const uint32_t lo = __builtin_bit_cast(uint16_t, (_Float16)__uint_as_float(s[0]));
-        const uint32_t hi = __builtin_bit_cast(uint16_t, (_Float16)__uint_as_float(s[1]));
-        const int word = 4 * (g & 1) + j + (g & 2);
-        if (out) *(uint32_t *)(out + 64 * b + 8 * word + 2 * i) = lo | hi << 16;
+        const uint32_t pair = row_pair(x, j);
+        if (out) *(uint32_t *)(out + 64 * b + 8 * (4 * (g & 1) + j + (g & 2)) + 2 * i) = pair;
     }
 }
 
@@ -778,11 +844,10 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
     for (int64_t x = line.lo; x < line.hi;) {
         Item item;
         if (!next_item<kStep>(a, line_lds, line, x, item, kRows)) continue;
-        const Cost &c = item.c;
-        const int s0 = item.s0, s1 = item.s1, head = item.head, tile0 = item.tile0, rows = item.rows, b = line.b;
+        const int s0 = item.s0, head = item.head, tile0 = item.tile0, rows = item.rows, b = line.b;
         const bool cut = item.cut;
 
-        Work w = c.w;
+        Work w{item.c.w};
         span<kStep>(a, w, tile0 / a.group, ((tile0 + kRows < rows ? tile0 + kRows : rows) - 1) / a.group);
         // the wave's own rows (none: nothing is visible)
         const int row0 = tile0 + rg * 16 * NT;
@@ -812,8 +877,8 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
 
         // The same part of the steps that this tile has.
         auto place = [&](int e) { return e < w.sink_steps ? e : e - w.sink_steps + w.lo; };
-        const int e1 = uniform((int)((int64_t)s1 * w.steps / c.steps));
-        int e = uniform((int)((int64_t)s0 * w.steps / c.steps));
+        const int e1 = share_of(item.s1, item.all, w.steps);
+        int e = share_of(s0, item.all, w.steps);
         const int turns = (e1 - e + KW - 1) / KW;  // the same for all waves
         e += kg;
         const int32_t *row = uniform_ptr(a.table + (int64_t)b * a.ld_table);
@@ -964,16 +1029,14 @@ template <int D, int NT> struct Prompt {
     static constexpr int kScale = kWide * R * 2;            // K's scales of a step: [token][block] fp16
     static constexpr int kLds = 2 * kBuf + 3 * kScale;
     static constexpr int kPart = kWaves * NT * 4 * R * 256; // floats of a part
-    static constexpr int kPairs = kWide * (D / 16) / 256;   // key word pairs of a thread
+    static constexpr int kUnits = 2 * D;                    // 16-byte units of a step's key codes, and of its value codes
 };
 
-// What a thread has of a step to come: key word pairs and its token's scales,
-// or four tokens' value words and scales.
+// What a thread has of a step to come: one unit of codes, and the scales of
+// the four tokens that its own belongs to.
 template <int D> struct Raw {
-    uint2 k[Prompt<D, 1>::kPairs];
-    uint32_t ks;
-    uint4 v;
-    uint32_t vs[2 * (D / 64)];
+    uint4 w;
+    uint32_t s[2 * (D / 64)];
 };
 
 template <int D, int NT>
@@ -990,21 +1053,21 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
     const bool keys = wave >= 4;       // unpacks keys; else values
-    const int half_tid = tid & 255;
     const int T = 1 << a.c.shift;      // tokens of a page
-    // A key thread: pairs (row, 2 words); a value thread: four tokens of one word.
-    constexpr int kPer = D / 16;       // pairs of a row
-    const int k_row = half_tid / kPer, k_pair = half_tid % kPer;
-    const int v_t4 = half_tid / (D / 8), v_word = half_tid % (D / 8);
-    const bool v_on = !keys && v_t4 < kWide / 4;
-
+    // A thread's unit (narrow heads leave every second thread a copy of
+    // another's, which it does not write).  Of keys: D / 32 units a row, four
+    // words.  Of values: word `part` of four tokens.
+    const int unit = tid & (P::kUnits - 1);
+    const bool on = (tid & 255) < P::kUnits;
+    const int part = keys ? unit % (D / 32) : unit % (D / 8);
+    const int token = keys ? unit / (D / 32) : unit / (D / 8) * 4;  // of the step
     Line line;
     if (!line_part<kWide>(a, line_lds, line, kRows)) return;
     for (int64_t x = line.lo; x < line.hi;) {
         Item item;
         if (!next_item<kWide>(a, line_lds, line, x, item, kRows)) continue;
         const int head = item.head, tile0 = item.tile0, rows = item.rows, b = line.b;
-        Work w = item.c.w;
+        Work w{item.c.w};
         const int tile_last = (tile0 + kRows < rows ? tile0 + kRows : rows) - 1;
         span<kWide>(a, w, tile0 / a.group, tile_last / a.group);
         const int32_t t_low = w.first + tile0 / a.group, t_high = w.first + tile_last / a.group;  // the tile's positions
@@ -1038,141 +1101,99 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
         float up = 1.0f;   // 2^u on the values being added
         uint32_t cap = 0;  // largest scale (fp16 bits) that the next step's u leaves below 2^11
 
-        const int e0 = uniform((int)((int64_t)item.s0 * w.steps / item.c.steps));
-        const int count = uniform((int)((int64_t)item.s1 * w.steps / item.c.steps)) - e0;
+        const int e0 = share_of(item.s0, item.all, w.steps);
+        const int count = share_of(item.s1, item.all, w.steps) - e0;
         auto token_of = [&](int i) {
             const int e = e0 + i;
             return (e < w.sink_steps ? e : e - w.sink_steps + w.lo) * kWide;
         };
-        const int32_t *row = a.table + (int64_t)b * a.ld_table;
-        // Page of token t, -1 if it is none of the cache.
-        auto page_at = [&](int t) {
-            const int at = t >> a.c.shift;
-            return at < a.max_pages ? row[at] : -1;
+        const int32_t *row = uniform_ptr(a.table + (int64_t)b * a.ld_table);
+        // Page of the thread's token in step i.  Steps past the end repeat the last.
+        auto page_of = [&](int i) {
+            const int at = (token_of(i < count ? i : count - 1) + token) >> a.c.shift;
+            return ((const PN_GLOBAL int32_t *)row)[at < a.max_pages ? at : a.max_pages - 1];
         };
-        struct Ids {
-            int32_t p[P::kPairs];
+        auto ok_page = [&](int32_t page, int i) {
+            return (uint32_t)page < (uint32_t)a.c.num_pages && (token_of(i) + token) >> a.c.shift < a.max_pages;
         };
-        // The pages of the thread's tokens in step i.
-        auto ids_of = [&](int i) {
-            Ids d;
-#pragma unroll
-            for (int y = 0; y < P::kPairs; ++y) d.p[y] = -1;
-            if (i < count) {
-                const int t0 = token_of(i);
-                if (keys) {
-#pragma unroll
-                    for (int y = 0; y < P::kPairs; ++y) d.p[y] = page_at(t0 + k_row + 256 / kPer * y);
-                } else if (v_on) {
-                    d.p[0] = page_at(t0 + 4 * v_t4);
-                }
-            }
-            return d;
-        };
-        auto base_of = [&](int32_t page) { return a.c.pages + ((int64_t)page * a.c.heads + head) * a.c.chunk; };
-        auto ok_page = [&](int32_t page) { return (uint32_t)page < (uint32_t)a.c.num_pages; };
-        // Start the loads of step i.
-        auto fetch = [&](Raw<D> &raw, const Ids &d, int i) {
-            if (i >= count) return;
-            const int t0 = token_of(i);
-            if (keys) {
-#pragma unroll
-                for (int y = 0; y < P::kPairs; ++y) {
-                    const int o = (t0 + k_row + 256 / kPer * y) & (T - 1);
-                    raw.k[y] = make_uint2(0x88888888u, 0x88888888u);
-                    if (ok_page(d.p[y])) raw.k[y] = *(const uint2 *)(base_of(d.p[y]) + o * L::kRow + 8 * k_pair);
-                }
-                // the scales of one row a thread: pair y of it (pairs 0 .. kPairs - 1 fetch rows k_row + ... y)
-                raw.ks = 0;
-#pragma unroll
-                for (int y = 0; y < P::kPairs; ++y) {
-                    if (k_pair != y) continue;
-                    const int o = (t0 + k_row + 256 / kPer * y) & (T - 1);
-                    if (ok_page(d.p[y])) {
-                        const uint8_t *s = base_of(d.p[y]) + L::k_scales(T) + 2 * R * o;
-                        raw.ks = R == 1 ? *(const uint16_t *)s : *(const uint32_t *)s;
-                    }
-                }
-            } else if (v_on) {
-                const int o = (t0 + 4 * v_t4) & (T - 1);
-                raw.v = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int y = 0; y < 2 * R; ++y) raw.vs[y] = 0;
-                if (ok_page(d.p[0])) {
-                    const uint8_t *from = base_of(d.p[0]);
-                    raw.v = *(const uint4 *)(from + L::v_codes(T) + ((o >> 2) * (D / 8) + v_word) * 16);
-                    const uint8_t *s = from + L::v_scales(T) + 2 * R * o;
-                    if constexpr (R == 1) {
-                        const uint2 y = *(const uint2 *)s;
-                        raw.vs[0] = y.x, raw.vs[1] = y.y;
-                    } else {
-                        const uint4 y = *(const uint4 *)s;
-                        raw.vs[0] = y.x, raw.vs[1] = y.y, raw.vs[2] = y.z, raw.vs[3] = y.w;
-                    }
-                }
+        // Start the loads of step i; without a branch, or a join of branches
+        // would wait for them.  A page that is none of the cache reads page 0.
+        auto fetch = [&](Raw<D> &raw, int32_t page, int i) {
+            const int o = (token_of(i < count ? i : count - 1) + token) & (T - 1);
+            const int64_t at = (uint32_t)page < (uint32_t)a.c.num_pages ? page : 0;
+            const uint8_t *from = a.c.pages + (at * a.c.heads + head) * a.c.chunk;
+            raw.w = *(const uint4 *)(from + (uint32_t)(keys ? o * L::kRow + 16 * part
+                                                            : L::v_codes(T) + ((o >> 2) * (D / 8) + part) * 16));
+            const uint8_t *sc = from + (uint32_t)((keys ? L::k_scales(T) : L::v_scales(T)) + 2 * R * (o & ~3));
+            if constexpr (R == 1) {
+                const uint2 y = *(const uint2 *)sc;
+                raw.s[0] = y.x, raw.s[1] = y.y;
+            } else {
+                const uint4 y = *(const uint4 *)sc;
+                raw.s[0] = y.x, raw.s[1] = y.y, raw.s[2] = y.z, raw.s[3] = y.w;
             }
         };
         // The step's words have come: value scales that no row sees become 0
         // (they may be anything), the others are held against the cap; key
         // scales go to LDS, NaN for a token without a page.
-        auto look = [&](Raw<D> &raw, const Ids &d, int i) {
+        auto look = [&](Raw<D> &raw, int32_t page, int i) {
             if (i >= count) return;
-            const int t0 = token_of(i);
+            const bool gone = !ok_page(page, i);
             if (keys) {
-#pragma unroll
-                for (int y = 0; y < P::kPairs; ++y) {
-                    if (k_pair != y) continue;
-                    const int t = k_row + 256 / kPer * y;
-                    const bool gone = !ok_page(d.p[y]);
-                    uint8_t *to = lds + 2 * P::kBuf + i % 3 * P::kScale + 2 * R * t;
-                    if (R == 1) *(uint16_t *)to = gone ? 0x7e00 : (uint16_t)raw.ks;
-                    else *(uint32_t *)to = gone ? 0x7e007e00u : raw.ks;
+                if (part == 0 && on) {
+                    uint8_t *to = lds + 2 * P::kBuf + i % 3 * P::kScale + 2 * R * token;
+                    if constexpr (R == 1) {
+                        const uint32_t w2 = token & 2 ? raw.s[1] : raw.s[0];
+                        *(uint16_t *)to = gone ? 0x7e00 : (uint16_t)(token & 1 ? w2 >> 16 : w2);
+                    } else {
+                        const uint32_t lo = token & 1 ? raw.s[1] : raw.s[0], hi = token & 1 ? raw.s[3] : raw.s[2];
+                        *(uint32_t *)to = gone ? 0x7e007e00u : token & 2 ? hi : lo;
+                    }
                     if (gone) bad[i % 4] = 1;
                 }
-            } else if (v_on) {
+            } else {
+                const int t0 = token_of(i);
                 const int32_t under = a.window > 0 ? t_low - a.window : -1;
-                uint32_t any = 0;
+                const bool whole = t0 + kWide <= w.len && t0 + kWide - 1 <= t_high && (t0 > under || t0 + kWide <= a.sinks);
+                if (!whole || gone) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int t = t0 + 4 * v_t4 + j;
-                    const bool seen = t < w.len && t <= t_high && (t > under || t < a.sinks);
+                    for (int j = 0; j < 4; ++j) {
+                        const int t = t0 + token + j;
+                        const bool seen = !gone && t < w.len && t <= t_high && (t > under || t < a.sinks);
 #pragma unroll
-                    for (int z = 0; z < R; ++z) {
-                        const int h = R * j + z;
-                        if (!seen) raw.vs[h >> 1] &= h & 1 ? 0x0000ffffu : 0xffff0000u;
+                        for (int z = 0; z < R; ++z) {
+                            const int h = R * j + z;
+                            if (!seen) raw.s[h >> 1] &= h & 1 ? 0x0000ffffu : 0xffff0000u;
+                        }
                     }
                 }
+                ushort2_t any = {0, 0};
 #pragma unroll
-                for (int y = 0; y < 2 * R; ++y) {
-                    const uint32_t s = raw.vs[y] & 0x7fff7fffu;
-                    any = (s >> 16) > any ? s >> 16 : any;
-                    any = (s & 0xffffu) > any ? s & 0xffffu : any;
-                }
-                if (any > cap) atomicMax(&most[i % 3], any);
+                for (int y = 0; y < 2 * R; ++y)
+                    any = __builtin_elementwise_max(any, __builtin_bit_cast(ushort2_t, raw.s[y] & 0x7fff7fffu));
+                const uint32_t big = any[0] > any[1] ? any[0] : any[1];
+                if (big > cap) atomicMax(&most[i % 3], big);
             }
         };
         // Words into fragments.
         auto unpack = [&](const Raw<D> &raw, int i, float factor) {
-            if (i >= count) return;
+            if (i >= count || !on) return;
             half8_t *buf = (half8_t *)(lds + (i & 1) * P::kBuf);
+            const uint32_t words[4] = {raw.w.x, raw.w.y, raw.w.z, raw.w.w};
             if (keys) {
+                // words (b, h) of one group g of the row, or with one block (h) of two groups
+                half8_t *to = buf + (token >> 4) * 2 * R * 64 + (R == 1 ? 32 : 16) * part + (token & 15);
 #pragma unroll
-                for (int y = 0; y < P::kPairs; ++y) {
-                    const int t = k_row + 256 / kPer * y, kg = k_pair / R, kb = k_pair % R;
-                    half8_t *to = buf + ((t >> 4) * 2 * R + 2 * kb) * 64 + 16 * kg + (t & 15);
-                    to[0] = codes8(raw.k[y].x);
-                    to[64] = codes8(raw.k[y].y);
-                }
-            } else if (v_on) {
-                const int vb = v_word >> 3, group = v_t4 >> 3, second = v_t4 >> 2 & 1, vg = v_t4 & 3;
+                for (int y = 0; y < 4; ++y) to[R == 1 ? (y & 1) * 64 + (y >> 1) * 16 : y * 64] = codes8(words[y]);
+            } else {
+                const int vb = part >> 3, group = token >> 5, second = token >> 4 & 1, vg = token >> 2 & 3;
                 const half2_t f2 = {(_Float16)factor, (_Float16)factor};
-                const uint32_t words[4] = {raw.v.x, raw.v.y, raw.v.z, raw.v.w};
                 half2_t e[2][2][4];  // [token pair][odd element][product]
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     half2_t sc;
-                    if constexpr (R == 1) sc = as_half2(raw.vs[u]);
-                    else sc = as_half2(__builtin_amdgcn_perm(raw.vs[2 * u + 1], raw.vs[2 * u], vb ? 0x07060302u : 0x05040100u));
+                    if constexpr (R == 1) sc = as_half2(raw.s[u]);
+                    else sc = as_half2(__builtin_amdgcn_perm(raw.s[2 * u + 1], raw.s[2 * u], vb ? 0x07060302u : 0x05040100u));
                     sc *= f2;
 #pragma unroll
                     for (int odd = 0; odd < 2; ++odd) {
@@ -1182,7 +1203,7 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
                     }
                 }
                 // a lane's 16 bytes: tokens 4 g .. of the first tile, then of the second
-                uint8_t *to = (uint8_t *)(buf + (P::kFrags + (group * R + vb) * 4) * 64 + 16 * vg + (v_word & 7)) + 8 * second;
+                uint8_t *to = (uint8_t *)(buf + (P::kFrags + (group * R + vb) * 4) * 64 + 16 * vg + (part & 7)) + 8 * second;
 #pragma unroll
                 for (int i4 = 0; i4 < 4; ++i4)
 #pragma unroll
@@ -1197,13 +1218,17 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
         if (tid < 4) bad[tid] = 0;
         __syncthreads();
         Raw<D> raw;
-        Ids d0 = ids_of(0), d1 = ids_of(1);
-        fetch(raw, d0, 0);
-        look(raw, d0, 0);
-        for (int it = -1; it < count; ++it) {
+        int32_t d0 = 0, d1 = 0;  // pages of steps it + 1 and it + 2
+        if (count > 0) {
+            d0 = page_of(0), d1 = page_of(1);
+            fetch(raw, d0, 0);
+            if (!keys) look(raw, d0, 0);
+        }
+        for (int it = -1; it < count && count > 0; ++it) {
             // Step it's fragments are written, step it + 1's words are looked
-            // at, and no wave reads step it - 1 any more.
-            __syncthreads();
+            // at, and no wave reads step it - 1 any more.  __syncthreads()
+            // would wait for the global loads in flight too.
+            lds_barrier();
             float next_up = up, f = 1.0f;
             if (it + 1 < count) {
                 const uint32_t big = uniform((int)most[(it + 1) % 3]);
@@ -1218,10 +1243,13 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
                 most[it % 3] = 0;        // for step it + 3, looked at after the next barrier
                 bad[(it + 3) % 4] = 0;   // step it - 1's, for step it + 3
             }
-            unpack(raw, it + 1, next_up);
-            fetch(raw, d1, it + 2);
-            d0 = d1;
-            d1 = ids_of(it + 3);
+            // Waves that share a SIMD unpack before and after their products,
+            // so that one's products meet the other's arithmetic.
+            const int32_t d2 = page_of(it + 3);
+            if (!keys) {
+                unpack(raw, it + 1, next_up);
+                fetch(raw, d1, it + 2);
+            }
             if (it >= 0) {
                 const half8_t *buf = (const half8_t *)(lds + (it & 1) * P::kBuf);
                 const uint8_t *scales = lds + 2 * P::kBuf + it % 3 * P::kScale;
@@ -1233,31 +1261,39 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
                     if (token0 > p1 || (a.window > 0 && (int64_t)token0 + 31 + a.window <= p0 && token0 >= a.sinks)) continue;
                     const bool some = gone || token0 + 32 > w.len || token0 + 31 > p0 ||
                                       !(a.window <= 0 || (int64_t)token0 + a.window > p1 || token0 + 32 <= a.sinks);
-                    // scores
-                    float4_t sc[NT][2];
+                    // scores: all products, then the scales
+                    float4_t sc[NT][2], c[NT][2][R];
                     uint32_t ks[2][2 * R];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) read_words(ks[i], scales + 2 * R * (32 * sub + 16 * i + 4 * g));
+                    const half8_t *k = buf + sub * 4 * R * 64 + lane;  // [tile][block][h]
 #pragma unroll
-                    for (int y = 0; y < R; ++y) {
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const half8_t *k = buf + ((2 * sub + i) * 2 * R + 2 * y) * 64 + lane;
-                            const half8_t k0 = k[0], k1 = k[64];
-                            float4_t c[NT];
+                        for (int i = 0; i < 2; ++i)
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                c[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, q[n][2 * y], (float4_t){0, 0, 0, 0}, 0, 0, 0);
+                            for (int y = 0; y < R; ++y) {
+                                const half8_t kk = k[(i * 2 * R + 2 * y + h) * 64];
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                c[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, q[n][2 * y + 1], c[n], 0, 0, 0);
+                                for (int n = 0; n < NT; ++n)
+                                    c[n][i][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                                        kk, q[n][2 * y + h], h ? c[n][i][y] : (float4_t){0, 0, 0, 0}, 0, 0, 0);
+                            }
+                    // the first half of the values on their way meanwhile
+                    const half8_t *v = buf + (P::kFrags + sub * R * 4) * 64 + lane;
+                    half8_t vv[4];
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
+                    for (int i = 0; i < 4; ++i) vv[i] = v[i * 64];
+                    keep_order();
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int y = 0; y < R; ++y)
 #pragma unroll
                                 for (int j = 0; j < 4; ++j)
-                                    sc[n][i][j] = __builtin_fmaf(c[n][j], half_at(ks[i], R * j + y), y == 0 ? 0.0f : sc[n][i][j]);
-                        }
-                    }
+                                    sc[n][i][j] = __builtin_fmaf(c[n][i][y][j], half_at(ks[i], R * j + y), y == 0 ? 0.0f : sc[n][i][j]);
                     if (some) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
@@ -1272,42 +1308,61 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
                         }
                     }
                     // weights
-                    half8_t p[NT];
+                    float mx[NT], more = kLowest;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        float mx = max3(sc[n][0][0], sc[n][0][1], sc[n][0][2]);
-                        mx = max3(mx, sc[n][0][3], sc[n][1][0]);
-                        mx = max3(mx, sc[n][1][1], sc[n][1][2]);
-                        mx = group_max(max2(mx, sc[n][1][3]));
-                        if (__ballot(mx > m[n] + a.slack)) {
-                            const float s = mx > m[n] ? __builtin_amdgcn_exp2f((m[n] - mx) * a.c2) : 1.0f;
-                            m[n] = max2(m[n], mx);
+                        mx[n] = max3(sc[n][0][0], sc[n][0][1], sc[n][0][2]);
+                        mx[n] = max3(mx[n], sc[n][0][3], sc[n][1][0]);
+                        mx[n] = max3(mx[n], sc[n][1][1], sc[n][1][2]);
+                        mx[n] = max2(mx[n], sc[n][1][3]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mx[n] = group_max(mx[n]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) more = max2(more, mx[n] - m[n]);
+                    if (__ballot(more > a.slack)) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const float s = mx[n] > m[n] ? __builtin_amdgcn_exp2f((m[n] - mx[n]) * a.c2) : 1.0f;
+                            m[n] = max2(m[n], mx[n]);
                             l[n] *= s;
 #pragma unroll
                             for (int y = 0; y < R; ++y)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) o[n][y][i] *= s;
                         }
+                    }
+                    half8_t p[NT];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
                         const float mm = kBias - m[n] * a.c2;
                         float sum = 0.0f;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const float v = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][j >> 2][j & 3], a.c2, mm));
-                            sum += v;
-                            p[n][j] = (_Float16)v;
+                            const float x2 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][j >> 2][j & 3], a.c2, mm));
+                            sum += x2;
+                            p[n][j] = (_Float16)x2;
                         }
                         l[n] += sum;
                     }
                     // values
 #pragma unroll
-                    for (int y = 0; y < R; ++y)
+                    for (int y = 0; y < R; ++y) {
+                        half8_t next[4];
+                        if (y + 1 < R) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const half8_t v = buf[(P::kFrags + (sub * R + y) * 4 + i) * 64 + lane];
+                            for (int i = 0; i < 4; ++i) next[i] = v[(4 * y + 4 + i) * 64];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
-                                o[n][y][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[n], o[n][y][i], 0, 0, 0);
+                                o[n][y][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv[i], p[n], o[n][y][i], 0, 0, 0);
+                        if (y + 1 < R) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) vv[i] = next[i];
                         }
+                    }
                 }
             }
             if (f != 1.0f) {
@@ -1319,29 +1374,55 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
                         for (int i = 0; i < 4; ++i) o[n][y][i] *= f;
             }
             up = next_up;
-            look(raw, d0, it + 2);
+            if (!keys) {
+                look(raw, d1, it + 2);
+            } else {
+                look(raw, d0, it + 1);
+                unpack(raw, it + 1, 0.0f);
+                fetch(raw, d1, it + 2);
+            }
+            d0 = d1;
+            d1 = d2;
         }
 
         const float down = 1.0f / up;
         const int part_at = 2 * (int)blockIdx.x + (item.s0 == 0 ? 1 : 0);
-        float4_t *part = (float4_t *)(a.part + (int64_t)part_at * P::kPart);
+        if (item.cut) {
+            float4_t *part = (float4_t *)(a.part + (int64_t)part_at * P::kPart);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const float all_l = group_sum(l[n]);
-            const float f = item.cut ? down : all_l > 0.0f ? down / all_l : 0.0f;
-            const int at = row0 + 16 * n + r, i = at / a.group;
-            const bool live = at < rows;
-            uint16_t *out = a.out + (w.q0 + i) * a.ldo + (int64_t)(head * a.group + at - i * a.group) * D;
+            for (int n = 0; n < NT; ++n) {
+                const float all_l = group_sum(l[n]);
+                if (row0 + 16 * n + r < rows) {
 #pragma unroll
-            for (int y = 0; y < 4 * R; ++y) {
-                const float4_t v = o[n][y >> 2][y & 3] * f;
-                if (item.cut) {
-                    if (live) part[((wave * NT + n) * 4 * R + y) * 64 + lane] = v;
-                } else {
-                    store_row(live ? out : nullptr, v, y >> 2, y & 3, g);
+                    for (int y = 0; y < 4 * R; ++y) part[((wave * NT + n) * 4 * R + y) * 64 + lane] = o[n][y >> 2][y & 3] * down;
+                    if (g == 0) a.part_ml[(int64_t)part_at * kRows + (wave * NT + n) * 16 + r] = make_float2(m[n], all_l);
                 }
             }
-            if (item.cut && g == 0) a.part_ml[(int64_t)part_at * kRows + (wave * NT + n) * 16 + r] = make_float2(m[n], all_l);
+            continue;
+        }
+        // By way of LDS into whole rows: a wave's rows lie where the
+        // fragments were, a row's 16-byte pieces permuted by its number.
+        lds_barrier();
+        uint8_t *mine = lds + wave * (16 * NT * 2 * D);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float all_l = group_sum(l[n]), f = all_l > 0.0f ? down / all_l : 0.0f;
+#pragma unroll
+            for (int y = 0; y < 4 * R; ++y)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int word = 8 * (y >> 2) + 4 * (g & 1) + j + (g & 2);  // piece of the row
+                    *(uint32_t *)(mine + (16 * n + r) * 2 * D + 16 * (word ^ (r & (D / 8 - 1))) + 4 * (y & 3)) =
+                        row_pair(o[n][y >> 2][y & 3] * f, j);
+                }
+        }
+        asm volatile("" ::: "memory");  // a wave reads what it wrote itself
+#pragma unroll
+        for (int y = 0; y < 16 * NT * D / 8; y += 64) {
+            const int at = (y + lane) / (D / 8), c = (y + lane) % (D / 8), row_at = row0 + at, i = row_at / a.group;
+            const uint4 v = *(const uint4 *)(mine + at * 2 * D + 16 * (c ^ (at & 15 & (D / 8 - 1))));
+            if (row_at < rows)
+                *(uint4 *)(a.out + (w.q0 + i) * a.ldo + (int64_t)(head * a.group + row_at - i * a.group) * D + 8 * c) = v;
         }
     }
 }
@@ -1353,7 +1434,7 @@ template <int D, int W>
 __global__ __launch_bounds__(64 * W) void kv4_join(AttnArgs a, int groups)
 {
     constexpr int R = D / 64, F = W / 4;  // F: waves that share a product's parts
-    constexpr int kAt = 4 * W;            // parts at a time
+    constexpr int kDeep = 16, kAt = F * kDeep;  // parts of a wave, and in all, at a time
     __shared__ float4_t frag[W][64];
     __shared__ float2 ml[kAt][16];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
@@ -1368,9 +1449,9 @@ __global__ __launch_bounds__(64 * W) void kv4_join(AttnArgs a, int groups)
     // each wave takes its share of the parts for its product, and the rows'
     // (m, l) come one a thread
     for (int j0 = 0; j0 < parts; j0 += kAt) {
-        float4_t v[16];
+        float4_t v[kDeep];
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
+        for (int x = 0; x < kDeep; ++x) {
             const int j = j0 + (wave >> 2) + F * x;
             v[x] = (float4_t){0, 0, 0, 0};
             if (j < parts) v[x] = ((const float4_t *)a.part)[(part(j) * groups + n) * 4 * R * 64 + (4 * y + i) * 64 + lane];
@@ -1388,7 +1469,7 @@ __global__ __launch_bounds__(64 * W) void kv4_join(AttnArgs a, int groups)
         o *= f;
         for (int j2 = g; j2 < kAt; j2 += 4) l += ml[j2][r].y * __builtin_amdgcn_exp2f((ml[j2][r].x - top) * a.c2);
 #pragma unroll
-        for (int x2 = 0; x2 < 16; ++x2)
+        for (int x2 = 0; x2 < kDeep; ++x2)
             if (j0 + (wave >> 2) + F * x2 < parts)
                 o += v[x2] * __builtin_amdgcn_exp2f((ml[(wave >> 2) + F * x2][r].x - top) * a.c2);
         m = top;
@@ -1578,7 +1659,7 @@ extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, i
     a.sinks = sinks;
     a.workers = t.workers;
     a.whole = t.whole;
-    a.over = t.rg == kWaves ? 4 : 32;
+    a.over = t.rg == kWaves ? 6 : 32;
     a.negate = scale < 0.0f;
     // Not 0: a masked score is -inf, whose product with c2 has to stay so.
     a.c2 = __builtin_fmaxf(__builtin_fabsf(scale) * 1.4426950408889634f, 0x1p-100f);
