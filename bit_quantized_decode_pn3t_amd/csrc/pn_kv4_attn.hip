@@ -1027,7 +1027,9 @@ template <int D, int NT> struct Prompt {
     static constexpr int kFrags = kWide / 16 * 2 * R;       // of K: [tile][block][h]; of V: [32 tokens][block][product], as many
     static constexpr int kBuf = 2 * kFrags * 1024;          // one step's K and V
     static constexpr int kScale = kWide * R * 2;            // K's scales of a step: [token][block] fp16
-    static constexpr int kLds = 2 * kBuf + 3 * kScale;
+    static constexpr int kOut = kRows * 2 * D;              // the rows on their way out, where the fragments were
+    static constexpr int kSteps = 2 * kBuf + 3 * kScale;
+    static constexpr int kLds = kSteps > kOut ? kSteps : kOut;
     static constexpr int kPart = kWaves * NT * 4 * R * 256; // floats of a part
     static constexpr int kUnits = 2 * D;                    // 16-byte units of a step's key codes, and of its value codes
 };
@@ -1489,7 +1491,7 @@ __global__ __launch_bounds__(64 * W) void kv4_join(AttnArgs a, int groups)
 }
 
 // 16-row groups of a prompt's waves.
-template <int D> constexpr int kPromptRows = 2;
+template <int D> constexpr int kPromptRows = D == 64 ? 4 : 2;
 
 // How a call is cut.
 struct Cut {
