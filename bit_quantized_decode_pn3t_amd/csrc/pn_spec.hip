@@ -11,11 +11,14 @@
 //
 // Only one target row and one draft row of each request are read whole: the
 // bytes are B * V * 8.  Kernel spec_sums cuts a row into chunks, one
-// workgroup a chunk, and leaves each chunk's sum (and whether p itself has to
-// serve, in a second sum); every workgroup finds the row by itself from the
-// few gathered probabilities.  Kernel spec_pick, one workgroup a request,
-// finds the chunk that holds the border from the sums, then the index within
-// it.  A workgroup of one launch never waits for another.
+// workgroup a chunk with all of its loads in flight at once, and leaves each
+// chunk's sum of r and of p (which serves where nothing of r is left); every
+// workgroup finds the row by itself from the few gathered probabilities, and
+// the first chunk's notes how many drafts stand.  Kernel spec_pick, one
+// workgroup a request, finds the chunk that holds the border from the sums
+// (every wave for itself), then the index within it: two rounds of loads and
+// two barriers, because with few requests latency is all there is.  A
+// workgroup of one launch never waits for another.
 #include "pn_kv4.h"
 
 using namespace pn::host;
@@ -31,6 +34,7 @@ struct SpecArgs {
     const int32_t *tokens, *n_draft;
     int32_t *out, *accepted;
     double *sums;  // [B][chunks][2]: of r, of p
+    int32_t *took; // [B]: drafts that stand
     int64_t ldt, ldd, ld_tok, ldu, ld_out, V;
     int32_t k, chunks;
 };
@@ -52,12 +56,16 @@ struct Row {
     }
 };
 
-// Every wave computes this alike: lane j tests draft j.
-__device__ __forceinline__ Row find_row(const SpecArgs &a, int b, int lane)
+// Drafts of request b that are tested.
+__device__ __forceinline__ int drafts(const SpecArgs &a, int b)
 {
-    int n = a.n_draft ? a.n_draft[b] : a.k;
-    n = n < 0 ? 0 : n > a.k ? a.k : n;
-    int took = n;
+    const int n = a.n_draft ? a.n_draft[b] : a.k;
+    return n < 0 ? 0 : n > a.k ? a.k : n;
+}
+
+// How many of them stand.  Every wave computes this alike: lane j tests draft j.
+__device__ __forceinline__ int standing(const SpecArgs &a, int b, int n, int lane)
+{
     for (int j0 = 0; j0 < n; j0 += 64) {
         const int j = j0 + lane;
         bool ok = true;
@@ -71,11 +79,14 @@ __device__ __forceinline__ Row find_row(const SpecArgs &a, int b, int lane)
             }
         }
         const uint64_t bad = __ballot(!ok);
-        if (bad) {
-            took = j0 + __builtin_ctzll(bad);
-            break;
-        }
+        if (bad) return j0 + __builtin_ctzll(bad);
     }
+    return n;
+}
+
+// The row that a request with `took` of n drafts standing draws from.
+__device__ __forceinline__ Row row_of(const SpecArgs &a, int b, int n, int took)
+{
     Row row;
     row.accepted = took;
     row.p = a.target + ((int64_t)b * (a.k + 1) + took) * a.ldt;
@@ -84,137 +95,148 @@ __device__ __forceinline__ Row find_row(const SpecArgs &a, int b, int lane)
     return row;
 }
 
-// Sum over the workgroup, in every thread.
-__device__ __forceinline__ double block_sum(double v, double *part, int lane, int wave)
-{
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
-    __syncthreads();
-    if (lane == 0) part[wave] = v;
-    __syncthreads();
-    v = 0.0;
-    for (int w = 0; w < kWaves; ++w) v += part[w];
-    return v;
-}
+// Four entries at once from a row that need only be aligned to one.
+typedef float float4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+
+constexpr int kEach = kChunk / kThreads;  // entries of a thread
 
 __global__ __launch_bounds__(kThreads) void spec_sums(SpecArgs a)
 {
     __shared__ double part[kWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b = blockIdx.y;
-    const Row row = find_row(a, b, lane);
+    const int n = drafts(a, b);
+    const Row row = row_of(a, b, n, standing(a, b, n, lane));
     const int64_t lo = (int64_t)blockIdx.x * kChunk, hi = lo + kChunk < a.V ? lo + kChunk : a.V;
     double sr = 0.0, sp = 0.0;
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
-        sr += (double)row.r(i);
-        sp += (double)clean(row.p[i]);
+    if (hi - lo == kChunk) {
+        float4_a4 p[kEach / 4], q[kEach / 4] = {};
+#pragma unroll
+        for (int i = 0; i < kEach / 4; ++i) p[i] = *(const float4_a4 *)(row.p + lo + 4 * (threadIdx.x + kThreads * i));
+        if (row.q) {
+#pragma unroll
+            for (int i = 0; i < kEach / 4; ++i) q[i] = *(const float4_a4 *)(row.q + lo + 4 * (threadIdx.x + kThreads * i));
+        }
+#pragma unroll
+        for (int i = 0; i < kEach / 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool drop = lo + 4 * (threadIdx.x + kThreads * i) + e == row.drop;
+                sr += drop ? 0.0 : (double)clean(row.q ? p[i][e] - q[i][e] : p[i][e]);
+                sp += (double)clean(p[i][e]);
+            }
+    } else {
+        for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
+            sr += (double)row.r(i);
+            sp += (double)clean(row.p[i]);
+        }
     }
-    sr = block_sum(sr, part, lane, wave);
-    sp = block_sum(sp, part, lane, wave);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        sr += __shfl_xor(sr, d, 64);
+        sp += __shfl_xor(sp, d, 64);
+    }
+    __shared__ double part_p[kWaves];
+    if (lane == 0) part[wave] = sr, part_p[wave] = sp;
+    __syncthreads();
     if (threadIdx.x == 0) {
+        sr = sp = 0.0;
+        for (int w = 0; w < kWaves; ++w) sr += part[w], sp += part_p[w];
         double *s = a.sums + 2 * ((int64_t)b * a.chunks + blockIdx.x);
         s[0] = sr;
         s[1] = sp;
+        if (blockIdx.x == 0) a.took[b] = row.accepted;
     }
 }
 
-// Exclusive prefix of v over the workgroup.
-__device__ __forceinline__ double block_before(double v, double *part, int lane, int wave)
+// Inclusive prefix over the wave.
+__device__ __forceinline__ double wave_prefix(double x, int lane)
 {
-    double x = v;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const double y = __shfl_up(x, d, 64);
         if (lane >= d) x += y;
     }
-    __syncthreads();
-    if (lane == 63) part[wave] = x;
-    __syncthreads();
-    double before = 0.0;
-    for (int w = 0; w < wave; ++w) before += part[w];
-    const double up = __shfl_up(x, 1, 64);
-    return lane == 0 ? before : before + up;
+    return x;
 }
 
 __global__ __launch_bounds__(kThreads) void spec_pick(SpecArgs a)
 {
     __shared__ double part[kWaves];
-    __shared__ int64_t found;
-    __shared__ double before_found;
-    __shared__ int64_t last;
+    __shared__ int32_t found, last;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.x;
-    Row row = find_row(a, b, lane);
     const double *s = a.sums + 2 * (int64_t)b * a.chunks;
+    const int n = drafts(a, b), took = a.took[b];
+    const double u = a.u[b * a.ldu + a.k];
+    Row row = row_of(a, b, n, took);
+    for (int j = tid; j <= a.k; j += kThreads)
+        if (j != took) a.out[b * a.ld_out + j] = j < took ? a.tokens[b * a.ld_tok + j] : -1;
+    if (tid == 0) a.accepted[b] = took, found = INT32_MAX, last = -1;
 
+    // the sums' totals, as every wave for itself
     double sr = 0.0, sp = 0.0;
-    for (int c = tid; c < a.chunks; c += kThreads) {
-        sr += s[2 * c];
-        sp += s[2 * c + 1];
-    }
-    double total = block_sum(sr, part, lane, wave);
+    for (int c = lane; c < a.chunks; c += 64) sr += s[2 * c], sp += s[2 * c + 1];
     int which = 0;
+    double total = __shfl(wave_prefix(sr, lane), 63, 64);
     if (!(total > 0.0)) {  // nothing left of p - q: p itself
-        total = block_sum(sp, part, lane, wave);
+        total = __shfl(wave_prefix(sp, lane), 63, 64);
         which = 1;
         row.q = nullptr;
         row.drop = -1;
     }
-    const double goal = (double)a.u[b * a.ldu + a.k] * total;
+    const double goal = u * total;
 
     // first chunk whose end is above the goal; without one (u >= 1), the last chunk with anything in it
-    if (tid == 0) found = INT64_MAX, last = -1;
-    __syncthreads();
-    double base = 0.0;
-    for (int c0 = 0; c0 < a.chunks; c0 += kThreads) {
-        const int c = c0 + tid;
-        const double v = c < a.chunks ? s[2 * c + which] : 0.0;
-        const double before = base + block_before(v, part, lane, wave);
-        const bool hit = v > 0.0 && before + v > goal;
-        if (hit) atomicMin((unsigned long long *)&found, (unsigned long long)c);
-        if (v > 0.0) atomicMax((long long *)&last, (long long)c);
-        __syncthreads();
-        if (hit && found == c) before_found = before;
-        if (v > 0.0 && found == INT64_MAX && last == c) before_found = before;
-        base += block_sum(v, part, lane, wave);
-        if (found != INT64_MAX) break;
-    }
-    __syncthreads();
-    const int64_t chunk = found != INT64_MAX ? found : last;
-    int32_t token = -1;
-    if (chunk >= 0) {  // the same for the whole workgroup
-        base = before_found;
-        __syncthreads();
-        if (tid == 0) found = INT64_MAX, last = -1;
-        __syncthreads();
-        const int64_t lo = chunk * kChunk, hi = lo + kChunk < a.V ? lo + kChunk : a.V;
-        constexpr int kEach = kChunk / kThreads;  // consecutive entries of a thread
-        float v[kEach];
-        double sum = 0.0;
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-            const int64_t i = lo + tid * kEach + e;
-            v[e] = i < hi ? row.r(i) : 0.0f;
-            sum += (double)v[e];
+    int chunk = -1;
+    double base = 0.0, run = 0.0;
+    for (int c0 = 0; c0 < a.chunks; c0 += 64) {
+        const double v = c0 + lane < a.chunks ? s[2 * (c0 + lane) + which] : 0.0;
+        const double end = run + wave_prefix(v, lane);
+        const uint64_t hit = __ballot(v > 0.0 && end > goal), any = __ballot(v > 0.0);
+        if (hit || any) {
+            const int l = hit ? __builtin_ctzll(hit) : 63 - __builtin_clzll(any);
+            chunk = c0 + l;
+            base = l ? __shfl(end, l - 1, 64) : run;
         }
-        double run = base + block_before(sum, part, lane, wave);
-        int64_t mine = INT64_MAX, end = -1;
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-            run += (double)v[e];
-            const int64_t i = lo + tid * kEach + e;
-            if (v[e] > 0.0f) {
-                end = i;
-                if (run > goal && mine == INT64_MAX) mine = i;
-            }
-        }
-        if (mine != INT64_MAX) atomicMin((unsigned long long *)&found, (unsigned long long)mine);
-        if (end >= 0) atomicMax((long long *)&last, (long long)end);
-        __syncthreads();
-        // Rounding may leave the chunk's own last prefix at the goal: its last entry then.
-        token = (int32_t)(found != INT64_MAX ? found : last);
+        if (hit) break;
+        run = __shfl(end, 63, 64);
     }
-    for (int j = tid; j <= a.k; j += kThreads)
-        a.out[b * a.ld_out + j] = j < row.accepted ? a.tokens[b * a.ld_tok + j] : j == row.accepted ? token : -1;
-    if (tid == 0) a.accepted[b] = row.accepted;
+    if (chunk < 0) {  // nothing counts; the same in every wave
+        if (tid == 0) a.out[b * a.ld_out + took] = -1;
+        return;
+    }
+
+    const int64_t lo = (int64_t)chunk * kChunk, hi = lo + kChunk < a.V ? lo + kChunk : a.V;
+    const int64_t at = lo + tid * kEach;
+    float v[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) v[e] = at + e < hi ? row.r(at + e) : 0.0f;
+    double sum = 0.0;
+    int32_t end = -1;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        sum += (double)v[e];
+        if (v[e] > 0.0f) end = (int32_t)(at + e);
+    }
+    const double mine = wave_prefix(sum, lane);
+    if (lane == 63) part[wave] = mine;
+    __syncthreads();
+    double before = base;
+    for (int w = 0; w < wave; ++w) before += part[w];
+    // this thread's entries, one after another
+    const double up = __shfl_up(mine, 1, 64);
+    double x = lane ? before + up : before;
+    int32_t first = -1;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        x += (double)v[e];
+        if (v[e] > 0.0f && x > goal && first < 0) first = (int32_t)(at + e);
+    }
+    const uint64_t hit = __ballot(first >= 0), any = __ballot(end >= 0);
+    if (hit && lane == (int)__builtin_ctzll(hit)) atomicMin(&found, first);
+    if (any && lane == 63 - (int)__builtin_clzll(any)) atomicMax(&last, end);
+    __syncthreads();
+    // Rounding may leave the chunk's own last prefix at the goal: its last entry then.
+    if (tid == 0) a.out[b * a.ld_out + took] = found < INT32_MAX ? found : last;
 }
 
 int chunks_of(int64_t V) { return (int)((V + kChunk - 1) / kChunk); }
@@ -224,7 +246,7 @@ int chunks_of(int64_t V) { return (int)((V + kChunk - 1) / kChunk); }
 extern "C" size_t pn_spec_workspace(int B, int64_t V)
 {
     if (B < 1 || V < 1 || V > INT32_MAX) return 0;
-    return (size_t)B * chunks_of(V) * 2 * sizeof(double);
+    return (size_t)B * (chunks_of(V) * 2 * sizeof(double) + sizeof(double));
 }
 
 extern "C" pn_status pn_spec_verify(const float *target, int64_t ldt, const float *draft, int64_t ldd,
@@ -242,8 +264,9 @@ extern "C" pn_status pn_spec_verify(const float *target, int64_t ldt, const floa
     if (!aligned(ws, 8)) return PN_EALIGN;
     if (B > 65535 || k > 1024 || V > INT32_MAX) return PN_EUNSUPPORTED;
     if (ws_bytes < pn_spec_workspace(B, V)) return PN_ESHAPE;
-    const SpecArgs a = {target, draft, u, tokens, n_draft, out, accepted, (double *)ws, ldt, ldd, ld_tok, ldu, ld_out,
-                        V, k, chunks_of(V)};
+    const SpecArgs a = {target, draft, u, tokens, n_draft, out, accepted, (double *)ws,
+                        (int32_t *)((double *)ws + (size_t)B * chunks_of(V) * 2), ldt, ldd, ld_tok, ldu, ld_out, V, k,
+                        chunks_of(V)};
     const hipStream_t s = (hipStream_t)stream;
     hipLaunchKernelGGL(spec_sums, dim3((unsigned)a.chunks, (unsigned)B), dim3(kThreads), 0, s, a);
     if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
