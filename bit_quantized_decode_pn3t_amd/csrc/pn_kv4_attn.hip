@@ -19,8 +19,8 @@
 //                 (scale times code) are rounded once each to fp16, half a
 //                 step, 2^-11 relative: with the scale in the weights instead
 //                 the codes would be exact, but each block of the head then
-//                 needs weights of its own, and 64 rows of two blocks spend a
-//                 sixth more instructions on that than on 32 products.
+//                 needs weights of its own (32 query heads, a prompt of 4096,
+//                 128 wide: 0.60 ms that way and 0.51 this way, in kv4_attn).
 //                 Neither factor leaves fp16's full precision: the running
 //                 maximum m follows only scores that pass it by 4 (in log2),
 //                 so that O is rarely scaled, and weights carry 2^10: they
@@ -64,7 +64,15 @@ constexpr int kWaves = 8;
 constexpr int kStep = 32;          // tokens of a step
 constexpr float kLowest = -1e30f;  // a maximum before any score
 constexpr float kBias = 10.0f;     // weights carry 2^kBias
-constexpr int kShare = 16;         // steps of a workgroup at least
+// Steps of a workgroup at least.  One 256-wide token over 8000 keys of two
+// heads: 22 us, with 32 27 us; 256 tokens over up to 1024 keys: 81 us, with 4
+// 86 us.
+constexpr int kShare = 16;
+// And of each of two on a compute unit, else one takes the steps of both.
+// 64 wide, 4 key-value heads: one token over 65536 keys (16 steps each) 29 us
+// with two, 22 with one; 24 requests of up to 16384 (48) 31 and 32; 64 of them
+// (128) 54 and 61.
+constexpr int kTwo = 48;
 constexpr int kNothing = (int)0x80000000;  // an offset past every buffer: reads zero
 
 struct AttnArgs {
@@ -79,6 +87,7 @@ struct AttnArgs {
     int64_t max_q, max_kv;
     int32_t q_heads, group, B, max_pages, window, sinks;
     int32_t workers, whole;  // workgroups; whole: items are not cut
+    int32_t two;             // of the workgroups share a compute unit
     int32_t over;            // what an item's start and end cost, in steps
     int32_t negate;          // scale < 0: the queries are negated
     float c2;                // |scale| log2(e), above 0
@@ -267,7 +276,9 @@ __device__ __forceinline__ bool line_part(const AttnArgs &a, LineLds &s, Line &t
     total = uniform64(total);
     // A few workgroups fewer than there are: with four items or more no item
     // then has over 64 parts, which is what the join takes at a time.
-    const int32_t dealt = a.workers - a.workers / 64;
+    // Two workgroups a compute unit only share it: with short parts one does more.
+    const int32_t used = a.two && total < (int64_t)a.workers * (kTwo * kUnit) ? a.workers / 2 : a.workers;
+    const int32_t dealt = used - used / 64;
     t.share = quotient(total + dealt - 1, dealt);
     if (t.share < kShare * kUnit && !a.whole) t.share = kShare * kUnit;
     t.lo = blockIdx.x * t.share;
@@ -817,7 +828,9 @@ template <int D, int NT, int RG> struct Shape {
     static constexpr int kPart = RG * NT * 4 * G::R * 256;
 };
 
-// Two workgroups share a compute unit where registers and LDS allow it.
+// Two workgroups share a compute unit where registers and LDS allow it (64
+// requests of up to 16384 tokens, 64 wide: 54 us, one a unit 61 us; 128 wide
+// 73 and 80 us).
 template <int D, int NT, int RG> constexpr int waves_per_simd() { return D < 256 && NT == 1 && RG == 1 ? 4 : 2; }
 
 template <int D, int NT, int RG>
@@ -1490,13 +1503,16 @@ __global__ __launch_bounds__(64 * W) void kv4_join(AttnArgs a, int groups)
     }
 }
 
-// 16-row groups of a prompt's waves.
+// 16-row groups of a prompt's waves.  64 wide: two would do for the registers'
+// sake but give each unpacked step half the work (16 heads, a prompt of 4096:
+// 104 us with four, 118 with two); 128 wide has registers for two.
 template <int D> constexpr int kPromptRows = D == 64 ? 4 : 2;
 
 // How a call is cut.
 struct Cut {
     int nt, rg;   // 16-row groups of a wave, row groups of a workgroup
     int workers;
+    bool two;     // of them a compute unit
     bool whole;
     size_t part;  // bytes that one workgroup's parts and record need
 };
@@ -1507,14 +1523,22 @@ Cut cut(const pn_kv4_cache *c, int q_heads, int64_t max_q, int64_t max_kv, int w
     const int64_t rows = max_q * (q_heads / c->heads);
     const int most = c->dim == 256 ? 2 : 4;  // that the registers hold
     t.nt = rows >= 16 * most ? most : (int)((rows + 15) / 16);
-    t.rg = rows > 32 * most ? c->dim == 256 ? 4 : kWaves : 1;
+    // A prompt's workgroup pays for its whole row tile; up to one tile's rows
+    // the kernel of few rows is faster, each 16 nt rows a tile of its own and
+    // the keys read again for each.  8 requests over 4096 keys: 64 wide, 512
+    // rows 78 us either way, 192 rows 43 (prompt kernel 58), 768 rows 98
+    // (86); 128 wide, 256 rows 67 (68), 192 rows 57 (65), 384 rows 88 (75);
+    // 256 wide, 96 rows 63 (66), 256 rows 115 (106).
+    const int tile = c->dim == 256 ? 128 : 16 * kWaves * (c->dim == 128 ? kPromptRows<128> : kPromptRows<64>);
+    t.rg = rows > tile ? c->dim == 256 ? 4 : kWaves : 1;
     if (t.rg == kWaves) t.nt = c->dim == 128 ? kPromptRows<128> : kPromptRows<64>;
     int64_t keys = max_kv;
     if (window > 0) {
         const int64_t reach = (int64_t)window + max_q + sinks + 2 * kStep;
         if (reach < keys) keys = reach;
     }
-    t.workers = device_cus() * (c->dim < 256 && t.nt == 1 ? 2 : 1);
+    t.two = c->dim < 256 && t.nt == 1;
+    t.workers = device_cus() * (t.two ? 2 : 1);
     t.whole = keys <= 2 * kShare * kStep;
     const size_t groups = t.rg * t.nt;
     t.part = 2 * groups * (c->dim * 16 * sizeof(float) + 16 * sizeof(float2)) + sizeof(Cutoff);
@@ -1660,7 +1684,11 @@ extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, i
     a.window = window;
     a.sinks = sinks;
     a.workers = t.workers;
+    a.two = t.two;
     a.whole = t.whole;
+    // What an item's start and end cost in steps.  64 wide, 64 requests of up
+    // to 16384: 54 us, counted as nothing 80, twice as much 57; 128 wide, a
+    // prompt of 4096 with 16 heads: 149 us, nothing 185, twice 162.
     a.over = t.rg == kWaves ? 6 : 32;
     a.negate = scale < 0.0f;
     // Not 0: a masked score is -inf, whose product with c2 has to stay so.
