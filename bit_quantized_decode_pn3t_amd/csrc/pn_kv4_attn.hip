@@ -19,7 +19,7 @@
 //                 (scale times code) are rounded once each to fp16, half a
 //                 step, 2^-11 relative: with the scale in the weights instead
 //                 the codes would be exact, but each block of the head then
-//                 needs weights of its own (32 query heads, a prompt of 4096,
+//                 needs weights of its own (48 query heads, a prompt of 4096,
 //                 128 wide: 0.60 ms that way and 0.51 this way, in kv4_attn).
 //                 Neither factor leaves fp16's full precision: the running
 //                 maximum m follows only scores that pass it by 4 (in log2),
@@ -88,6 +88,7 @@ struct AttnArgs {
     int32_t q_heads, group, B, max_pages, window, sinks;
     int32_t workers, whole;  // workgroups; whole: items are not cut
     int32_t two;             // of the workgroups share a compute unit
+    int32_t parts;           // that an item is cut into, about
     int32_t over;            // what an item's start and end cost, in steps
     int32_t negate;          // scale < 0: the queries are negated
     float c2;                // |scale| log2(e), above 0
@@ -1443,8 +1444,12 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
 }
 
 // Add the parts of an item that a workgroup left unfinished.  Grid: x =
-// workgroup, y = block, z = 16-row group.  Product i = wave & 3; W = 16 waves
-// take a fourth of the parts each (few rows: many parts), or four all of them.
+// workgroup, y = block, z = 16-row group.  Product i = wave & 3; of W = 4, 8 or
+// 16 waves those of a product share its parts, 16 of them each at a time: many
+// parts take more waves, but those cost where there are many items (256 wide,
+// 4 heads, 16 requests of 8 queries and up to 5000 tokens, 64 items of about
+// 4 parts: 36 us in all with 4 waves, 40 with 8, 49 with 16; one token over
+// 65536 keys, 4 items of 63 parts: this launch 15, 9.5 and 7.9 us).
 template <int D, int W>
 __global__ __launch_bounds__(64 * W) void kv4_join(AttnArgs a, int groups)
 {
@@ -1514,10 +1519,11 @@ struct Cut {
     int workers;
     bool two;     // of them a compute unit
     bool whole;
+    int parts;    // of an item, about, with one workgroup a compute unit
     size_t part;  // bytes that one workgroup's parts and record need
 };
 
-Cut cut(const pn_kv4_cache *c, int q_heads, int64_t max_q, int64_t max_kv, int window, int sinks)
+Cut cut(const pn_kv4_cache *c, int q_heads, int B, int64_t max_q, int64_t max_kv, int window, int sinks)
 {
     Cut t;
     const int64_t rows = max_q * (q_heads / c->heads);
@@ -1540,6 +1546,9 @@ Cut cut(const pn_kv4_cache *c, int q_heads, int64_t max_q, int64_t max_kv, int w
     t.two = c->dim < 256 && t.nt == 1;
     t.workers = device_cus() * (t.two ? 2 : 1);
     t.whole = keys <= 2 * kShare * kStep;
+    const int64_t tile_rows = 16 * t.nt * t.rg, items = (int64_t)B * c->heads * ((rows + tile_rows - 1) / tile_rows);
+    const int64_t longest = keys / (kShare * kStep) + 1;
+    t.parts = (int)(items * longest < device_cus() ? longest : device_cus() / items);
     const size_t groups = t.rg * t.nt;
     t.part = 2 * groups * (c->dim * 16 * sizeof(float) + 16 * sizeof(float2)) + sizeof(Cutoff);
     return t;
@@ -1572,8 +1581,10 @@ pn_status launch(const AttnArgs &a, hipStream_t s)
     hipLaunchKernelGGL((kv4_attn<D, NT, RG>), dim3((unsigned)a.workers), dim3(kThreads), (Shape<D, NT, RG>::kLds), s, a);
     if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
     if (!a.whole) {
-        constexpr int W = RG == 1 ? 16 : 4;
-        hipLaunchKernelGGL((kv4_join<D, W>), dim3((unsigned)a.workers, D / 64, NT * RG), dim3(64 * W), 0, s, a, NT * RG);
+        const dim3 grid((unsigned)a.workers, D / 64, NT * RG);
+        if (RG > 1 || a.parts <= 4) hipLaunchKernelGGL((kv4_join<D, 4>), grid, dim3(256), 0, s, a, NT * RG);
+        else if (a.parts <= 32) hipLaunchKernelGGL((kv4_join<D, 8>), grid, dim3(512), 0, s, a, NT * RG);
+        else hipLaunchKernelGGL((kv4_join<D, 16>), grid, dim3(1024), 0, s, a, NT * RG);
         if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
     }
     return PN_OK;
@@ -1631,7 +1642,7 @@ extern "C" size_t pn_kv4_attn_workspace(const pn_kv4_cache *cache, int q_heads, 
     if (check_cache(cache, &c) || !sizes_ok(cache, q_heads, B, total_q, max_q, max_kv, sinks) || total_q == 0) return 0;
     if (max_q > total_q) max_q = total_q;
     if (!sizes_fit(cache, q_heads, B, total_q, max_q, max_kv)) return 0;
-    const Cut t = cut(cache, q_heads, max_q, max_kv, window, sinks);
+    const Cut t = cut(cache, q_heads, B, max_q, max_kv, window, sinks);
     return t.whole ? 0 : t.workers * t.part;
 }
 
@@ -1654,7 +1665,7 @@ extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, i
     if (max_q > total_q) max_q = total_q;  // no request has more
     if (!sizes_fit(cache, q_heads, B, total_q, max_q, max_kv)) return PN_EUNSUPPORTED;
     if (total_q == 0) return PN_OK;
-    Cut t = cut(cache, q_heads, max_q, max_kv, window, sinks);
+    Cut t = cut(cache, q_heads, B, max_q, max_kv, window, sinks);
     if (!t.whole && ws_bytes < t.workers * t.part) {
         // As many workgroups as there is room for, while that leaves most of
         // the device at work; else every item is one workgroup's.
@@ -1685,6 +1696,7 @@ extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, i
     a.sinks = sinks;
     a.workers = t.workers;
     a.two = t.two;
+    a.parts = t.parts;
     a.whole = t.whole;
     // What an item's start and end cost in steps.  64 wide, 64 requests of up
     // to 16384: 54 us, counted as nothing 80, twice as much 57; 128 wide, a
