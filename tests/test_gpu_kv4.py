@@ -558,3 +558,46 @@ def test_verify_degenerate():
     for d in (draft, None):
         got, want = run_verify(target, d, tokens, None, u), R.verify(target, d, tokens, None, u)
         assert np.array_equal(got[1], want[1]) and np.array_equal(got[0], want[0]), (got, want)
+
+
+# ---- places past 32 bits ----------------------------------------------------
+@pytest.mark.parametrize("dim,q", [(64, 1), (128, 5), (256, 1), (128, 300)])
+def test_far_pages_and_rows(dim, q):
+    """A cache of over 5 GiB, used at its far end, and query rows over
+    6 GiB give what a small cache and dense rows give."""
+    heads, group, page, n = 2, 3, 64, 2
+    q_heads, kv = heads * group, 333
+    per = B.pn_kv4_page_bytes(page, heads, dim)
+    width = -(-kv // page)
+    num = (5 << 30) // per + n * width
+    g = torch.Generator(device="cuda")
+    g.manual_seed(dim + q)
+    k, v = (torch.randn((n * kv, heads * dim), generator=g, device="cuda") for _ in range(2))
+    rows = torch.randn((n * q, q_heads * dim), generator=g, device="cuda").half()
+    pos = torch.arange(kv, device="cuda").repeat(n)
+    outs, loads = [], []
+    far = (3 << 30) // (8 * (n * q - 1)) * 8  # the last row is 6 GiB on
+    for count, first, ld in ((n * width, 0, q_heads * dim), (num, num - n * width, far)):
+        say("far: dim=%d q=%d pages=%d ld=%d" % (dim, q, count, ld))
+        pages = torch.empty(count * per, dtype=torch.uint8, device="cuda")
+        cache = B.KV4Cache(pages, count, page, heads, dim)
+        table = (torch.arange(n * width, device="cuda") + first).int().view(n, width)
+        slots = table.long().repeat_interleave(page, 1)[:, :kv].reshape(-1) * page + pos % page
+        B.pn_kv4_store(cache, n * kv, None, k, v, "f32", 0, heads * dim, heads * dim, q_heads, None, None, 0.0, None,
+                       0, False, pos.int(), slots, None, 0)
+        back = torch.empty((2, n * kv, heads * dim), device="cuda")
+        B.pn_kv4_load(cache, slots, n * kv, back[0], back[1])
+        loads.append(back)
+        flat = torch.empty((n * q - 1) * ld + q_heads * dim, dtype=torch.float16, device="cuda")
+        at = flat.as_strided(rows.shape, (ld, 1))
+        at.copy_(rows)
+        out = torch.empty_like(flat)
+        need = B.pn_kv4_attn_workspace(cache, q_heads, n, n * q, q, kv)
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+        B.pn_kv4_attn(cache, flat, ld, q_heads, i32([0, q, 2 * q]), i32([kv, kv - 20]), table, width, n, n * q, q, kv,
+                      dim ** -0.5, 0, 0, out, ld, ws, need)
+        sync()
+        outs.append(out.as_strided(rows.shape, (ld, 1)).clone())
+    assert torch.equal(loads[0], loads[1])
+    assert outs[0].isfinite().all() and outs[0].abs().max() > 0
+    assert torch.equal(outs[0], outs[1])
