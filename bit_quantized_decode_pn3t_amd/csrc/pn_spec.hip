@@ -19,6 +19,10 @@
 // (every wave for itself), then the index within it: two rounds of loads and
 // two barriers, because with few requests latency is all there is.  A
 // workgroup of one launch never waits for another.
+//
+// 64 requests of 248320 entries: sums 20 us, 6.1 TB/s, of 6.9 that streaming
+// reads reach here; pick 8.0.  One request of 62080: 4.3 and 7.2, launches
+// and a chain of dependent loads.
 #include "pn_kv4.h"
 
 using namespace pn::host;

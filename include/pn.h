@@ -447,7 +447,8 @@ pn_status pn_kv4_load(const pn_kv4_cache *cache, const int64_t *slots, int64_t T
  *              call can use (less means fewer splits).  One workspace serves
  *              calls that follow each other on a stream; calls that may
  *              overlap need their own.
- * PN_EUNSUPPORTED: B > 65535, or heads * row tiles past the grid's limits. */
+ * PN_EUNSUPPORTED: B or q_heads > 65535, total_q or max_kv > 2^30 - 1, or max_q
+ * * q_heads / heads > 2^29 - 1. */
 size_t pn_kv4_attn_workspace(const pn_kv4_cache *cache, int q_heads, int B, int64_t total_q, int64_t max_q,
                              int64_t max_kv, int window, int sinks);
 pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, int64_t ldq, int q_heads, const int32_t *q_start,
