@@ -97,6 +97,7 @@ struct AttnArgs {
     int32_t workers, whole;  // workgroups; whole: items are not cut
     int32_t two;             // of the workgroups share a compute unit
     int32_t parts;           // that an item is cut into, about
+    int32_t queries, grow;   // of a row tile; what a tile's length is more than the last one's (Cost)
     int32_t over;            // what an item's start and end cost, in steps
     int32_t negate;          // scale < 0: the queries are negated
     float c2;                // |scale| log2(e), above 0
@@ -181,16 +182,15 @@ __device__ __forceinline__ Cost cost(const AttnArgs &a, int b, int tile_rows)
     c.tiles = c.base = c.top = c.grow = 0;
     if (c.w.qn < 1) return c;
     c.tiles = (c.w.qn * a.group + tile_rows - 1) / tile_rows;
-    const int queries = (tile_rows + a.group - 1) / a.group;  // of a tile
-    int32_t see = c.w.first + (c.w.qn < queries ? c.w.qn : queries);
+    int32_t see = c.w.first + (c.w.qn < a.queries ? c.w.qn : a.queries);
     see = see < 0 ? 0 : see < c.w.len ? see : c.w.len;
     int32_t most = c.w.len;
-    if (a.window > 0 && (int64_t)a.window + a.sinks + queries < most) most = a.window + a.sinks + queries;
+    if (a.window > 0 && (int64_t)a.window + a.sinks + a.queries < most) most = a.window + a.sinks + a.queries;
     const int32_t fixed = (a.over + 1) * kUnit;
     c.top = fixed + (int32_t)((int64_t)most * kUnit / STEP);
     c.base = fixed + (int32_t)((int64_t)see * kUnit / STEP);
     if (c.base > c.top) c.base = c.top;
-    c.grow = tile_rows * kUnit / (a.group * STEP);
+    c.grow = a.grow;
     return c;
 }
 
@@ -209,6 +209,7 @@ __device__ __forceinline__ int64_t before_tile(const Cost &c, int32_t n, int64_t
 }
 __device__ __forceinline__ int64_t length(const AttnArgs &a, const Cost &c)
 {
+    if (c.tiles == 1) return (int64_t)c.base * a.c.heads;
     return before_tile(c, growing(c), c.tiles) * a.c.heads;
 }
 
@@ -326,41 +327,48 @@ struct Item {
 };
 
 // Steps that a part of an item stands for: the same part of the `steps` it has.
-__device__ __forceinline__ int share_of(int32_t s, int32_t all, int steps) { return uniform((int)quotient((int64_t)s * steps, all)); }
+__device__ __forceinline__ int share_of(int32_t s, int32_t all, int steps)
+{
+    return s == 0 ? 0 : s == all ? steps : uniform((int)quotient((int64_t)s * steps, all));
+}
 
 // Go on along the line from x; false: a stretch without an item's steps.
 template <int STEP>
 __device__ __forceinline__ bool next_item(const AttnArgs &a, const LineLds &s, Line &t, int64_t &x, Item &m, int tile_rows)
 {
     m.c = scalar(t.few ? s.known[t.b] : cost<STEP>(a, t.b, tile_rows));
-    const int32_t n = growing(m.c);
-    const int64_t head_len = before_tile(m.c, n, m.c.tiles);
+    const bool single = m.c.tiles == 1;  // most requests: few instructions, which is what an item's start costs
+    const int32_t n = single ? 0 : growing(m.c);
+    const int64_t head_len = single ? m.c.base : before_tile(m.c, n, m.c.tiles);
     if (x >= t.start + head_len * a.c.heads) {
         t.start += head_len * a.c.heads;
         ++t.b;
         return false;
     }
     m.head = uniform((int)quotient(x - t.start, head_len));
-    const int64_t off = x - t.start - m.head * head_len;
-    // the tile: largest with before_tile <= off
+    int64_t first = t.start + m.head * head_len;  // of the item on the line
+    int one = (int)head_len;
     int32_t tile = 0;
-    const int64_t flat = before_tile(m.c, n, n);
-    if (m.c.tiles == 1) {
-    } else if (off >= flat) {
-        tile = n + (int32_t)quotient(off - flat, m.c.top);
-    } else if (m.c.grow == 0) {
-        tile = (int32_t)quotient(off, m.c.base);
-    } else {
-        const double h = m.c.base - 0.5 * m.c.grow;
-        tile = (int32_t)((__builtin_sqrt(h * h + 2.0 * m.c.grow * (double)off) - h) / m.c.grow);
-        if (tile >= n) tile = n - 1;
-        if (tile < 0) tile = 0;
-        while (tile > 0 && before_tile(m.c, n, tile) > off) --tile;
-        while (tile + 1 < n && before_tile(m.c, n, tile + 1) <= off) ++tile;
+    if (!single) {
+        // the tile: largest with before_tile <= off
+        const int64_t off = x - first, flat = before_tile(m.c, n, n);
+        if (off >= flat) {
+            tile = n + (int32_t)quotient(off - flat, m.c.top);
+        } else if (m.c.grow == 0) {
+            tile = (int32_t)quotient(off, m.c.base);
+        } else {
+            const double h = m.c.base - 0.5 * m.c.grow;
+            tile = (int32_t)((__builtin_sqrt(h * h + 2.0 * m.c.grow * (double)off) - h) / m.c.grow);
+            if (tile >= n) tile = n - 1;
+            if (tile < 0) tile = 0;
+            while (tile > 0 && before_tile(m.c, n, tile) > off) --tile;
+            while (tile + 1 < n && before_tile(m.c, n, tile + 1) <= off) ++tile;
+        }
+        tile = uniform(tile);
+        const int64_t at = before_tile(m.c, n, tile);
+        first += at;
+        one = (int)(before_tile(m.c, n, tile + 1) - at);
     }
-    tile = uniform(tile);
-    const int64_t first = t.start + m.head * head_len + before_tile(m.c, n, tile);  // of the item on the line
-    const int one = (int)(before_tile(m.c, n, tile + 1) - before_tile(m.c, n, tile));
     int s0 = (int)(x - first), s1 = (int)(t.hi - first < one ? t.hi - first : one);
     x = first + s1;
     if (a.whole) {  // items are taken whole, by the workgroup they start in
@@ -434,8 +442,11 @@ __device__ __forceinline__ Pages pages_of(const AttnArgs &a, const int32_t *row,
     Pages t;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+        // (no branch around a load: all of a call's are on their way at once)
         const int at = (step * kStep + 16 * i) >> a.c.shift;
-        t.p[i] = there && at < a.max_pages ? ((const PN_CONST int32_t *)row)[uniform(at)] : -1;
+        const bool in = there && at < a.max_pages;
+        const int32_t p = ((const PN_CONST int32_t *)row)[uniform(in ? at : 0)];
+        t.p[i] = in ? p : -1;
     }
     return t;
 }
@@ -1709,6 +1720,9 @@ extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, i
     a.workers = t.workers;
     a.two = t.two;
     a.parts = t.parts;
+    const int tile_rows = 16 * t.nt * t.rg;
+    a.queries = (tile_rows + a.group - 1) / a.group;
+    a.grow = tile_rows * kUnit / (a.group * (t.rg == kWaves ? kWide : kStep));
     a.whole = t.whole;
     // What an item's start and end cost in steps.  64 wide, 64 requests of up
     // to 16384: 54 us, counted as nothing 80, twice as much 57; 128 wide, a
