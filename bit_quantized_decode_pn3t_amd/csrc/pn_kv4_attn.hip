@@ -887,6 +887,19 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
         const int last = (row0 + 16 * NT < rows ? row0 + 16 * NT : rows) - 1;
         const int32_t p0 = row0 < rows ? w.first + row0 / a.group : -1, p1 = row0 < rows ? w.first + last / a.group : -1;
 
+        // The same part of the steps that this tile has.
+        auto place = [&](int e) { return e < w.sink_steps ? e : e - w.sink_steps + w.lo; };
+        const int e1 = share_of(item.s1, item.all, w.steps);
+        int e = share_of(s0, item.all, w.steps);
+        const int turns = (e1 - e + KW - 1) / KW;  // the same for all waves
+        e += kg;
+        const int32_t *row = uniform_ptr(a.table + (int64_t)b * a.ld_table);
+        const uint64_t head_base = (uint64_t)a.c.pages + (uint64_t)head * a.c.chunk;
+        const int32_t page_bytes = a.c.heads * a.c.chunk;
+        // pages of the steps in the ring, and of the next to be staged
+        Pages held[S::kAhead + 1];
+#pragma unroll
+        for (int i = 0; i <= S::kAhead; ++i) held[i] = pages_of(a, row, place(e + KW * i), e + KW * i < e1);
         // the queries into LDS
         for (int y = tid; y < RG * NT * 2 * R * 64; y += kThreads) {
             const int at = tile0 + 16 * (y / (2 * R * 64)) + (y & 15), i = at / a.group;
@@ -908,19 +921,6 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
         st.up = 1.0f;
         st.cap = 0;
 
-        // The same part of the steps that this tile has.
-        auto place = [&](int e) { return e < w.sink_steps ? e : e - w.sink_steps + w.lo; };
-        const int e1 = share_of(item.s1, item.all, w.steps);
-        int e = share_of(s0, item.all, w.steps);
-        const int turns = (e1 - e + KW - 1) / KW;  // the same for all waves
-        e += kg;
-        const int32_t *row = uniform_ptr(a.table + (int64_t)b * a.ld_table);
-        const uint64_t head_base = (uint64_t)a.c.pages + (uint64_t)head * a.c.chunk;
-        const int32_t page_bytes = a.c.heads * a.c.chunk;
-        // pages of the steps in the ring, and of the next to be staged
-        Pages held[S::kAhead + 1];
-#pragma unroll
-        for (int i = 0; i <= S::kAhead; ++i) held[i] = pages_of(a, row, place(e + KW * i), e + KW * i < e1);
 #pragma unroll
         for (int i = 0; i < S::kAhead; ++i)
             stage<D, RG>(a, ring + i * G::kStage, off, held[i], place(e + KW * i), head_base, page_bytes, rg);
