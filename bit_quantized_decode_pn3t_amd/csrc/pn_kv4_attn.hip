@@ -27,7 +27,9 @@
 //                 stay below 2^14, normal down to 2^-24 of the largest.
 //                 Scales may have any fp16 size, so each wave keeps a power of
 //                 two 2^u that puts the scales it has met below 2^7 at first
-//                 and 2^11 at most, values below 2^14.
+//                 and 2^11 at most, values below 2^14.  It is a factor in
+//                 fp16, so u is at most 15: the smallest subnormal scale then is
+//                 2^-9, and products with codes stay normal.
 // A row of A is element 2 i + (r >> 3) of word r & 7 of a block (r = lane &
 // 15, product i < 4), so that one product stays in one block; two v_perm-ed
 // words give the token pairs.
@@ -546,6 +548,17 @@ template <int N> __device__ __forceinline__ void wait_loads()
 // step ahead of its products and runs out of registers.
 __device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
 
+// The power of two on the value scales for a largest scale of the bits `big`,
+// and the largest scale (fp16 bits) that it leaves below 2^11.  The scales are
+// below 2^(e - 14); e from 6 on keeps the factor, 2^15 at most, inside fp16.
+__device__ __forceinline__ void fit_scales(uint32_t big, float &up, uint32_t &cap)
+{
+    int e = (int)(big >> 10);
+    e = e < 6 ? 6 : e < 30 ? e : 30;
+    up = __builtin_ldexpf(1.0f, 21 - e);
+    cap = e + 5 > 30 ? 0xffffu : (uint32_t)((e + 5) << 10) - 1;
+}
+
 __device__ __forceinline__ half8_t codes8(uint32_t word)
 {
     half2_t t[4];
@@ -737,10 +750,10 @@ __device__ __forceinline__ void advance(State<D, NT> &st, const uint8_t *from, c
             const uint32_t y = __shfl_xor(big, x, 64);
             big = y > big ? y : big;
         }
-        const int e = (int)(big >> 10) < 30 ? (int)(big >> 10) : 30;  // scales < 2^(e - 14)
-        const float up = __builtin_ldexpf(1.0f, 21 - e), f = up / st.up;  // the first time O is 0
+        float up;
+        fit_scales(big, up, st.cap);
+        const float f = up / st.up;  // the first time O is 0
         st.up = up;
-        st.cap = e + 5 > 30 ? 0xffffu : (uint32_t)((e + 5) << 10) - 1;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -1275,10 +1288,8 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
             if (it + 1 < count) {
                 const uint32_t big = uniform((int)most[(it + 1) % 3]);
                 if (big > cap) {  // the same in every wave
-                    const int e = (int)(big >> 10) < 30 ? (int)(big >> 10) : 30;  // scales < 2^(e - 14)
-                    next_up = __builtin_ldexpf(1.0f, 21 - e);
+                    fit_scales(big, next_up, cap);
                     f = next_up / up;
-                    cap = e + 5 > 30 ? 0xffffu : (uint32_t)((e + 5) << 10) - 1;
                 }
             }
             if (it >= 0 && tid == 0) {
