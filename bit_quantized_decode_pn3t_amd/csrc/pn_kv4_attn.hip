@@ -162,6 +162,14 @@ __device__ __forceinline__ void span(const AttnArgs &a, Work &w, int i0, int i1)
     w.steps = w.sink_steps + (end > w.lo ? end - w.lo : 0);
 }
 
+// The last position that the window of a query at `pos` leaves out, -1 or less
+// if there is none.  (A query ahead of all keys has a negative position, from
+// which a wide window must not be taken off.)
+__device__ __forceinline__ int32_t before_window(const AttnArgs &a, int32_t pos)
+{
+    return a.window > 0 && pos >= 0 ? pos - a.window : -1;
+}
+
 // a / b for non-negative a: a 64-bit quotient takes some hundred instructions.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
 {
@@ -697,7 +705,7 @@ __device__ __forceinline__ void advance(State<D, NT> &st, const uint8_t *from, c
 #pragma unroll
     for (int i = 0; i < 2; ++i) read_words(d[i], from + G::kScales + 256 * i + 32 * R + 8 * R * g);
     if (mask.some) {
-        const int32_t under = a.window > 0 ? mask.low - a.window : -1;
+        const int32_t under = before_window(a, mask.low);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int key = mask.token0 + 16 * (j >> 2) + 4 * g + (j & 3);
@@ -712,7 +720,7 @@ __device__ __forceinline__ void advance(State<D, NT> &st, const uint8_t *from, c
         for (int n = 0; n < NT; ++n) {
             const int at = mask.row0 + 16 * n + r;
             const int32_t pos = at < mask.rows ? mask.first + at / a.group : -1;
-            const int32_t below = a.window > 0 && pos >= 0 ? pos - a.window : -1;
+            const int32_t below = before_window(a, pos);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int key = mask.token0 + 16 * (j >> 2) + 4 * g + (j & 3);
@@ -733,7 +741,7 @@ __device__ __forceinline__ void advance(State<D, NT> &st, const uint8_t *from, c
         const int x = r & (4 * R - 1), i = x / (2 * R), h = x % (2 * R);
         uint32_t w = *(const uint32_t *)(from + G::kScales + 256 * i + 32 * R + 8 * R * g + 4 * h) & 0x7fff7fffu;
         if (mask.some) {  // as above
-            const int32_t under = a.window > 0 ? mask.low - a.window : -1;
+            const int32_t under = before_window(a, mask.low);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 const int key = mask.token0 + 16 * i + 4 * g + (2 * h + y) / R;
@@ -1208,7 +1216,7 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
                 }
             } else {
                 const int t0 = token_of(i);
-                const int32_t under = a.window > 0 ? t_low - a.window : -1;
+                const int32_t under = before_window(a, t_low);
                 const bool whole = t0 + kWide <= w.len && t0 + kWide - 1 <= t_high && (t0 > under || t0 + kWide <= a.sinks);
                 if (!whole || gone) {
 #pragma unroll
@@ -1350,7 +1358,7 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
                     if (some) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            const int32_t below = a.window > 0 && pos[n] >= 0 ? pos[n] - a.window : -1;
+                            const int32_t below = before_window(a, pos[n]);
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
                                 const int key = token0 + 16 * (j >> 2) + 4 * g + (j & 3), h = R * (j & 3);

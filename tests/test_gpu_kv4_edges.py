@@ -1,5 +1,5 @@
 """Edges of the attention-side operators on the GPU, against plain 64-bit
-implementations: small values."""
+implementations: small values, windows wider than any context."""
 import numpy as np
 import pytest
 
@@ -154,3 +154,11 @@ def test_small_values_first(shape, q, power):
 def test_small_value_alone(dim, power):
     """One key with a small value."""
     run([4, dim, -power], [1, 1, 1], [1, 1, 33], dim, 16, 2, 2, factor=lambda b, t: 2.0 ** power)
+
+
+# ---- windows ----------------------------------------------------------------------
+@pytest.mark.parametrize("shape,q", FORMS)
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 20, 2 ** 30])
+def test_window_wider_than_anything(shape, q, window):
+    """A window that hides nothing, with fewer keys than queries in some requests."""
+    run([5, q], [q, q + 3, q], [max(1, q // 2), q + 40, 1], *shape, window=window, sinks=2)
