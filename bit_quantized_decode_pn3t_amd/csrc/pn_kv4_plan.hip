@@ -9,15 +9,17 @@
 // most 8192 requests of 12 bytes, which the L2s hold) and then takes its
 // share of the tokens and of the fresh pages by binary search, so the whole
 // step is one launch with no workgroup waiting for another, no atomics, and
-// the same result every time.  Sums saturate at INT32_MAX: saturating
-// addition of non-negative numbers is associative, so the scan may group as
-// it likes.
+// the same result every time.  One more workgroup counts the lost tokens,
+// which takes table entries and free pages that the others need not read
+// alike: 4000 requests 12.4 us so, 11.7 where it counted by lengths alone (and
+// missed entries of -1).  Sums saturate at INT32_MAX: saturating addition of
+// non-negative numbers is associative, so the scan may group as it likes.
 //
 // Latency bounds it: the bytes are a few MB at most.  16 requests of 8 new
-// tokens: 6.0 us, 4000 requests of 8 tokens or a prompt: 11.7 us, where a
+// tokens: 5.4 us, 4000 requests of 8 tokens or a prompt: 12.4 us, where a
 // launch alone takes 3.6: the rest is three dependent rounds of loads, the
-// scan and the searches in LDS.  (All loads of a thread's requests first, and
-// the count of lost tokens in a workgroup of its own, change neither.)
+// scan and the searches in LDS.  (All loads of a thread's requests first
+// changes neither.)
 #include "pn_kv4.h"
 
 using namespace pn::host;
@@ -26,6 +28,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kPer = PN_KV4_MAX_BATCH / kThreads;  // requests a thread scans at most
+constexpr int kOwn = 2;  // columns of a request that a thread looks at alone
 
 struct PlanArgs {
     const int32_t *ctx, *fresh, *held, *free_pages;
@@ -56,12 +59,82 @@ __device__ __forceinline__ int32_t pages_for(int64_t tokens, int shift)
     return (int32_t)((tokens + ((int64_t)1 << shift) - 1) >> shift);
 }
 
+// The tokens without a place, by one workgroup: a request loses a tail (from
+// its first column without an entry, or from max_tokens on) and what lies in
+// columns before it whose entry is -1.
+__device__ void count_lost(const PlanArgs &a, const int32_t *start, const int32_t *page0)
+{
+    __shared__ int32_t lost[kThreads / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int32_t pages = page0[a.B];
+    int32_t mine = 0;
+    // New tokens of request i before its tail.
+    auto keep_of = [&](int i) {
+        const int64_t n = pos0(a.fresh[i]), held = pos0(a.held[i]), took = page0[i + 1] - page0[i];
+        int64_t got = (int64_t)a.num_free - page0[i];
+        got = got < 0 ? 0 : got < took ? got : took;
+        const int64_t cols = held + got < a.max_pages ? held + got : a.max_pages;
+        int64_t keep = (cols << a.shift) - pos0(a.ctx[i]);
+        if (n < keep) keep = n;
+        if (a.max_tokens - start[i] < keep) keep = a.max_tokens - start[i];
+        return keep < 0 ? 0 : keep;
+    };
+    // Of the first `keep` new tokens of a request with ctx before, those in column c.
+    auto in_column = [&](int64_t ctx, int64_t keep, int64_t c) {
+        const int64_t lo = c << a.shift, hi = lo + ((int64_t)1 << a.shift);
+        const int64_t n = (hi < ctx + keep ? hi : ctx + keep) - (lo > ctx ? lo : ctx);
+        return (int32_t)(n < 0 ? 0 : n);
+    };
+    for (int i0 = 0; i0 < a.B; i0 += kThreads) {
+        const int i = i0 + tid;
+        int64_t ctx = 0, keep = 0;
+        int32_t c0 = 0, c1 = 0;  // held columns that its new tokens lie in
+        if (i < a.B) {
+            ctx = pos0(a.ctx[i]);
+            keep = keep_of(i);
+            mine = sat_add(mine, (int32_t)(pos0(a.fresh[i]) - keep));
+            const int32_t held = pos0(a.held[i]), end = pages_for(ctx + keep, a.shift);
+            c0 = (int32_t)(ctx >> a.shift);
+            c1 = keep > 0 ? end < held ? end : held : 0;
+        }
+        // Entries of -1 among them.  A few are this thread's, many (pages held
+        // far ahead of a prompt) the whole wave's.
+        const bool many = c1 - c0 > kOwn;
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j)
+            if (!many && c0 + j < c1 && a.table[i * a.ld_table + c0 + j] < 0)
+                mine = sat_add(mine, in_column(ctx, keep, c0 + j));
+        for (uint64_t left = __ballot(many); left; left &= left - 1) {
+            const int l = __builtin_ctzll(left), from = __shfl(c0, l, 64), to = __shfl(c1, l, 64);
+            const int64_t row = (int64_t)(i0 + (tid & ~63) + l) * a.ld_table;
+            const int64_t its_ctx = __shfl(ctx, l, 64), its_keep = __shfl(keep, l, 64);
+            for (int c = from + lane; c < to; c += 64)
+                if (a.table[row + c] < 0) mine = sat_add(mine, in_column(its_ctx, its_keep, c));
+        }
+    }
+    // Entries of -1 among the fresh ones.
+    for (int64_t p = tid; p < pages && p < a.num_free; p += kThreads) {
+        if (a.free_pages[p] >= 0) continue;
+        const int i = last_at_most(page0, a.B, (int32_t)p);
+        mine = sat_add(mine, in_column(pos0(a.ctx[i]), keep_of(i), (int64_t)pos0(a.held[i]) + (p - page0[i])));
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) mine = sat_add(mine, __shfl_xor(mine, d, 64));
+    if (lane == 0) lost[wave] = mine;
+    __syncthreads();
+    if (tid == 0) {
+        int32_t all = 0;
+        for (int w = 0; w < kThreads / 64; ++w) all = sat_add(all, lost[w]);
+        a.info[0] = pages < a.num_free ? pages : a.num_free;
+        a.info[1] = all;
+    }
+}
+
 __global__ __launch_bounds__(kThreads) void kv4_plan(PlanArgs a)
 {
     __shared__ int32_t start[PN_KV4_MAX_BATCH + 1];  // first token of each request
     __shared__ int32_t page0[PN_KV4_MAX_BATCH + 1];  // first fresh page of each request
     __shared__ int32_t part[2][kThreads / 64];
-    __shared__ int32_t lost[kThreads / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int per = (a.B + kThreads - 1) / kThreads;
 
@@ -114,7 +187,11 @@ __global__ __launch_bounds__(kThreads) void kv4_plan(PlanArgs a)
     }
     __syncthreads();
 
-    const int64_t step = (int64_t)gridDim.x * kThreads, first = (int64_t)blockIdx.x * kThreads + tid;
+    if (blockIdx.x == gridDim.x - 1) {  // the last workgroup has this alone to do
+        count_lost(a, start, page0);
+        return;
+    }
+    const int64_t step = (int64_t)(gridDim.x - 1) * kThreads, first = (int64_t)blockIdx.x * kThreads + tid;
     const int32_t total = start[a.B], pages = page0[a.B];
 
     // what each request gets
@@ -155,33 +232,6 @@ __global__ __launch_bounds__(kThreads) void kv4_plan(PlanArgs a)
         a.positions[t] = pos;
         a.slots[t] = slot;
     }
-
-    if (blockIdx.x != 0) return;  // the same for the whole workgroup
-    // A request loses the tokens from its first missing page on, and those
-    // past max_tokens: both a tail.
-    int32_t mine = 0;
-    for (int i = tid; i < a.B; i += kThreads) {
-        const int64_t ctx = pos0(a.ctx[i]), n = pos0(a.fresh[i]), held = pos0(a.held[i]);
-        const int64_t took = page0[i + 1] - page0[i];
-        int64_t got = (int64_t)a.num_free - page0[i];
-        got = got < 0 ? 0 : got < took ? got : took;
-        const int64_t cols = held + got < a.max_pages ? held + got : a.max_pages;
-        int64_t keep = (cols << a.shift) - ctx;  // of its new tokens
-        const int64_t room = a.max_tokens - start[i];
-        if (room < keep) keep = room;
-        if (keep < 0) keep = 0;
-        if (keep < n) mine = sat_add(mine, (int32_t)(n - keep));
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) mine = sat_add(mine, __shfl_xor(mine, d, 64));
-    if (lane == 0) lost[wave] = mine;
-    __syncthreads();
-    if (tid == 0) {
-        int32_t all = 0;
-        for (int w = 0; w < kThreads / 64; ++w) all = sat_add(all, lost[w]);
-        a.info[0] = pages < a.num_free ? pages : a.num_free;
-        a.info[1] = all;
-    }
 }
 
 }  // namespace
@@ -207,7 +257,7 @@ extern "C" pn_status pn_kv4_plan(const int32_t *ctx_len, const int32_t *new_len,
                         slots, ld_table, max_tokens, B, num_free, shift, max_pages};
     int64_t grid = (max_tokens + kThreads - 1) / kThreads;
     if (grid > device_cus()) grid = device_cus();
-    hipLaunchKernelGGL(kv4_plan, dim3((unsigned)grid), dim3(kThreads), 0, (hipStream_t)stream, a);
+    hipLaunchKernelGGL(kv4_plan, dim3((unsigned)grid + 1), dim3(kThreads), 0, (hipStream_t)stream, a);
     if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
     g_last_variant = kVarKv4Plan;
     return PN_OK;

@@ -361,9 +361,14 @@ size_t pn_kv4_page_bytes(int page_size, int heads, int dim);
  *                  token has no page
  *   info[0] = entries of free_pages taken (<= num_free)
  *   info[1] = tokens without a place: past the free pages, past max_pages
- *             columns or past max_tokens
+ *             columns or past max_tokens, or in a column whose entry (held or
+ *             fresh) is negative
  * A request keeps pages that rejected drafts left ahead of its tokens, so a
  * caller lowers ctx_len freely and returns pages only when a request ends.
+ * held_out counts the columns of -1 that a shortage left, too, and columns that
+ * are held are not filled again.  To bring lost tokens again, a caller passes
+ * as held the entries before the row's first -1, and as ctx_len at most their
+ * tokens.
  *   table    : int32, B rows of ld_table >= max_pages; page ids
  *   held_out : must not overlap held
  *   B        : 1 .. PN_KV4_MAX_BATCH;  num_free >= 0;  max_tokens >= 1
