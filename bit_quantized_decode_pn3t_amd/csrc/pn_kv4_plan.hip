@@ -251,8 +251,17 @@ extern "C" pn_status pn_kv4_plan(const int32_t *ctx_len, const int32_t *new_len,
     for (const void *p : words)
         if (!aligned(p, 4)) return PN_EALIGN;
     if (!aligned(slots, 8)) return PN_EALIGN;
-    if (held_out < held + B && held < held_out + B) return PN_EINVAL;  // workgroups read held while others write held_out
     if (B > PN_KV4_MAX_BATCH || max_tokens > INT32_MAX) return PN_EUNSUPPORTED;
+    // Workgroups read the first five while others write the last seven (of the table different entries).
+    const struct { const void *p; int64_t bytes; } arrays[] = {
+        {ctx_len, 4 * (int64_t)B}, {new_len, 4 * (int64_t)B}, {held, 4 * (int64_t)B}, {free_pages, 4 * (int64_t)num_free},
+        {table, 4 * ((int64_t)(B - 1) * ld_table + max_pages)}, {held_out, 4 * (int64_t)B}, {q_start, 4 * ((int64_t)B + 1)},
+        {kv_len, 4 * (int64_t)B}, {positions, 4 * max_tokens}, {slots, 8 * max_tokens}, {info, 8}};
+    for (int i = 4; i < 11; ++i)
+        for (int j = 0; j < i; ++j) {
+            const uintptr_t x = (uintptr_t)arrays[i].p, y = (uintptr_t)arrays[j].p;
+            if (x < y + (uintptr_t)arrays[j].bytes && y < x + (uintptr_t)arrays[i].bytes) return PN_EINVAL;
+        }
     const PlanArgs a = {ctx_len, new_len, held, free_pages, table, held_out, q_start, kv_len, positions, info,
                         slots, ld_table, max_tokens, B, num_free, shift, max_pages};
     int64_t grid = (max_tokens + kThreads - 1) / kThreads;

@@ -370,7 +370,8 @@ size_t pn_kv4_page_bytes(int page_size, int heads, int dim);
  * as held the entries before the row's first -1, and as ctx_len at most their
  * tokens.
  *   table    : int32, B rows of ld_table >= max_pages; page ids
- *   held_out : must not overlap held
+ *   outputs  : (table among them) must not overlap each other or an input,
+ *              so kv_len is not ctx_len and held_out is not held
  *   B        : 1 .. PN_KV4_MAX_BATCH;  num_free >= 0;  max_tokens >= 1
  * Sums saturate at INT32_MAX. */
 #define PN_KV4_MAX_BATCH 8192

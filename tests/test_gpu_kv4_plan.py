@@ -11,6 +11,8 @@ torch = pytest.importorskip("torch")
 
 pytestmark = pytest.mark.gpu
 
+from bit_quantized_decode_pn3t_amd import _binding as B  # noqa: E402
+
 
 @pytest.fixture(scope="module", autouse=True)
 def _gpu():
@@ -66,3 +68,26 @@ def test_plan_holes(n, long, page):
         tokens = max(1, int(new.sum()) - (30 if turn == 3 else -30))
         say("plan holes n=%d page=%d turn=%d tokens=%d free=%d" % (n, page, turn, tokens, len(free)))
         check((ctx, new, held, free, page, table, width, tokens))
+
+
+def test_plan_arrays_side_by_side():
+    """All of a plan's arrays next to each other in one buffer: none is refused, none runs into another."""
+    ctx, new, held, free, page, width, tokens = [40, 0, 7], [5, 20, 0], [3, 0, 1], [9, 8, 7], 16, 4, 30
+    table = [[5, 4, 3, -1], [-1] * 4, [2, -1, -1, -1]]
+    want = R.plan(ctx, new, held, free, page, table, width, tokens)
+    parts = [("slots", [0] * 2 * tokens), ("ctx", ctx), ("new", new), ("held", held), ("free", free),
+             ("table", sum(table, [])), ("held_out", [0] * 3), ("q_start", [0] * 4), ("kv_len", [0] * 3),
+             ("positions", [0] * tokens), ("info", [0] * 2)]
+    flat = torch.tensor(sum((v for _, v in parts), []), dtype=torch.int32, device="cuda")
+    at, n = {}, 0
+    for name, v in parts:
+        at[name] = flat[n:n + len(v)]
+        n += len(v)
+    B.pn_kv4_plan(at["ctx"], at["new"], at["held"], 3, at["free"], 3, page, at["table"], width, width, at["held_out"],
+                  at["q_start"], at["kv_len"], at["positions"], at["slots"], tokens, at["info"])
+    torch.cuda.synchronize()
+    for name in want:
+        got = at[name].view(torch.int64) if name == "slots" else at[name]
+        assert got.tolist() == np.asarray(want[name]).reshape(-1).tolist(), name
+    for name, v in parts[1:5]:
+        assert at[name].tolist() == v
