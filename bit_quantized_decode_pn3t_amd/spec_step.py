@@ -90,14 +90,33 @@ class Requests:
         size = n * B.pn_kv4_page_bytes(page_size, model.heads, model.dim)
         self.caches = [B.KV4Cache(torch.empty(size, dtype=torch.uint8, device=dev), n, page_size, model.heads,
                                   model.dim) for _ in model.layers]
-        self.free = torch.arange(n, dtype=torch.int32, device=dev)
-        self.order = torch.arange(n, device=dev)
+        # page ids, -1 behind them: a request that is given none loses its tokens, and no page goes to two
+        self.free = torch.cat((torch.arange(n, dtype=torch.int32), torch.tensor([-1], dtype=torch.int32))).to(dev)
+        self.order = torch.arange(n + 1, device=dev)
+        self.lost = torch.zeros((), dtype=torch.int32, device=dev)  # tokens that found no place
+        self.longest = 0  # at least every request's tokens, known without waiting for the GPU
         i32 = dict(dtype=torch.int32, device=dev)
         self.table = torch.full((batch, self.max_pages), -1, **i32)
         self.ctx, self.held, self.last = (torch.zeros(batch, **i32) for _ in range(3))
         self.kv_len, self.q_start = torch.empty(batch, **i32), torch.empty(batch + 1, **i32)
         self.info = torch.empty(2, **i32)
         self.ws = torch.empty(0, dtype=torch.uint8, device=dev)
+
+    def _room(self, max_q):
+        """Refuse a step that could bring a request past max_len.  Its table
+        row ends there: tokens past it would not reach the cache, and pages
+        taken for them would be lost.  Near the end the lengths themselves are
+        read, which waits for the GPU."""
+        if self.longest + max_q > self.max_len:
+            self.longest = int(self.ctx.max())
+        if self.longest + max_q > self.max_len:
+            raise ValueError("%d more tokens for a request of %d pass max_len = %d" % (max_q, self.longest, self.max_len))
+        self.longest += max_q
+
+    def check(self):
+        """Raise if a token of any step so far found no place in the cache (waits for the GPU)."""
+        if int(self.lost):
+            raise RuntimeError("%d tokens found no place in the cache" % int(self.lost))
 
     def _forward(self, tokens, new_len, max_q):
         """Hidden states [T, hidden] of the step's tokens, which enter the cache."""
@@ -109,7 +128,7 @@ class Requests:
                       self.table, self.max_pages, self.max_pages, held, self.q_start, self.kv_len, positions, slots, T,
                       self.info)
         self.held = held
-        # Every request's pages fit, so what moves up behind the list is never reached.
+        self.lost += self.info[1]
         self.free = self.free[(self.order + self.info[0]).clamp_(max=self.order.numel() - 1)]
 
         q_row, kv_row = m.q_heads * m.dim, m.heads * m.dim
@@ -150,6 +169,7 @@ class Requests:
     def prompt(self, tokens, lengths, u, greedy=False):
         """Prompts (one flat row of tokens; lengths on the host) into the
         cache and each request's first token; u: [batch, 1]."""
+        self._room(max(lengths))
         new = torch.tensor(lengths, dtype=torch.int32, device=self.device)
         h = self._forward(tokens, new, max(lengths))
         self.ctx = self.kv_len.clone()
@@ -161,6 +181,7 @@ class Requests:
         [batch, k, vocab], or None for a drafter that is certain) and draw one
         more each; u: [batch, k + 1].  Returns out, accepted and the logits."""
         k = 0 if tokens is None else tokens.shape[1]
+        self._room(k + 1)
         row = self.last[:, None] if k == 0 else torch.cat((self.last[:, None], tokens), 1)
         new = torch.full((self.batch,), k + 1, dtype=torch.int32, device=self.device)
         h = self._forward(row.reshape(-1), new, k + 1)
@@ -204,6 +225,7 @@ def main():
         total += accepted.sum() + a.batch
     torch.cuda.synchronize()
     ms = (time.perf_counter() - t0) / max(a.steps, 1) * 1e3
+    req.check()
     print("%d requests, prompts of %d..%d tokens, %d layers: %.2f tokens a request and step (1 to %d), %.2f ms a step"
           % (a.batch, min(lengths), max(lengths), a.layers, int(total) / max(a.steps, 1) / a.batch, a.drafts + 1, ms))
 

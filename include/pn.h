@@ -365,6 +365,9 @@ size_t pn_kv4_page_bytes(int page_size, int heads, int dim);
  *             fresh) is negative
  * A request keeps pages that rejected drafts left ahead of its tokens, so a
  * caller lowers ctx_len freely and returns pages only when a request ends.
+ * Columns from max_pages on take fresh pages like the others (info[0], and the
+ * requests behind get later ones) though no entry keeps them, so a caller holds
+ * ctx_len + new_len within max_pages * page_size.
  * held_out counts the columns of -1 that a shortage left, too, and columns that
  * are held are not filled again.  To bring lost tokens again, a caller passes
  * as held the entries before the row's first -1, and as ctx_len at most their

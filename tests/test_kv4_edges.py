@@ -1,5 +1,5 @@
-"""Refusals of the attention-side entry points at their edges, on the CPU: every
-call here fails its host checks before any launch."""
+"""Refusals of the attention-side entry points and of the example at their
+edges, on the CPU: every call here fails its host checks before any launch."""
 import pytest
 
 from bit_quantized_decode_pn3t_amd import _binding as B
@@ -30,3 +30,38 @@ def test_plan_refuses_outputs_over_other_arrays(out, other):
     for shift in (0, size[other] - last, last - size[out]):  # the same place, its last word, up to its first
         shift = shift // last * last
         assert plan(**{other: at, out: at + shift}) == EINVAL, (out, other, shift)
+
+
+def requests(monkeypatch, max_len, lengths):
+    """The example's requests on the CPU, with steps that only count."""
+    torch = pytest.importorskip("torch")
+    from types import SimpleNamespace
+    from bit_quantized_decode_pn3t_amd import spec_step as S
+    model = SimpleNamespace(device=torch.device("cpu"), heads=1, dim=64, layers=[0])
+    req = S.Requests(model, len(lengths), max_len, 16)
+    ran = []
+    monkeypatch.setattr(S.Requests, "_forward", lambda self, tokens, new_len, max_q: ran.append(max_q) or torch.zeros(8, 4))
+    monkeypatch.setattr(S.Requests, "_answer", lambda self, *a: (None, torch.zeros(len(lengths), dtype=torch.int32), None))
+    req.kv_len, req.q_start = torch.tensor(lengths, dtype=torch.int32), torch.ones(len(lengths) + 1, dtype=torch.int32)
+    return torch, req, ran
+
+
+def test_example_refuses_steps_past_max_len(monkeypatch):
+    """A request that would pass its table row is refused before anything runs."""
+    torch, req, ran = requests(monkeypatch, 30, [20, 27])  # two pages: 32
+    assert req.max_len == 32
+    none = torch.zeros((2, 1), dtype=torch.int32)
+    with pytest.raises(ValueError):
+        req.prompt(torch.zeros(60, dtype=torch.int32), [33, 27], none)
+    assert ran == []
+    req.prompt(torch.zeros(47, dtype=torch.int32), [20, 27], none)
+    for _ in range(3):  # drafts refused each time: one token a step, 27 -> 30, though 27 + 3 * 3 > 32
+        req.step(none, torch.zeros((2, 2), dtype=torch.int32))
+    assert req.ctx.tolist() == [23, 30] and ran == [27, 3, 3, 3]
+    with pytest.raises(ValueError):
+        req.step(none, torch.zeros((2, 2), dtype=torch.int32))
+    req.step(none, torch.zeros((2, 1), dtype=torch.int32))
+    req.step(none)
+    with pytest.raises(ValueError):
+        req.step(none)
+    assert req.ctx.tolist() == [25, 32] and len(ran) == 6
