@@ -1,5 +1,7 @@
 """Edges of the attention-side operators on the GPU, against plain 64-bit
-implementations: small values, windows wider than any context."""
+implementations: small values, windows wider than any context, batches above
+64 requests, items cut between workgroups in every kernel, workspaces of every
+size, missing pages, bounds of lengths."""
 import numpy as np
 import pytest
 
@@ -162,3 +164,76 @@ def test_small_value_alone(dim, power):
 def test_window_wider_than_anything(shape, q, window):
     """A window that hides nothing, with fewer keys than queries in some requests."""
     run([5, q], [q, q + 3, q], [max(1, q // 2), q + 40, 1], *shape, window=window, sinks=2)
+
+
+# ---- batches above 64 requests ------------------------------------------------------
+@pytest.mark.parametrize("n", [64, 65, 300, 513, 1000, 2049])
+@pytest.mark.parametrize("dim,page,heads,group", [(64, 16, 2, 2), (128, 16, 1, 3), (256, 32, 1, 6)])
+def test_many_requests(n, dim, page, heads, group):
+    """Single tokens, drafts and a few prompts, requests without queries or
+    keys among them; short ones alone, and with a few long ones that are cut."""
+    g = np.random.default_rng([n, dim])
+    for most, long, window, sinks in ((1, 0, 0, 0), (6, 0, 0, 0), (6, 1500, 0, 0), (6, 1500, 30, 4), (1, 2500, 700, 0)):
+        q = g.integers(1, most + 1, n)
+        kv = q + g.integers(0, 70, n)
+        q[g.random(n) < 0.15] = 0
+        kv[g.random(n) < 0.1] = 0
+        if long:
+            at = g.permutation(n)[:4]
+            kv[at] = g.integers(long // 2, long, 4)
+            q[at] = np.minimum(g.integers(1, 4 * most, 4), kv[at])
+            kv[at[0]] = long
+        run([6, n, dim, most], q.tolist(), kv.tolist(), dim, page, heads, group, window, sinks)
+
+
+@pytest.mark.parametrize("dim,page,heads,group,q", [(64, 64, 1, 8, 70), (128, 16, 1, 6, 50), (256, 16, 1, 6, 30)])
+def test_many_requests_with_prompts(dim, page, heads, group, q):
+    """The kernels of many rows over more than 64 requests."""
+    g = np.random.default_rng([7, dim])
+    for n in (65, 140):
+        lens = np.where(g.random(n) < 0.2, q, g.integers(0, 4, n))
+        lens[0] = q
+        kv = lens + g.integers(0, 60, n)
+        kv[n // 2], lens[n // 2] = 1400, 20
+        run([7, n, dim], lens.tolist(), kv.tolist(), dim, page, heads, group)
+
+
+# ---- items cut between workgroups ----------------------------------------------------
+# rows of the longest request: one to four 16-row groups a wave, then the kernels of many rows
+ROWS = [(64, 16, 1, 5, 2), (64, 32, 1, 4, 7), (64, 16, 1, 8, 6), (64, 64, 1, 6, 11), (64, 64, 1, 8, 40),
+        (64, 16, 1, 8, 65), (64, 64, 1, 16, 70),
+        (128, 16, 1, 5, 2), (128, 32, 1, 4, 7), (128, 16, 1, 8, 6), (128, 64, 1, 6, 11), (128, 32, 1, 6, 42),
+        (128, 16, 1, 8, 33), (128, 64, 1, 6, 90),
+        (256, 16, 1, 5, 2), (256, 64, 1, 6, 8), (256, 16, 1, 6, 21), (256, 16, 1, 6, 22), (256, 32, 1, 8, 40)]
+
+
+@pytest.mark.parametrize("share", [1.0, 0.6, 0.27, 0.1, 0.0])
+@pytest.mark.parametrize("dim,page,heads,group,q", ROWS)
+def test_cut_items(dim, page, heads, group, q, share):
+    """More than 1024 keys: parts of items are joined, with room for all, some or none."""
+    run([8, dim, q], [q, 1, q, 0], [1700, 1300, 900 + q, 40], dim, page, heads, group, share=share)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (40, 3), (300, 70), (1100, 0), (5000, 4)])
+@pytest.mark.parametrize("dim,page,heads,group,q", ROWS)
+def test_cut_items_window(dim, page, heads, group, q, window, sinks):
+    run([9, dim, q, window], [q, 1, q], [2100, 1300, 900 + q], dim, page, heads, group, window, sinks)
+
+
+@pytest.mark.parametrize("dim,page,heads,group,q", ROWS)
+def test_holes_and_empty_rows(dim, page, heads, group, q):
+    """Pages that are not of the cache, whole requests of them, and more queries than keys."""
+    last = -(-1500 // page) - 1
+    holes = ((0, 0, -1), (0, 3, 10 ** 6), (0, last, -9), (1, 0, -1), (1, 1, 2 ** 31 - 1), (2, 1, -1))
+    for window, sinks in ((0, 0), (60, 5)):
+        run([10, dim, q, window], [q, q, q, q], [1500, min(33, 2 * page), 400, max(1, q // 3)], dim, page, heads, group,
+            window, sinks, holes=holes)
+
+
+@pytest.mark.parametrize("dim,page,heads,group,q", ROWS)
+def test_bounds_of_lengths(dim, page, heads, group, q):
+    """Keys past max_kv and queries past max_q are left out."""
+    for max_kv in (40, 1100):
+        run([11, dim, q, max_kv], [q, 1, q], [1500, 60, 1101], dim, page, heads, group, max_kv=max_kv)
+        run([12, dim, q, max_kv], [q, 1, q], [1500, 60, 1101], dim, page, heads, group, 50, 6, max_kv=max_kv)
+    run([13, dim, q], [q + 9, 1, q], [1300, 60, 700], dim, page, heads, group, max_q=q)
