@@ -1700,6 +1700,7 @@ extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, i
     if (const pn_status st = check_cache(cache, &a.c)) return st;
     if (!q || !q_start || !kv_len || !table || !out || (!ws && ws_bytes)) return PN_EINVAL;
     if (!sizes_ok(cache, q_heads, B, total_q, max_q, max_kv, sinks)) return PN_ESHAPE;
+    if (!(__builtin_fabsf(scale) <= 0x1.fffffep127f)) return PN_ESHAPE;  // infinite or NaN
     const int64_t cols = (int64_t)q_heads * cache->dim;
     if (ldq < cols || ldo < cols) return PN_ESHAPE;
     const int64_t pages = (max_kv + cache->page_size - 1) / cache->page_size;

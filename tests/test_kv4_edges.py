@@ -65,3 +65,12 @@ def test_example_refuses_steps_past_max_len(monkeypatch):
     with pytest.raises(ValueError):
         req.step(none)
     assert req.ctx.tolist() == [25, 32] and len(ran) == 6
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf")])
+def test_attn_refuses_scales_that_are_not_finite(scale):
+    cache = B.KV4Cache(BASE, 4, 16, 2, 64)
+    args = dict(q=BASE, ldq=256, q_heads=4, q_start=BASE, kv_len=BASE, table=BASE, ld_table=8, B=3, total_q=0, max_q=2,
+                max_kv=100, window=0, sinks=0, out=BASE, ldo=256, ws=None, ws_bytes=0, stream=0, check=False)
+    assert B.pn_kv4_attn(cache, scale=scale, **args) == ESHAPE
+    assert B.pn_kv4_attn(cache, scale=3.4e38, **args) == 0  # no queries: nothing to launch
