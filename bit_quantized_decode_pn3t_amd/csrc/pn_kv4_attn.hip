@@ -75,7 +75,9 @@ typedef __attribute__((address_space(3))) void lds_void;
 constexpr int kThreads = 512;
 constexpr int kWaves = 8;
 constexpr int kStep = 32;          // tokens of a step
-constexpr float kLowest = -1e30f;  // a maximum before any score
+// A maximum before any score: below all of them (65504^2 * 8 * 256 = 9e12), and
+// no further, so that its product with a large scale stays finite.
+constexpr float kLowest = -1e15f;
 constexpr float kBias = 10.0f;     // weights carry 2^kBias
 // Steps of a workgroup at least.  One 256-wide token over 8000 keys of two
 // heads: 22 us, with 32 27 us; 256 tokens over up to 1024 keys: 81 us, with 4

@@ -447,7 +447,7 @@ pn_status pn_kv4_load(const pn_kv4_cache *cache, const int64_t *slots, int64_t T
  *   q, out   : fp16, total_q rows, 16-byte aligned, ld >= q_heads * dim and a
  *              multiple of 8; must not overlap
  *   table    : int32, B rows of ld_table >= ceil(max_kv / page_size)
- *   scale    : finite
+ *   scale    : finite, up to 2^70; scale * q . k_t below 2^24
  *   max_q    : at least every request's queries (those past it are left out)
  *   max_kv   : at least every kv_len (keys past it are left out)
  *   sinks    : >= 0, read only with window > 0 (0: no window)

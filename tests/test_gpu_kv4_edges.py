@@ -63,7 +63,7 @@ def attend(q, pages, page, heads, dim, q_start, kv_len, table, scale, window, si
 
 
 def run(seed, q_lens, kv_lens, dim, page, heads, group, window=0, sinks=0, share=1.0, holes=(), factor=None,
-        max_q=None, max_kv=None, variant=None):
+        max_q=None, max_kv=None, variant=None, scale=None, sharp=1.0):
     """One call against the plain form.  share: part of the workspace that the
     call could use; factor(b, t): what the value scales of a request's tokens
     are multiplied by; variant: the kernel that must have run."""
@@ -94,9 +94,9 @@ def run(seed, q_lens, kv_lens, dim, page, heads, group, window=0, sinks=0, share
         scales[where[past], :, :, (t % page)[past]] = np.where(t[past] % 2, np.nan, -np.inf)[:, None, None, None]
     for b, c, entry in holes:
         table[b, c] = entry
-    scale = dim ** -0.5
+    scale = dim ** -0.5 if scale is None else scale
     ld = q_heads * dim + 8
-    q = g.standard_normal((T, ld)).astype(np.float16)
+    q = (g.standard_normal((T, ld)) * sharp).astype(np.float16)
     cache = B.KV4Cache(dev(pages), num_pages, page, heads, dim)
     mq = max_q or max(max(q_lens), 1)
     size = int(B.pn_kv4_attn_workspace(cache, q_heads, n, T, mq, top, window, sinks) * share) // 8 * 8
@@ -237,3 +237,13 @@ def test_bounds_of_lengths(dim, page, heads, group, q):
         run([11, dim, q, max_kv], [q, 1, q], [1500, 60, 1101], dim, page, heads, group, max_kv=max_kv)
         run([12, dim, q, max_kv], [q, 1, q], [1500, 60, 1101], dim, page, heads, group, 50, 6, max_kv=max_kv)
     run([13, dim, q], [q + 9, 1, q], [1300, 60, 700], dim, page, heads, group, max_q=q)
+
+
+# ---- large scales ------------------------------------------------------------------
+@pytest.mark.parametrize("dim,page,heads,group,q", ROWS)
+@pytest.mark.parametrize("scale,sharp", [(1e9, 2.0 ** -14), (-2e10, 2.0 ** -18), (1e-20, 1.0)])
+def test_scales_of_any_size(dim, page, heads, group, q, scale, sharp):
+    """A scale that is large and queries that are small: rows whose first steps,
+    or all keys, are masked stay what they are."""
+    run([14, dim, q], [q, q + 5, 1], [1500, max(1, q // 2), 40], dim, page, heads, group, scale=scale, sharp=sharp)
+    run([15, dim, q], [q, q], [1500, 300 + q], dim, page, heads, group, 20, 2, scale=scale, sharp=sharp)
