@@ -55,12 +55,13 @@ inline pn_status check_cache(const pn_kv4_cache *c, Kv4 *out)
     const int shift = page_shift(c->page_size);
     if (shift < 0 || !dim_ok(c->dim) || c->heads < 1 || c->num_pages < 1) return PN_ESHAPE;
     if (!aligned(c->pages, 16)) return PN_EALIGN;
-    if (c->heads > 65535) return PN_EUNSUPPORTED;
+    const int chunk = c->page_size * (c->dim + c->dim / 16);
+    if (c->heads > 65535 || (int64_t)c->heads * chunk > INT32_MAX) return PN_EUNSUPPORTED;  // a page's bytes are an int
     out->pages = (uint8_t *)c->pages;
     out->num_pages = c->num_pages;
     out->shift = shift;
     out->heads = c->heads;
-    out->chunk = c->page_size * (c->dim + c->dim / 16);
+    out->chunk = chunk;
     return PN_OK;
 }
 

@@ -332,7 +332,8 @@ pn_status pn_read_probe(const void *buf, size_t bytes, void *scratch, size_t scr
  *   K scales  page_size * R fp16: token o, block b at o * R + b
  *   V scales  likewise
  * Keys are stored normed and rotated.  Slot s is token s % page_size of page
- * s / page_size. */
+ * s / page_size.  Calls refuse (PN_EUNSUPPORTED) caches of more than 65535
+ * heads or whose page has 2^31 bytes or more. */
 #define PN_KV4_BLOCK 64
 typedef struct pn_kv4_cache {
     void *pages;       /* device, 16-byte aligned, num_pages * pn_kv4_page_bytes */

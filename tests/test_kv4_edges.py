@@ -74,3 +74,14 @@ def test_attn_refuses_scales_that_are_not_finite(scale):
                 max_kv=100, window=0, sinks=0, out=BASE, ldo=256, ws=None, ws_bytes=0, stream=0, check=False)
     assert B.pn_kv4_attn(cache, scale=scale, **args) == ESHAPE
     assert B.pn_kv4_attn(cache, scale=3.4e38, **args) == 0  # no queries: nothing to launch
+
+
+def test_pages_past_2_gib_are_refused():
+    """A page's bytes are 32-bit offsets in attention."""
+    for heads, dim, page, status in ((65535, 256, 256, EUNSUPPORTED), (30841, 256, 256, EUNSUPPORTED), (30840, 256, 256, 0),
+                                     (65535, 128, 256, EUNSUPPORTED), (65535, 64, 256, 0)):
+        cache = B.KV4Cache(BASE, 2, page, heads, dim)
+        assert B.pn_kv4_page_bytes(page, heads, dim) == page * heads * (dim + dim // 16)
+        assert B.pn_kv4_load(cache, BASE, 0, BASE, BASE, stream=0, check=False) == status
+        assert B.pn_kv4_attn(cache, BASE, heads * dim, heads, BASE, BASE, BASE, 8, 1, 0, 1, 100, 1.0, 0, 0, BASE,
+                             heads * dim, None, 0, stream=0, check=False) == status
