@@ -38,6 +38,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kUnit = 512;  // elements a wave holds
+constexpr int64_t kGrid = (int64_t)UINT32_MAX / kThreads;  // workgroups of a launch
 
 struct StoreArgs {
     Kv4 c;
@@ -321,10 +322,11 @@ extern "C" pn_status pn_kv4_store(const pn_kv4_cache *cache, const pn_kv4_store_
     a.split = 1;
     while (a.split < most && d->T * a.split < 2 * device_cus()) a.split *= 2;
     if (a.split > most) a.split = most;
-    a.tokens = 1;
-    const int64_t groups = (d->T + a.tokens - 1) / a.tokens;
-    if (groups * a.split > INT32_MAX) return PN_EUNSUPPORTED;
-    const unsigned grid = (unsigned)(groups * a.split);
+    // A launch holds less than 2^32 threads: past 2^24 tokens a workgroup takes several.
+    const int64_t tokens = d->T > kGrid ? (d->T + kGrid - 1) / kGrid : 1;
+    if (tokens > INT32_MAX) return PN_EUNSUPPORTED;
+    a.tokens = (int32_t)tokens;
+    const unsigned grid = (unsigned)((d->T + tokens - 1) / tokens * a.split);
     const hipStream_t s = (hipStream_t)stream;
     if (dim == 64) store_launch<64>(a, grid, s);
     else if (dim == 128) store_launch<128>(a, grid, s);
@@ -344,7 +346,7 @@ extern "C" pn_status pn_kv4_load(const pn_kv4_cache *cache, const int64_t *slots
     if (!aligned(slots, 8) || !aligned(k, 16) || !aligned(v, 16)) return PN_EALIGN;
     if (T == 0) return PN_OK;
     const int64_t per = (int64_t)cache->heads * (cache->dim / 8);
-    if (T > ((int64_t)INT32_MAX * kThreads) / per) return PN_EUNSUPPORTED;
+    if (T > kGrid * kThreads / per) return PN_EUNSUPPORTED;
     const int64_t words = T * per;
     const unsigned grid = (unsigned)((words + kThreads - 1) / kThreads);
     const hipStream_t s = (hipStream_t)stream;

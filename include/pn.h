@@ -431,7 +431,8 @@ pn_status pn_kv4_store(const pn_kv4_cache *cache, const pn_kv4_store_desc *d, vo
 /* The cached keys and values of T slots as fp32, d * (n - 8) exactly: k[t] and
  * v[t] rows of heads * dim, 16-byte aligned (either may be NULL); a slot
  * outside the cache gives zeros.  The check path of pn_kv4_store, and how a
- * request's cache is read back. */
+ * request's cache is read back.  T * heads * dim / 8 <= 2^32 - 256, else
+ * PN_EUNSUPPORTED. */
 pn_status pn_kv4_load(const pn_kv4_cache *cache, const int64_t *slots, int64_t T, float *k, float *v, void *stream);
 
 /* Attention of a ragged batch over the cache.  Request i has queries

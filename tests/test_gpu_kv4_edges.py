@@ -247,3 +247,30 @@ def test_scales_of_any_size(dim, page, heads, group, q, scale, sharp):
     or all keys, are masked stay what they are."""
     run([14, dim, q], [q, q + 5, 1], [1500, max(1, q // 2), 40], dim, page, heads, group, scale=scale, sharp=sharp)
     run([15, dim, q], [q, q], [1500, 300 + q], dim, page, heads, group, 20, 2, scale=scale, sharp=sharp)
+
+
+# ---- many tokens -------------------------------------------------------------------
+def test_store_more_tokens_than_workgroups():
+    """More than 2^24 tokens in one call leave what two calls leave."""
+    T, dim, page = 2 ** 24 + 1000, 64, 256
+    n = -(-T // page)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x = torch.randn((T, dim), generator=g, device="cuda", dtype=torch.float16)
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    slots = torch.arange(T, device="cuda")
+    inv = dev((10000.0 ** (-np.arange(dim // 2) / (dim // 2))).astype(np.float32))
+    gain = torch.linspace(0.5, 1.5, dim, device="cuda")
+    outs = []
+    for parts in ((0, T), (0, T // 2, T)):
+        pages = torch.zeros((n, B.pn_kv4_page_bytes(page, 1, dim)), dtype=torch.uint8, device="cuda")
+        q = torch.zeros_like(x)
+        cache = B.KV4Cache(pages, n, page, 1, dim)
+        for lo, hi in zip(parts, parts[1:]):
+            say("store tokens %d..%d" % (lo, hi))
+            B.pn_kv4_store(cache, hi - lo, x[lo:], x[lo:], x[lo:], "f16", dim, dim, dim, 1, gain, gain, 1e-6, inv, dim,
+                           False, pos[lo:], slots[lo:], q[lo:], dim)
+        sync()
+        outs.append((pages, q))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    assert outs[0][1][-1].abs().max() > 0 and outs[0][0][(T - 1) // page].any()

@@ -85,3 +85,9 @@ def test_pages_past_2_gib_are_refused():
         assert B.pn_kv4_load(cache, BASE, 0, BASE, BASE, stream=0, check=False) == status
         assert B.pn_kv4_attn(cache, BASE, heads * dim, heads, BASE, BASE, BASE, 8, 1, 0, 1, 100, 1.0, 0, 0, BASE,
                              heads * dim, None, 0, stream=0, check=False) == status
+
+
+def test_load_refuses_more_than_a_launch_holds():
+    cache = B.KV4Cache(BASE, 4, 16, 2, 64)  # 16 words a token
+    for tokens in (2 ** 28, 2 ** 40):
+        assert B.pn_kv4_load(cache, BASE, tokens, BASE, None, stream=0, check=False) == EUNSUPPORTED
