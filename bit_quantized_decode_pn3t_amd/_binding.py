@@ -71,8 +71,6 @@ class pn_kv4_store_desc(ctypes.Structure):
                 ("rot", ctypes.c_int32), ("pairs", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
-KV4_BLOCK = 64  # PN_KV4_BLOCK
-KV4_MAX_BATCH = 8192  # PN_KV4_MAX_BATCH
 ROW_TYPES = {"f32": 0, "f16": 1, 0: 0, 1: 1}  # PN_ROWS_*
 
 _lib = None

@@ -36,6 +36,7 @@ enum Variant {
     kVarKv4Load = 20,
     kVarKv4Attn = 21,
     kVarSpecVerify = 22,
+    kVarKv4Prompt = 23,
 };
 
 extern thread_local int g_last_variant;

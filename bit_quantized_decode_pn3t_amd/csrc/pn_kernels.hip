@@ -1047,6 +1047,7 @@ const char *pn_variant_name(int v)
     case kVarKv4Load: return "kv4_load";
     case kVarKv4Attn: return "kv4_attn";
     case kVarSpecVerify: return "spec_verify";
+    case kVarKv4Prompt: return "kv4_prompt";
     }
     return "unknown";
 }

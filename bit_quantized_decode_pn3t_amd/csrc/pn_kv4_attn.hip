@@ -1082,14 +1082,14 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
 // row groups took 510.  Three chunks of 1000 queries under a window of 2048,
 // 64 wide (151 GFLOP): 300 to 324 us and 19; 54 % and 19.
 // ---------------------------------------------------------------------------
-constexpr int kWide = 64;  // tokens of a prompt's step
+constexpr int kPromptStep = 64;  // tokens of a prompt's step
 
 template <int D, int NT> struct Prompt {
     static constexpr int R = D / 64;
     static constexpr int kRows = kWaves * 16 * NT;
-    static constexpr int kFrags = kWide / 16 * 2 * R;       // of K: [tile][block][h]; of V: [32 tokens][block][product], as many
+    static constexpr int kFrags = kPromptStep / 16 * 2 * R;       // of K: [tile][block][h]; of V: [32 tokens][block][product], as many
     static constexpr int kBuf = 2 * kFrags * 1024;          // one step's K and V
-    static constexpr int kScale = kWide * R * 2;            // K's scales of a step: [token][block] fp16
+    static constexpr int kScale = kPromptStep * R * 2;            // K's scales of a step: [token][block] fp16
     static constexpr int kOut = kRows * 2 * D;              // the rows on their way out, where the fragments were
     static constexpr int kSteps = 2 * kBuf + 3 * kScale;
     static constexpr int kLds = kSteps > kOut ? kSteps : kOut;
@@ -1127,14 +1127,14 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
     const int part = keys ? unit % (D / 32) : unit % (D / 8);
     const int token = keys ? unit / (D / 32) : unit / (D / 8) * 4;  // of the step
     Line line;
-    if (!line_part<kWide>(a, line_lds, line, kRows)) return;
+    if (!line_part<kPromptStep>(a, line_lds, line, kRows)) return;
     for (int64_t x = line.lo; x < line.hi;) {
         Item item;
-        if (!next_item<kWide>(a, line_lds, line, x, item, kRows)) continue;
+        if (!next_item<kPromptStep>(a, line_lds, line, x, item, kRows)) continue;
         const int head = item.head, tile0 = item.tile0, rows = item.rows, b = line.b;
         Work w{item.c.w};
         const int tile_last = (tile0 + kRows < rows ? tile0 + kRows : rows) - 1;
-        span<kWide>(a, w, tile0 / a.group, tile_last / a.group);
+        span<kPromptStep>(a, w, tile0 / a.group, tile_last / a.group);
         const int32_t t_low = w.first + tile0 / a.group, t_high = w.first + tile_last / a.group;  // the tile's positions
         const int row0 = tile0 + wave * 16 * NT;
         const int last = (row0 + 16 * NT < rows ? row0 + 16 * NT : rows) - 1;
@@ -1170,7 +1170,7 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
         const int count = share_of(item.s1, item.all, w.steps) - e0;
         auto token_of = [&](int i) {
             const int e = e0 + i;
-            return (e < w.sink_steps ? e : e - w.sink_steps + w.lo) * kWide;
+            return (e < w.sink_steps ? e : e - w.sink_steps + w.lo) * kPromptStep;
         };
         const int32_t *row = uniform_ptr(a.table + (int64_t)b * a.ld_table);
         // Page of the thread's token in step i.  Steps past the end repeat the last.
@@ -1219,7 +1219,8 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
             } else {
                 const int t0 = token_of(i);
                 const int32_t under = before_window(a, t_low);
-                const bool whole = t0 + kWide <= w.len && t0 + kWide - 1 <= t_high && (t0 > under || t0 + kWide <= a.sinks);
+                const int t1 = t0 + kPromptStep;
+                const bool whole = t1 <= w.len && t1 - 1 <= t_high && (t0 > under || t1 <= a.sinks);
                 if (!whole || gone) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -1318,7 +1319,7 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
                 const uint8_t *scales = lds + 2 * P::kBuf + it % 3 * P::kScale;
                 const bool gone = uniform((int)bad[it % 4]) != 0;
 #pragma unroll 1
-                for (int sub = 0; sub < kWide / 32; ++sub) {
+                for (int sub = 0; sub < kPromptStep / 32; ++sub) {
                     const int token0 = token_of(it) + 32 * sub;
                     // nothing of it is visible to the wave's rows
                     if (token0 > p1 || (a.window > 0 && (int64_t)token0 + 31 + a.window <= p0 && token0 >= a.sinks)) continue;
@@ -1747,7 +1748,7 @@ extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, i
     a.parts = t.parts;
     const int tile_rows = 16 * t.nt * t.rg;
     a.queries = (tile_rows + a.group - 1) / a.group;
-    a.grow = tile_rows * kUnit / (a.group * (t.rg == kWaves ? kWide : kStep));
+    a.grow = tile_rows * kUnit / (a.group * (t.rg == kWaves ? kPromptStep : kStep));
     a.whole = t.whole;
     // What an item's start and end cost in steps.  64 wide, 64 requests of up
     // to 16384: 54 us, counted as nothing 80, twice as much 57; 128 wide, a
@@ -1761,6 +1762,6 @@ extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, i
     const pn_status st = cache->dim == 64    ? launch_rows<64>(a, t, s)
                          : cache->dim == 128 ? launch_rows<128>(a, t, s)
                                              : launch_rows<256>(a, t, s);
-    if (st == PN_OK) g_last_variant = kVarKv4Attn;
+    if (st == PN_OK) g_last_variant = t.rg == kWaves ? kVarKv4Prompt : kVarKv4Attn;
     return st;
 }
