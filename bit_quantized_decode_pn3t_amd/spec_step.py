@@ -167,8 +167,10 @@ class Requests:
         return out, accepted, logits
 
     def prompt(self, tokens, lengths, u, greedy=False):
-        """Prompts (one flat row of tokens; lengths on the host) into the
-        cache and each request's first token; u: [batch, 1]."""
+        """Prompts (one flat row of tokens; lengths on the host, 1 and up) into
+        the cache and each request's first token; u: [batch, 1]."""
+        if len(lengths) != self.batch or min(lengths) < 1 or sum(lengths) != tokens.numel():
+            raise ValueError("%d tokens for prompts of %s" % (tokens.numel(), lengths))
         self._room(max(lengths))
         new = torch.tensor(lengths, dtype=torch.int32, device=self.device)
         h = self._forward(tokens, new, max(lengths))

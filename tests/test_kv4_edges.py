@@ -91,3 +91,12 @@ def test_load_refuses_more_than_a_launch_holds():
     cache = B.KV4Cache(BASE, 4, 16, 2, 64)  # 16 words a token
     for tokens in (2 ** 28, 2 ** 40):
         assert B.pn_kv4_load(cache, BASE, tokens, BASE, None, stream=0, check=False) == EUNSUPPORTED
+
+
+@pytest.mark.parametrize("lengths,count", [([0, 9], 9), ([4, 5], 8), ([9], 9), ([3, 3, 3], 9), ([10, -1], 9)])
+def test_example_refuses_prompts_that_do_not_fit(monkeypatch, lengths, count):
+    """A prompt without tokens has no last token to answer from."""
+    torch, req, ran = requests(monkeypatch, 30, [20, 27])
+    with pytest.raises(ValueError):
+        req.prompt(torch.zeros(count, dtype=torch.int32), lengths, torch.zeros((2, 1)))
+    assert ran == []
