@@ -48,16 +48,19 @@
 // take rows of their own and share the staged steps, one of two each.  The
 // waves of the same rows are joined through LDS.  All sums have a fixed order.
 //
-// What bounds it: for single tokens the unpacking, half a vector instruction a
-// code, and at few steps a wave the latency of start and join.  One 256-wide
-// token over 65536 keys (4 key-value heads, 71 MB): 26.1 us and 7.8 for the
-// join, 2.1 TB/s in all; 64 128-wide requests of up to 16384 (135 MB): 54 and
-// 5.3, 2.3 TB/s, vector instructions 45 % of the time and products 7; with 64
-// full requests of 16384 the loop alone runs at 4.4 to 4.8 TB/s.  16 requests
-// of 8 drafts over up to 5003 keys, 256 wide: 36.5 and 5.5 us.  One token over
-// one key, 64 wide: 9.6 us, 1.7 of them until a workgroup has its part of the
-// line, 1.4 until it has an item, 2.4 until its queries and loads are under
-// way, 2.2 for a step and 1.1 to join the waves: code that is run once.
+// What bounds it: latency; no pipe is full.  One 256-wide token over 65536 keys
+// (4 key-value heads, 71 MB): 26.5 us and 7.8 for the join, 2.1 TB/s in all,
+// vector instructions 33 % of the time: four steps a wave between code that is
+// run once.  64 128-wide requests of up to 16384 (135 MB): 54 and 5.3, 2.3
+// TB/s, vector instructions (half of one a code) 45 % of the time and products
+// 7; with 64 full requests of 16384 the loop alone runs at 4.4 to 4.8 TB/s, so
+// the rest is where items start and end.  16 requests of 8 drafts over up to
+// 5003 keys, 256 wide: 36.7 and 5.5 us.  One token over one key, 64 wide: 9.6
+// us, 1.7 of them until a workgroup has its part of the line, 1.4 until it has
+// an item, 2.4 until its queries and loads are under way, 2.2 for a step and
+// 1.1 to join the waves: code that is run once.  1000 requests of up to 2000,
+// 128 wide (313 MB): 212 us.  A 256-wide prompt of 4096 with 24 heads (206
+// GFLOP): 536 us and 17.7.
 #include "pn_kv4.h"
 #include "pn_device.h"
 
@@ -1074,13 +1077,15 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
 // into those of the second, both as fp16 fragments in LDS that all waves then
 // read; the words come straight into registers two steps ahead.  64 tokens a
 // step, one barrier: while it is worked on, the next one is unpacked.
-// Unpacking costs a wave an eighth of what it would alone; what is left bounds
-// the kernel: exp2 and the arithmetic around it, which take twice as long as
-// the products they go with and overlap with them in part.  A prompt of 4096
-// with 48 heads, 128 wide (206 GFLOP): 340 to 365 us and 23 for the join, vector
-// instructions 47 % of the time and the matrix units 23; kv4_attn with four
-// row groups took 510.  Three chunks of 1000 queries under a window of 2048,
-// 64 wide (151 GFLOP): 300 to 324 us and 19; 54 % and 19.
+// Unpacking costs a wave an eighth of what it would alone.  What bounds the
+// kernel is that a part's scores, softmax and values wait for each other, with
+// two waves a SIMD to fill the gaps: exp2 and the arithmetic around it take
+// twice as long as the products they go with and overlap with them in part, and
+// neither pipe is full.  A prompt of 4096 with 48 heads, 128 wide (206 GFLOP):
+// 357 to 383 us and 23 for the join, vector instructions 47 % of the time and
+// the matrix units 23; kv4_attn with four row groups took 510.  Three chunks of
+// 1000 queries under a window of 2048, 64 wide (151 GFLOP): 305 to 329 us and
+// 19; 54 % and 19.
 // ---------------------------------------------------------------------------
 constexpr int kPromptStep = 64;  // tokens of a prompt's step
 

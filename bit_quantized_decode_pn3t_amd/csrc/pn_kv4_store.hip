@@ -21,9 +21,12 @@
 // out).  Queries end in fp16 and run in fp32.
 //
 // That shape, 128 wide, with 8191 tokens: 110 us, 3.4 TB/s, where a copy
-// reaches 5.05.  Vector instructions take half of the time (fp64 square roots,
-// quotients, selections and exchanges), loads the rest: the 120 registers that
-// the fp64 path needs allow four waves a SIMD.  Fewer registers spill (five
+// reaches 5.05.  Vector instructions take half of the time, at four waves a
+// SIMD.  The registers are those of the fp64 path (square roots, quotients,
+// selections and exchanges), which only the keys need, an eighth of the
+// columns: queries, three quarters of them, and values share the kernel and so
+// its registers.  Words leave four bytes at a time, 16 bytes apart for values:
+// 126 MB are written where the outputs have 110.  Fewer registers spill (five
 // waves 126 us, six 135), gains and angles kept in registers cost waves (133),
 // and loads of four units ahead gain nothing (111).  One token: 5 us.
 #include <math.h>

@@ -478,8 +478,8 @@ pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, int64_t ldq,
  *   with a = accepted drafts, one more token is drawn from r = max(p_a - q_a,
  *   0) if a < n (without `draft`: p_a with x_a's entry 0), else from p_n: the
  *   first index whose inclusive prefix sum (fp64) is above u[i][k] * sum r.
- * Entries that are not positive and finite count as 0.  If r has none, the
- * token is drawn from p_a; if that has none either it is -1.
+ * Entries of r and p_a that are not positive and finite count as 0.  If r has
+ * none, the token is drawn from p_a; if that has none either it is -1.
  *   out[i]      : the accepted drafts, the drawn token, then -1 (k + 1)
  *   accepted[i] : a
  *   target  : fp32, row (i, j) at (i * (k + 1) + j) * ldt, ldt >= V
