@@ -30,6 +30,7 @@ EXPORTS = ("pn_weights_per_block", "pn_row_bytes", "pn_gemv", "pn_gemv2",
            "pn_group_create", "pn_group_create_smallm", "pn_group_run", "pn_group_destroy", "pn_gemv_batch",
            "pn_kv4_page_bytes", "pn_kv4_plan", "pn_kv4_store", "pn_kv4_load", "pn_kv4_attn_workspace",
            "pn_kv4_attn", "pn_spec_workspace", "pn_spec_verify",
+           "pn_residual_norm", "pn_logprobs_workspace", "pn_logprobs",
            "pn_read_probe_scratch_bytes", "pn_read_probe", "pn_status_str", "pn_last_variant",
            "pn_variant_name")
 
@@ -71,7 +72,16 @@ class pn_kv4_store_desc(ctypes.Structure):
                 ("rot", ctypes.c_int32), ("pairs", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
+class pn_residual_norm_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("h", "y", "z", "post_gain", "chan_scale", "pre_gain", "h_out", "x")] + [
+        (n, ctypes.c_int64) for n in ("ldh", "ldy", "ldz", "ldho", "ldx", "T", "n")] + [
+        (n, ctypes.c_int32) for n in ("row_type", "gate", "post")] + [("scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 ROW_TYPES = {"f32": 0, "f16": 1, 0: 0, 1: 1}  # PN_ROWS_*
+GATES = {"none": 0, "plain": 1, "sigmoid": 2, "silu": 3, 0: 0, 1: 1, 2: 2, 3: 3}  # PN_GATE_*
+NORM_MAX = 32768  # PN_NORM_MAX
+LOGPROBS_MAX_TOP = 64  # PN_LOGPROBS_MAX_TOP
 
 _lib = None
 
@@ -141,6 +151,13 @@ def lib():
     L.pn_spec_verify.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i64, i32, i32, i64, vp, i64, vp, vp,
                                  ctypes.c_size_t, vp]
     L.pn_spec_verify.restype = i32
+    L.pn_residual_norm.argtypes = [ctypes.POINTER(pn_residual_norm_desc), vp]
+    L.pn_residual_norm.restype = i32
+    L.pn_logprobs_workspace.argtypes = [i64, i64, i32]
+    L.pn_logprobs_workspace.restype = ctypes.c_size_t
+    L.pn_logprobs.argtypes = [vp, i32, i64, i64, i64, ctypes.c_float, vp, i64, i32, vp, i64, vp, i32, vp, vp, i64, vp,
+                              ctypes.c_size_t, vp]
+    L.pn_logprobs.restype = i32
     L.pn_read_probe_scratch_bytes.argtypes = []
     L.pn_read_probe_scratch_bytes.restype = ctypes.c_size_t
     L.pn_read_probe.argtypes = [vp, ctypes.c_size_t, vp, ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t), vp]
@@ -426,6 +443,33 @@ def pn_spec_verify(target, ldt, draft, ldd, tokens, ld_tok, n_draft, u, ldu, B, 
                               B, k, V, _ptr(out), ld_out, _ptr(accepted), _ptr(ws), ws_bytes, _stream(stream))
     if check:
         _check(st, "pn_spec_verify")
+    return st
+
+
+def pn_residual_norm(T, n, h, ldh, y, ldy, row_type, gate, z, ldz, post, post_gain, scale, chan_scale, pre_gain, eps,
+                     h_out, ldho, x, ldx, stream=None, check=True):
+    """A block's output into the residual stream (norm, gate, scale), and the next block's normed fp16 input."""
+    d = pn_residual_norm_desc(_ptr(h), _ptr(y), _ptr(z), _ptr(post_gain), _ptr(chan_scale), _ptr(pre_gain), _ptr(h_out),
+                              _ptr(x), ldh, ldy, ldz, ldho, ldx, T, n, ROW_TYPES.get(row_type, -1), GATES.get(gate, -1),
+                              1 if post else 0, scale, eps)
+    st = lib().pn_residual_norm(d, _stream(stream))
+    if check:
+        _check(st, "pn_residual_norm")
+    return st
+
+
+def pn_logprobs_workspace(rows, V, K):
+    return lib().pn_logprobs_workspace(rows, V, K)
+
+
+def pn_logprobs(logits, row_type, ld, rows, V, scale, tokens, ld_tok, n_tok, logp, ld_lp, entropy, K, top_ids,
+                top_logp, ld_top, ws, ws_bytes, stream=None, check=True):
+    """Log probabilities of given tokens, entropy and the K best alternatives of logit rows."""
+    st = lib().pn_logprobs(_ptr(logits), ROW_TYPES.get(row_type, -1), ld, rows, V, scale, _ptr(tokens), ld_tok, n_tok,
+                           _ptr(logp), ld_lp, _ptr(entropy), K, _ptr(top_ids), _ptr(top_logp), ld_top, _ptr(ws),
+                           ws_bytes, _stream(stream))
+    if check:
+        _check(st, "pn_logprobs")
     return st
 
 

@@ -37,6 +37,8 @@ enum Variant {
     kVarKv4Attn = 21,
     kVarSpecVerify = 22,
     kVarKv4Prompt = 23,
+    kVarResidualNorm = 24,
+    kVarLogprobs = 25,
 };
 
 extern thread_local int g_last_variant;

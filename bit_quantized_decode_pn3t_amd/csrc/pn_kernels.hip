@@ -1048,6 +1048,8 @@ const char *pn_variant_name(int v)
     case kVarKv4Attn: return "kv4_attn";
     case kVarSpecVerify: return "spec_verify";
     case kVarKv4Prompt: return "kv4_prompt";
+    case kVarResidualNorm: return "residual_norm";
+    case kVarLogprobs: return "logprobs";
     }
     return "unknown";
 }

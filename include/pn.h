@@ -493,6 +493,73 @@ pn_status pn_spec_verify(const float *target, int64_t ldt, const float *draft, i
                          int64_t ld_tok, const int32_t *n_draft, const float *u, int64_t ldu, int B, int k, int64_t V,
                          int32_t *out, int64_t ld_out, int32_t *accepted, void *ws, size_t ws_bytes, void *stream);
 
+/* Between two blocks of a decoder: the norm of what a block gave, its gate and
+ * residual scale, the sum with the residual stream, and the norm ahead of the
+ * next block's products, in one pass.  For each of T rows of n elements
+ *   u  = y                                            (post 0)
+ *        y * post_gain / sqrt(mean(y^2) + eps)        (post 1)
+ *   h' = h + scale * chan_scale * g(z) * u            (y NULL: h' = h)
+ *   x  = fp16(h' * pre_gain / sqrt(mean(h'^2) + eps))
+ * with g(z) = 1, z, 1 / (1 + exp(-z)) or z / (1 + exp(-z)) (PN_GATE_*), in fp32
+ * throughout; gains and chan_scale that are NULL count as 1.  x is what
+ * pn_gemv, pn_gemm_smallm and pn_gemm_prefill read.
+ *   h, h_out : fp32 rows.  h_out may be h (same ld) or NULL (only x wanted)
+ *   y, z     : rows of row_type (PN_ROWS_*); z with a gate only, ldz 0: one row
+ *              for all
+ *   x        : fp16 rows, or NULL (only h_out wanted)
+ *   gains    : fp32 [n]; post_gain with post only
+ *   All 16-byte aligned; ld in elements, >= n and a multiple of 4 (fp32) or 8
+ *   (fp16).  Elements behind a row's n are neither read nor written.  Outputs
+ *   overlap no input (but h_out = h) and not each other, else PN_EINVAL.
+ *   scale finite; eps finite, >= 0;  T >= 0 (0 does nothing);
+ *   n 1 .. PN_NORM_MAX (else PN_EUNSUPPORTED). */
+#define PN_NORM_MAX 32768
+enum { PN_GATE_NONE = 0, PN_GATE_PLAIN = 1, PN_GATE_SIGMOID = 2, PN_GATE_SILU = 3 };
+typedef struct pn_residual_norm_desc {
+    const float *h;
+    const void *y, *z;
+    const float *post_gain, *chan_scale, *pre_gain;
+    float *h_out;
+    uint16_t *x;
+    int64_t ldh, ldy, ldz, ldho, ldx;
+    int64_t T, n;
+    int32_t row_type;             /* PN_ROWS_F32 or PN_ROWS_F16, of y and z */
+    int32_t gate;                 /* PN_GATE_*                              */
+    int32_t post;                 /* norm of y                              */
+    float scale, eps;
+} pn_residual_norm_desc;
+pn_status pn_residual_norm(const pn_residual_norm_desc *d, void *stream);
+
+/* Log probabilities of given tokens, entropy and the most probable
+ * alternatives of rows of logits: with p = softmax(scale * x) over a row's V
+ * entries
+ *   logp[r][j]     = ln p(tokens[r][j]);  -inf for a token outside 0..V-1
+ *   entropy[r]     = - sum p ln p
+ *   top_ids[r][i], top_logp[r][i] = the K entries of largest x, largest first,
+ *                    the lower index of equals, and their ln p
+ * An entry of -inf (a masked one) or NaN has p = 0 and is no alternative; +inf
+ * counts as the largest finite value.  Places past the alternatives there are
+ * get -1 and -inf.  A row without a finite entry gives -inf, entropy 0 and no
+ * alternatives.  ln p and entropy are computed in fp32 sums of fp64 and
+ * rounded once.
+ *   logits   : rows of row_type (PN_ROWS_*), ld >= V elements, any alignment
+ *              of its type
+ *   scale    : 2^-100 .. 2^64 (the inverse of a temperature)
+ *   tokens   : int32, rows of ld_tok >= n_tok; n_tok >= 0 (0: may be NULL, and
+ *              logp too); logp: rows of ld_lp >= n_tok
+ *   entropy  : or NULL
+ *   K        : 0 .. PN_LOGPROBS_MAX_TOP (0: top_ids and top_logp may be NULL);
+ *              rows of ld_top >= K
+ *   rows     : >= 0 (0 does nothing);  V 1..2^31-1;  rows * ceil(V / 1024) <
+ *              2^31, else PN_EUNSUPPORTED
+ *   ws       : device, 8-byte aligned, at least pn_logprobs_workspace bytes */
+#define PN_LOGPROBS_MAX_TOP 64
+size_t pn_logprobs_workspace(int64_t rows, int64_t V, int K);
+pn_status pn_logprobs(const void *logits, int row_type, int64_t ld, int64_t rows, int64_t V, float scale,
+                      const int32_t *tokens, int64_t ld_tok, int n_tok, float *logp, int64_t ld_lp, float *entropy,
+                      int K, int32_t *top_ids, float *top_logp, int64_t ld_top, void *ws, size_t ws_bytes,
+                      void *stream);
+
 /* Text for a status code. */
 const char *pn_status_str(pn_status e);
 
