@@ -29,7 +29,7 @@ EXPORTS = ("pn_weights_per_block", "pn_row_bytes", "pn_gemv", "pn_gemv2",
            "pn_get_gemv_kernel", "pn_dequantize", "pn_rotate", "pn_gemm_prefill", "pn_gemm_prefill_group",
            "pn_group_create", "pn_group_create_smallm", "pn_group_run", "pn_group_destroy", "pn_gemv_batch",
            "pn_kv4_page_bytes", "pn_kv4_plan", "pn_kv4_store", "pn_kv4_load", "pn_kv4_attn_workspace",
-           "pn_kv4_attn", "pn_spec_workspace", "pn_spec_verify",
+           "pn_kv4_attn", "pn_kv4_attn_shared_workspace", "pn_kv4_attn_shared", "pn_spec_workspace", "pn_spec_verify",
            "pn_residual_norm", "pn_logprobs_workspace", "pn_logprobs",
            "pn_read_probe_scratch_bytes", "pn_read_probe", "pn_status_str", "pn_last_variant",
            "pn_variant_name")
@@ -146,6 +146,11 @@ def lib():
     L.pn_kv4_attn.argtypes = [cache, vp, i64, i32, vp, vp, vp, i64, i32, i64, i64, i64, ctypes.c_float, i32, i32,
                               vp, i64, vp, ctypes.c_size_t, vp]
     L.pn_kv4_attn.restype = i32
+    L.pn_kv4_attn_shared_workspace.argtypes = [cache, i32, i32, i32, i64, i64, i64, i64]
+    L.pn_kv4_attn_shared_workspace.restype = ctypes.c_size_t
+    L.pn_kv4_attn_shared.argtypes = [cache, vp, i64, i32, vp, vp, vp, i64, i32, vp, vp, i64, vp, i32, i64, i64, i64, i64,
+                                     ctypes.c_float, vp, i64, vp, ctypes.c_size_t, vp]
+    L.pn_kv4_attn_shared.restype = i32
     L.pn_spec_workspace.argtypes = [i32, i64]
     L.pn_spec_workspace.restype = ctypes.c_size_t
     L.pn_spec_verify.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i64, i32, i32, i64, vp, i64, vp, vp,
@@ -429,6 +434,21 @@ def pn_kv4_attn(cache, q, ldq, q_heads, q_start, kv_len, table, ld_table, B, tot
                            ws_bytes, _stream(stream))
     if check:
         _check(st, "pn_kv4_attn")
+    return st
+
+
+def pn_kv4_attn_shared_workspace(cache, q_heads, B, G, total_q, max_q, max_kv, max_shared):
+    return lib().pn_kv4_attn_shared_workspace(cache.ref, q_heads, B, G, total_q, max_q, max_kv, max_shared)
+
+
+def pn_kv4_attn_shared(cache, q, ldq, q_heads, q_start, kv_len, table, ld_table, B, g_start, prefix, ld_prefix, shared,
+                       G, total_q, max_q, max_kv, max_shared, scale, out, ldo, ws, ws_bytes, stream=None, check=True):
+    """Attention of a ragged batch whose groups of requests share their first pages."""
+    st = lib().pn_kv4_attn_shared(cache.ref, _ptr(q), ldq, q_heads, _ptr(q_start), _ptr(kv_len), _ptr(table), ld_table, B,
+                                  _ptr(g_start), _ptr(prefix), ld_prefix, _ptr(shared), G, total_q, max_q, max_kv,
+                                  max_shared, scale, _ptr(out), ldo, _ptr(ws), ws_bytes, _stream(stream))
+    if check:
+        _check(st, "pn_kv4_attn_shared")
     return st
 
 

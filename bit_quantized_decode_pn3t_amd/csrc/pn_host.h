@@ -39,6 +39,7 @@ enum Variant {
     kVarKv4Prompt = 23,
     kVarResidualNorm = 24,
     kVarLogprobs = 25,
+    kVarKv4AttnShared = 26,
 };
 
 extern thread_local int g_last_variant;

@@ -1050,6 +1050,7 @@ const char *pn_variant_name(int v)
     case kVarKv4Prompt: return "kv4_prompt";
     case kVarResidualNorm: return "residual_norm";
     case kVarLogprobs: return "logprobs";
+    case kVarKv4AttnShared: return "kv4_attn_shared";
     }
     return "unknown";
 }

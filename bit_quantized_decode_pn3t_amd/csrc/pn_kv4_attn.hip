@@ -110,15 +110,27 @@ struct AttnArgs {
     int32_t queries, grow;   // of a row tile; what a tile's length is more than the last one's (Cost)
     int32_t over;            // what an item's start and end cost, in steps
     int32_t negate;          // scale < 0: the queries are negated
+    // Of kFront and kTail:
+    const int32_t *g_start, *g_pages;  // the groups' first requests, the pages they share
+    int32_t *skip;           // [request]: its pages that the group's part stands for
+    float *front;            // [query][query head][D]: sums over the shared keys, in the products' order
+    float2 *front_ml;        // their maxima and sums of weights
+    int32_t requests, groups, max_shared;
     float c2;                // |scale| log2(e), above 0
     float slack;             // 4 / c2
 };
+
+// What a launch computes.  kWhole: attention.  For requests that share their
+// first keys (pn_kv4_attn_shared): kFront, the queries of a whole group against
+// the keys that it shares, left as sums with their maxima; kTail, each
+// request's queries against its own keys, joined with those sums.
+enum Pass { kWhole = 0, kFront = 1, kTail = 2 };
 
 // An item whose steps go on in the workgroups behind this one.
 struct Cutoff {
     int64_t q0;          // the request's first query
     int32_t row0, rows;  // of the tile, of the request
-    int32_t head;
+    int32_t head;        // kTail: | kJoined where the shared keys' sums are to be added
     int32_t parts;       // workgroups that work on it; 0: none is unfinished
 };
 
@@ -128,14 +140,32 @@ struct Request {
     int32_t qn;       // queries of the request that are computed
     int32_t first;    // position of query 0
     int32_t len;      // keys
+    int32_t skip;     // kTail: pages ahead of them, whose sums exist
 };
+constexpr int32_t kJoined = 1 << 30;
 struct Work : Request {
     int32_t sink_steps, lo, steps;  // steps [0, sink_steps), then from lo; steps in all
 };
 
-__device__ __forceinline__ Request request(const AttnArgs &a, int b)
+// Request b; of kFront, group b as one request that sees all of its keys.
+template <int PASS> __device__ __forceinline__ Request request(const AttnArgs &a, int b)
 {
     Request w;
+    w.skip = 0;
+    if constexpr (PASS == kFront) {
+        int32_t b0 = a.g_start[b], b1 = a.g_start[b + 1], n = a.g_pages[b];
+        b0 = b0 < 0 ? 0 : b0 > a.requests ? a.requests : b0;
+        b1 = b1 < b0 ? b0 : b1 > a.requests ? a.requests : b1;
+        n = n < 0 ? 0 : n > a.max_shared ? a.max_shared : n;
+        int64_t q0 = a.q_start[b0], q1 = a.q_start[b1];
+        q0 = q0 < 0 ? 0 : q0 > a.total_q ? a.total_q : q0;
+        q1 = q1 < q0 ? q0 : q1 > a.total_q ? a.total_q : q1;
+        w.q0 = q0;
+        w.qn = n > 0 ? (int32_t)(q1 - q0) : 0;
+        w.len = (int64_t)n << a.c.shift < a.max_kv ? n << a.c.shift : (int32_t)a.max_kv;
+        w.first = w.len;
+        return w;
+    }
     int64_t q0 = a.q_start[b], q1 = a.q_start[b + 1];
     q0 = q0 < 0 ? 0 : q0 > a.total_q ? a.total_q : q0;
     q1 = q1 < q0 ? q0 : q1 > a.total_q ? a.total_q : q1;
@@ -144,7 +174,33 @@ __device__ __forceinline__ Request request(const AttnArgs &a, int b)
     w.first = (int32_t)(kv - (q1 - q0));
     w.qn = (int32_t)(q1 - q0 < a.max_q ? q1 - q0 : a.max_q);
     w.len = kv < a.max_kv ? kv : (int32_t)a.max_kv;
+    if constexpr (PASS == kTail) {
+        w.skip = a.skip[b];
+        const int32_t ahead = w.skip << a.c.shift;
+        w.first -= ahead;  // not below 0: group_skips
+        w.len = w.len > ahead ? w.len - ahead : 0;
+    }
     return w;
+}
+
+// kFront: what kTail's requests leave to the groups.  A request takes its
+// group's part if all of its queries stand behind the shared pages.
+__device__ __forceinline__ void group_skips(const AttnArgs &a)
+{
+    for (int b = threadIdx.x; b < a.requests; b += blockDim.x) {
+        int lo = 0, hi = a.groups;  // the last group that starts at b or before
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.g_start[mid] <= b) lo = mid;
+            else hi = mid;
+        }
+        const int32_t b0 = a.g_start[lo], b1 = a.g_start[lo + 1];
+        int32_t n = a.g_pages[lo];
+        n = n < 0 ? 0 : n > a.max_shared ? a.max_shared : n;
+        const Request w = request<kWhole>(a, b);
+        const bool in = b0 <= b && b < b1 && w.qn > 0 && w.first >= 0 && (int64_t)n << a.c.shift <= w.first;
+        a.skip[b] = in ? n : 0;
+    }
 }
 
 // The steps of STEP tokens that queries i0 .. i1 of the request can see.
@@ -192,11 +248,11 @@ struct Cost {
     int32_t tiles, base, grow, top;
 };
 
-template <int STEP>
+template <int STEP, int PASS>
 __device__ __forceinline__ Cost cost(const AttnArgs &a, int b, int tile_rows)
 {
     Cost c;
-    c.w = request(a, b);
+    c.w = request<PASS>(a, b);
     c.tiles = c.base = c.top = c.grow = 0;
     if (c.w.qn < 1) return c;
     c.tiles = (c.w.qn * a.group + tile_rows - 1) / tile_rows;
@@ -236,13 +292,14 @@ __device__ __forceinline__ int64_t uniform64(int64_t v)
 {
     return (int64_t)(((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32) | (uint32_t)uniform((int)v));
 }
-__device__ __forceinline__ Cost scalar(const Cost &m)
+template <int PASS> __device__ __forceinline__ Cost scalar(const Cost &m)
 {
     Cost c;
     c.w.q0 = uniform64(m.w.q0);
     c.w.qn = uniform(m.w.qn);
     c.w.first = uniform(m.w.first);
     c.w.len = uniform(m.w.len);
+    c.w.skip = PASS == kTail ? uniform(m.w.skip) : 0;
     c.tiles = uniform(m.tiles);
     c.base = uniform(m.base);
     c.grow = uniform(m.grow);
@@ -270,7 +327,7 @@ struct Line {
 // Up to 64 requests are summed by every wave for itself and kept in LDS; more
 // are summed by the workgroup and read again as they come.  False: nothing is
 // left for this workgroup.
-template <int STEP>
+template <int STEP, int PASS>
 __device__ __forceinline__ bool line_part(const AttnArgs &a, LineLds &s, Line &t, int tile_rows)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -278,11 +335,11 @@ __device__ __forceinline__ bool line_part(const AttnArgs &a, LineLds &s, Line &t
     const int per = (a.B + kThreads - 1) / kThreads;
     int64_t mine = 0, total = 0, before = 0;
     if (t.few) {
-        const Cost c = cost<STEP>(a, lane < a.B ? lane : 0, tile_rows);
+        const Cost c = cost<STEP, PASS>(a, lane < a.B ? lane : 0, tile_rows);
         mine = lane < a.B ? length(a, c) : 0;
         if (wave == 0) s.known[lane] = c;
     } else {
-        for (int b = tid * per; b < (tid + 1) * per && b < a.B; ++b) mine += length(a, cost<STEP>(a, b, tile_rows));
+        for (int b = tid * per; b < (tid + 1) * per && b < a.B; ++b) mine += length(a, cost<STEP, PASS>(a, b, tile_rows));
     }
     int64_t sum = mine;
 #pragma unroll
@@ -322,7 +379,7 @@ __device__ __forceinline__ bool line_part(const AttnArgs &a, LineLds &s, Line &t
         if (here) {
             int x = tid * per;
             for (;; ++x) {
-                const int64_t n = length(a, cost<STEP>(a, x, tile_rows));
+                const int64_t n = length(a, cost<STEP, PASS>(a, x, tile_rows));
                 if (t.lo < before + n) break;
                 before += n;
             }
@@ -351,10 +408,10 @@ __device__ __forceinline__ int share_of(int32_t s, int32_t all, int steps)
 }
 
 // Go on along the line from x; false: a stretch without an item's steps.
-template <int STEP>
+template <int STEP, int PASS>
 __device__ __forceinline__ bool next_item(const AttnArgs &a, const LineLds &s, Line &t, int64_t &x, Item &m, int tile_rows)
 {
-    m.c = scalar(t.few ? s.known[t.b] : cost<STEP>(a, t.b, tile_rows));
+    m.c = scalar<PASS>(t.few ? s.known[t.b] : cost<STEP, PASS>(a, t.b, tile_rows));
     const bool single = m.c.tiles == 1;  // most requests: few instructions, which is what an item's start costs
     const int32_t n = single ? 0 : growing(m.c);
     const int64_t head_len = single ? m.c.base : before_tile(m.c, n, m.c.tiles);
@@ -402,7 +459,7 @@ __device__ __forceinline__ bool next_item(const AttnArgs &a, const LineLds &s, L
     m.tile0 = tile * tile_rows;
     m.rows = m.c.w.qn * a.group;
     if (m.s0 == 0 && m.cut && threadIdx.x == 0)
-        a.cuts[blockIdx.x] = {m.c.w.q0, m.tile0, m.rows, m.head, (int)quotient(first + one - 1, t.share) - (int)blockIdx.x + 1};
+        a.cuts[blockIdx.x] = {m.c.w.q0, m.tile0, m.rows, m.c.w.skip > 0 ? m.head | kJoined : m.head, (int)quotient(first + one - 1, t.share) - (int)blockIdx.x + 1};
     return true;
 }
 
@@ -455,14 +512,14 @@ struct Pages {
     int32_t p[2];
 };
 
-__device__ __forceinline__ Pages pages_of(const AttnArgs &a, const int32_t *row, int step, bool there)
+__device__ __forceinline__ Pages pages_of(const AttnArgs &a, const int32_t *row, int32_t max_pages, int step, bool there)
 {
     Pages t;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         // (no branch around a load: all of a call's are on their way at once)
         const int at = (step * kStep + 16 * i) >> a.c.shift;
-        const bool in = there && at < a.max_pages;
+        const bool in = there && at < max_pages;
         const int32_t p = ((const PN_CONST int32_t *)row)[uniform(in ? at : 0)];
         t.p[i] = in ? p : -1;
     }
@@ -882,7 +939,27 @@ template <int D, int NT, int RG> struct Shape {
 // 73 and 80 us).
 template <int D, int NT, int RG> constexpr int waves_per_simd() { return D < 256 && NT == 1 && RG == 1 ? 4 : 2; }
 
-template <int D, int NT, int RG>
+// A row's place in the shared keys' sums: product i of block y, lane group g.
+template <int D>
+__device__ __forceinline__ float4_t *front_of(const AttnArgs &a, int64_t query, int head, int y, int i, int g)
+{
+    return (float4_t *)(a.front + (query * a.q_heads + head) * D + ((4 * y + i) * 4 + g) * 4);
+}
+
+// The sums of a row's own keys (m, l) and of the shared ones (front) as one:
+// the factors of both, normalized.  Both are 0 where nothing is visible.
+struct Both {
+    float own, front;
+};
+__device__ __forceinline__ Both join_front(float m, float l, float2 front, float c2)
+{
+    const float top = max2(m, front.x);
+    const float f = __builtin_amdgcn_exp2f((m - top) * c2), f1 = __builtin_amdgcn_exp2f((front.x - top) * c2);
+    const float all = l * f + front.y * f1, by = all > 0.0f ? 1.0f / all : 0.0f;
+    return {f * by, f1 * by};
+}
+
+template <int D, int NT, int RG, int PASS>
 __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_attn(AttnArgs a)
 {
     using G = Ring<D>;
@@ -899,13 +976,14 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
     half8_t *queries = (half8_t *)(lds + S::kRing), *q = queries + rg * NT * 2 * R * 64;
 
     Line line;
-    if (!line_part<kStep>(a, line_lds, line, kRows)) return;
+    if (PASS == kFront && blockIdx.x == 0) group_skips(a);
+    if (!line_part<kStep, PASS>(a, line_lds, line, kRows)) return;
     Offsets<D> off;
     off.set(lane, 1 << a.c.shift);
 
     for (int64_t x = line.lo; x < line.hi;) {
         Item item;
-        if (!next_item<kStep>(a, line_lds, line, x, item, kRows)) continue;
+        if (!next_item<kStep, PASS>(a, line_lds, line, x, item, kRows)) continue;
         const int s0 = item.s0, head = item.head, tile0 = item.tile0, rows = item.rows, b = line.b;
         const bool cut = item.cut;
 
@@ -922,13 +1000,14 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
         int e = share_of(s0, item.all, w.steps);
         const int turns = (e1 - e + KW - 1) / KW;  // the same for all waves
         e += kg;
-        const int32_t *row = uniform_ptr(a.table + (int64_t)b * a.ld_table);
+        const int32_t max_pages = a.max_pages - w.skip;  // 0: no keys of its own, and no entry behind the row's end is read
+        const int32_t *row = uniform_ptr(a.table + (int64_t)b * a.ld_table + (max_pages > 0 ? w.skip : 0));
         const uint64_t head_base = (uint64_t)a.c.pages + (uint64_t)head * a.c.chunk;
         const int32_t page_bytes = a.c.heads * a.c.chunk;
         // pages of the steps in the ring, and of the next to be staged
         Pages held[S::kAhead + 1];
 #pragma unroll
-        for (int i = 0; i <= S::kAhead; ++i) held[i] = pages_of(a, row, place(e + KW * i), e + KW * i < e1);
+        for (int i = 0; i <= S::kAhead; ++i) held[i] = pages_of(a, row, max_pages, place(e + KW * i), e + KW * i < e1);
         // the queries into LDS
         for (int y = tid; y < RG * NT * 2 * R * 64; y += kThreads) {
             const int at = tile0 + 16 * (y / (2 * R * 64)) + (y & 15), i = at / a.group;
@@ -999,7 +1078,7 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
 #pragma unroll
             for (int y = 0; y < S::kAhead; ++y) held[y] = held[y + 1];
             const int s = e + KW * (S::kAhead + 1);
-            held[S::kAhead] = pages_of(a, row, place(s), s < e1);
+            held[S::kAhead] = pages_of(a, row, max_pages, place(s), s < e1);
         }
         wait_loads<0>();  // nothing is written into the ring any more
 
@@ -1024,14 +1103,25 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
             for (int y = 0; y < KW; ++y)
                 all_l += ml[rg * KW + y][16 * n + r][1] * __builtin_amdgcn_exp2f((ml[rg * KW + y][16 * n + r][0] - m) * a.c2);
             float f = __builtin_amdgcn_exp2f((st.m[n] - m) * a.c2) * down;
-            if (!cut) f = all_l > 0.0f ? f / all_l : 0.0f;
             const int row_at = row0 + 16 * n + r, i = row_at / a.group;
             const bool live = row_at < rows;
-            uint16_t *out = a.out + (w.q0 + i) * a.ldo + (int64_t)(head * a.group + row_at - i * a.group) * D;
+            const int q_head = head * a.group + row_at - i * a.group;
+            uint16_t *out = a.out + (w.q0 + i) * a.ldo + (int64_t)q_head * D;
+            Both both = {0.0f, 0.0f};
+            const bool joined = PASS == kTail && !cut && w.skip > 0;  // the same for the item
+            if (joined) {
+                both = join_front(m, all_l, live ? a.front_ml[(w.q0 + i) * a.q_heads + q_head] : make_float2(kLowest, 0.0f), a.c2);
+                f *= both.own;
+            } else if (PASS != kFront && !cut) {
+                f = all_l > 0.0f ? f / all_l : 0.0f;
+            }
             auto give = [&](float4_t v, int y, int i4) {  // block y, product i4
                 if (cut) {
                     if (live) part[((rg * NT + n) * 4 * R + 4 * y + i4) * 64 + lane] = v;
+                } else if constexpr (PASS == kFront) {
+                    if (live) *front_of<D>(a, w.q0 + i, q_head, y, i4, g) = v;
                 } else {
+                    if (joined && live) v += *front_of<D>(a, w.q0 + i, q_head, y, i4, g) * both.front;
                     store_row(live ? out : nullptr, v, y, i4, g);
                 }
             };
@@ -1065,6 +1155,8 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
                 }
             }
             if (cut && kg == 0 && g == 0) a.part_ml[(int64_t)part_at * kRows + (rg * NT + n) * 16 + r] = make_float2(m, all_l);
+            if (PASS == kFront && !cut && kg == 0 && g == 0 && live)
+                a.front_ml[(w.q0 + i) * a.q_heads + q_head] = make_float2(m, all_l);
         }
         __syncthreads();
     }
@@ -1109,7 +1201,7 @@ template <int D> struct Raw {
     uint32_t s[2 * (D / 64)];
 };
 
-template <int D, int NT>
+template <int D, int NT, int PASS>
 __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
 {
     using P = Prompt<D, NT>;
@@ -1132,10 +1224,11 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
     const int part = keys ? unit % (D / 32) : unit % (D / 8);
     const int token = keys ? unit / (D / 32) : unit / (D / 8) * 4;  // of the step
     Line line;
-    if (!line_part<kPromptStep>(a, line_lds, line, kRows)) return;
+    if (PASS == kFront && blockIdx.x == 0) group_skips(a);
+    if (!line_part<kPromptStep, PASS>(a, line_lds, line, kRows)) return;
     for (int64_t x = line.lo; x < line.hi;) {
         Item item;
-        if (!next_item<kPromptStep>(a, line_lds, line, x, item, kRows)) continue;
+        if (!next_item<kPromptStep, PASS>(a, line_lds, line, x, item, kRows)) continue;
         const int head = item.head, tile0 = item.tile0, rows = item.rows, b = line.b;
         Work w{item.c.w};
         const int tile_last = (tile0 + kRows < rows ? tile0 + kRows : rows) - 1;
@@ -1177,14 +1270,15 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
             const int e = e0 + i;
             return (e < w.sink_steps ? e : e - w.sink_steps + w.lo) * kPromptStep;
         };
-        const int32_t *row = uniform_ptr(a.table + (int64_t)b * a.ld_table);
+        const int32_t max_pages = a.max_pages - w.skip;  // 0: no keys of its own, and no entry behind the row's end is read
+        const int32_t *row = uniform_ptr(a.table + (int64_t)b * a.ld_table + (max_pages > 0 ? w.skip : 0));
         // Page of the thread's token in step i.  Steps past the end repeat the last.
         auto page_of = [&](int i) {
             const int at = (token_of(i < count ? i : count - 1) + token) >> a.c.shift;
-            return ((const PN_GLOBAL int32_t *)row)[at < a.max_pages ? at : a.max_pages - 1];
+            return ((const PN_GLOBAL int32_t *)row)[at < max_pages ? at : max_pages - 1];
         };
         auto ok_page = [&](int32_t page, int i) {
-            return (uint32_t)page < (uint32_t)a.c.num_pages && (token_of(i) + token) >> a.c.shift < a.max_pages;
+            return (uint32_t)page < (uint32_t)a.c.num_pages && (token_of(i) + token) >> a.c.shift < max_pages;
         };
         // Start the loads of step i; without a branch, or a join of branches
         // would wait for them.  A page that is none of the cache reads page 0.
@@ -1469,13 +1563,39 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
             }
             continue;
         }
+        if constexpr (PASS == kFront) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float all_l = group_sum(l[n]);
+                const int row_at = row0 + 16 * n + r, i = row_at / a.group, q_head = head * a.group + row_at - i * a.group;
+                if (row_at < rows) {
+#pragma unroll
+                    for (int y = 0; y < 4 * R; ++y)
+                        *front_of<D>(a, w.q0 + i, q_head, y >> 2, y & 3, g) = o[n][y >> 2][y & 3] * down;
+                    if (g == 0) a.front_ml[(w.q0 + i) * a.q_heads + q_head] = make_float2(m[n], all_l);
+                }
+            }
+            continue;
+        }
         // By way of LDS into whole rows: a wave's rows lie where the
         // fragments were, a row's 16-byte pieces permuted by its number.
         lds_barrier();
         uint8_t *mine = lds + wave * (16 * NT * 2 * D);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float all_l = group_sum(l[n]), f = all_l > 0.0f ? down / all_l : 0.0f;
+            const float all_l = group_sum(l[n]);
+            float f = all_l > 0.0f ? down / all_l : 0.0f;
+            if constexpr (PASS == kTail) {
+                const int row_at = row0 + 16 * n + r, i = row_at / a.group, q_head = head * a.group + row_at - i * a.group;
+                if (w.skip > 0 && row_at < rows) {
+                    const Both both = join_front(m[n], all_l, a.front_ml[(w.q0 + i) * a.q_heads + q_head], a.c2);
+                    f = 1.0f;
+#pragma unroll
+                    for (int y = 0; y < 4 * R; ++y)
+                        o[n][y >> 2][y & 3] = o[n][y >> 2][y & 3] * (both.own * down) +
+                                              *front_of<D>(a, w.q0 + i, q_head, y >> 2, y & 3, g) * both.front;
+                }
+            }
 #pragma unroll
             for (int y = 0; y < 4 * R; ++y)
 #pragma unroll
@@ -1503,7 +1623,7 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
 // 4 heads, 16 requests of 8 queries and up to 5000 tokens, 64 items of about
 // 4 parts: 36 us in all with 4 waves, 40 with 8, 49 with 16; one token over
 // 65536 keys, 4 items of 63 parts: this launch 15, 9.5 and 7.9 us).
-template <int D, int W>
+template <int D, int W, int PASS>
 __global__ __launch_bounds__(64 * W) void kv4_join(AttnArgs a, int groups)
 {
     constexpr int R = D / 64, F = W / 4;  // F: waves that share a product's parts
@@ -1555,9 +1675,23 @@ __global__ __launch_bounds__(64 * W) void kv4_join(AttnArgs a, int groups)
         o = frag[wave][lane];
 #pragma unroll
         for (int x = 1; x < F; ++x) o += frag[4 * x + wave][lane];
-        const float f = l > 0.0f ? 1.0f / l : 0.0f;
-        uint16_t *out = a.out + (c.q0 + q) * a.ldo + (int64_t)(c.head * a.group + at - q * a.group) * D;
-        store_row(at < c.rows ? out : nullptr, o * f, y, wave, g);
+        const bool live = at < c.rows;
+        const int q_head = (c.head & ~kJoined) * a.group + at - q * a.group;
+        if constexpr (PASS == kFront) {
+            if (live) {
+                *front_of<D>(a, c.q0 + q, q_head, y, wave, g) = o;
+                if (y == 0 && wave == 0 && g == 0) a.front_ml[(c.q0 + q) * a.q_heads + q_head] = make_float2(m, l);
+            }
+            return;
+        }
+        float f = l > 0.0f ? 1.0f / l : 0.0f;
+        if (PASS == kTail && (c.head & kJoined) && live) {
+            const Both both = join_front(m, l, a.front_ml[(c.q0 + q) * a.q_heads + q_head], a.c2);
+            o = o * both.own + *front_of<D>(a, c.q0 + q, q_head, y, wave, g) * both.front;
+            f = 1.0f;
+        }
+        uint16_t *out = a.out + (c.q0 + q) * a.ldo + (int64_t)q_head * D;
+        store_row(live ? out : nullptr, o * f, y, wave, g);
     }
 }
 
@@ -1607,71 +1741,80 @@ Cut cut(const pn_kv4_cache *c, int q_heads, int B, int64_t max_q, int64_t max_kv
     return t;
 }
 
-template <int D, int NT, int RG> bool raise_one()
+template <int D, int NT, int RG, int PASS> bool raise_one()
 {
-    return hipFuncSetAttribute((const void *)kv4_attn<D, NT, RG>, hipFuncAttributeMaxDynamicSharedMemorySize,
+    return hipFuncSetAttribute((const void *)kv4_attn<D, NT, RG, PASS>, hipFuncAttributeMaxDynamicSharedMemorySize,
                                Shape<D, NT, RG>::kLds) == hipSuccess;
 }
 
-template <int D> bool raise_prompt()
+template <int D, int PASS> bool raise_prompt()
 {
-    return hipFuncSetAttribute((const void *)kv4_prompt<D, kPromptRows<D>>, hipFuncAttributeMaxDynamicSharedMemorySize,
+    return hipFuncSetAttribute((const void *)kv4_prompt<D, kPromptRows<D>, PASS>, hipFuncAttributeMaxDynamicSharedMemorySize,
                                Prompt<D, kPromptRows<D>>::kLds) == hipSuccess;
 }
 
-bool raise_lds()
+template <int PASS> bool raise_pass()
 {
-    return raise_one<64, 1, 1>() && raise_one<64, 2, 1>() && raise_one<64, 3, 1>() && raise_one<64, 4, 1>() &&
-           raise_one<128, 1, 1>() && raise_one<128, 2, 1>() && raise_one<128, 3, 1>() &&
-           raise_one<128, 4, 1>() && raise_one<256, 1, 1>() && raise_one<256, 2, 1>() &&
-           raise_one<256, 2, 4>() && raise_prompt<64>() && raise_prompt<128>();
+    return raise_one<64, 1, 1, PASS>() && raise_one<64, 2, 1, PASS>() && raise_one<64, 3, 1, PASS>() &&
+           raise_one<64, 4, 1, PASS>() && raise_one<128, 1, 1, PASS>() && raise_one<128, 2, 1, PASS>() &&
+           raise_one<128, 3, 1, PASS>() && raise_one<128, 4, 1, PASS>() && raise_one<256, 1, 1, PASS>() &&
+           raise_one<256, 2, 1, PASS>() && raise_one<256, 2, 4, PASS>() && raise_prompt<64, PASS>() &&
+           raise_prompt<128, PASS>();
 }
 
-template <int D, int NT, int RG>
+bool raise_lds() { return raise_pass<kWhole>() && raise_pass<kFront>() && raise_pass<kTail>(); }
+
+template <int D, int NT, int RG, int PASS>
 pn_status launch(const AttnArgs &a, hipStream_t s)
 {
     if (!once_per_device(kAttrKv4, raise_lds)) return PN_ELAUNCH;
-    hipLaunchKernelGGL((kv4_attn<D, NT, RG>), dim3((unsigned)a.workers), dim3(kThreads), (Shape<D, NT, RG>::kLds), s, a);
+    hipLaunchKernelGGL((kv4_attn<D, NT, RG, PASS>), dim3((unsigned)a.workers), dim3(kThreads), (Shape<D, NT, RG>::kLds), s, a);
     if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
     if (!a.whole) {
         const dim3 grid((unsigned)a.workers, D / 64, NT * RG);
-        if (RG > 1 || a.parts <= 4) hipLaunchKernelGGL((kv4_join<D, 4>), grid, dim3(256), 0, s, a, NT * RG);
-        else if (a.parts <= 32) hipLaunchKernelGGL((kv4_join<D, 8>), grid, dim3(512), 0, s, a, NT * RG);
-        else hipLaunchKernelGGL((kv4_join<D, 16>), grid, dim3(1024), 0, s, a, NT * RG);
+        if (RG > 1 || a.parts <= 4) hipLaunchKernelGGL((kv4_join<D, 4, PASS>), grid, dim3(256), 0, s, a, NT * RG);
+        else if (a.parts <= 32) hipLaunchKernelGGL((kv4_join<D, 8, PASS>), grid, dim3(512), 0, s, a, NT * RG);
+        else hipLaunchKernelGGL((kv4_join<D, 16, PASS>), grid, dim3(1024), 0, s, a, NT * RG);
         if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
     }
     return PN_OK;
 }
 
-template <int D, int NT>
+template <int D, int NT, int PASS>
 pn_status launch_prompt(const AttnArgs &a, hipStream_t s)
 {
     if (!once_per_device(kAttrKv4, raise_lds)) return PN_ELAUNCH;
-    hipLaunchKernelGGL((kv4_prompt<D, NT>), dim3((unsigned)a.workers), dim3(kThreads), (Prompt<D, NT>::kLds), s, a);
+    hipLaunchKernelGGL((kv4_prompt<D, NT, PASS>), dim3((unsigned)a.workers), dim3(kThreads), (Prompt<D, NT>::kLds), s, a);
     if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
     if (!a.whole) {
-        hipLaunchKernelGGL((kv4_join<D, 4>), dim3((unsigned)a.workers, D / 64, NT * kWaves), dim3(256), 0, s, a, NT * kWaves);
+        hipLaunchKernelGGL((kv4_join<D, 4, PASS>), dim3((unsigned)a.workers, D / 64, NT * kWaves), dim3(256), 0, s, a, NT * kWaves);
         if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
     }
     return PN_OK;
 }
 
-template <int D>
+template <int D, int PASS>
 pn_status launch_rows(const AttnArgs &a, const Cut &t, hipStream_t s)
 {
     constexpr int most = D == 256 ? 2 : 4;
     if constexpr (D == 256) {
-        if (t.rg > 1) return launch<D, most, 4>(a, s);
+        if (t.rg > 1) return launch<D, most, 4, PASS>(a, s);
     } else {
-        if (t.rg > 1) return launch_prompt<D, kPromptRows<D>>(a, s);
+        if (t.rg > 1) return launch_prompt<D, kPromptRows<D>, PASS>(a, s);
     }
-    if (t.nt == 1) return launch<D, 1, 1>(a, s);
-    if (t.nt == 2) return launch<D, 2, 1>(a, s);
+    if (t.nt == 1) return launch<D, 1, 1, PASS>(a, s);
+    if (t.nt == 2) return launch<D, 2, 1, PASS>(a, s);
     if constexpr (D <= 128) {
-        if (t.nt == 3) return launch<D, 3, 1>(a, s);
-        if (t.nt == 4) return launch<D, 4, 1>(a, s);
+        if (t.nt == 3) return launch<D, 3, 1, PASS>(a, s);
+        if (t.nt == 4) return launch<D, 4, 1, PASS>(a, s);
     }
     return PN_EUNSUPPORTED;
+}
+
+template <int PASS> pn_status launch_pass(const AttnArgs &a, const Cut &t, int dim, hipStream_t s)
+{
+    return dim == 64 ? launch_rows<64, PASS>(a, t, s) : dim == 128 ? launch_rows<128, PASS>(a, t, s)
+                                                                   : launch_rows<256, PASS>(a, t, s);
 }
 
 bool sizes_ok(const pn_kv4_cache *c, int q_heads, int B, int64_t total_q, int64_t max_q, int64_t max_kv, int sinks)
@@ -1685,6 +1828,65 @@ bool sizes_fit(const pn_kv4_cache *c, int q_heads, int B, int64_t total_q, int64
     return B <= 65535 && q_heads <= 65535 && total_q <= INT32_MAX / 2 && max_kv <= INT32_MAX / 2 &&
            max_q * (q_heads / c->heads) <= INT32_MAX / 4;
 }
+
+bool shared_fit(const pn_kv4_cache *c, int q_heads, int B, int G, int64_t total_q, int64_t max_q, int64_t max_kv,
+                int64_t max_shared)
+{
+    return sizes_fit(c, q_heads, B, total_q, max_q, max_kv) && G <= 65535 && max_shared <= INT32_MAX / 2 / c->page_size &&
+           total_q * (q_heads / c->heads) <= INT32_MAX / 4;
+}
+
+bool scale_ok(float scale) { return __builtin_fabsf(scale) <= 0x1.fffffep127f; }  // not infinite or NaN
+
+void set_scale(AttnArgs &a, float scale)
+{
+    a.negate = scale < 0.0f;
+    // Not 0: a masked score is -inf, whose product with c2 has to stay so.
+    a.c2 = __builtin_fmaxf(__builtin_fabsf(scale) * 1.4426950408889634f, 0x1p-100f);
+    a.slack = 4.0f / a.c2;
+}
+
+// The parts' memory of a launch cut by t, and fewer workgroups (or items that
+// are not cut) where there is not room for all.
+void set_cut(AttnArgs &a, const pn_kv4_cache *cache, Cut &t, void *ws, size_t ws_bytes)
+{
+    if (!t.whole && ws_bytes < t.workers * t.part) {
+        // As many workgroups as there is room for, while that leaves most of
+        // the device at work; else every item is one workgroup's.
+        const int fit = (int)(ws_bytes / t.part);
+        if (fit >= t.workers / 4) t.workers = fit;
+        else t.whole = true;
+    }
+    a.part = (float *)ws;
+    const size_t groups = 2 * (size_t)t.workers * t.nt * t.rg;
+    a.part_ml = (float2 *)(a.part + groups * cache->dim * 16);
+    a.cuts = (Cutoff *)(a.part_ml + groups * 16);
+    a.workers = t.workers;
+    a.two = t.two;
+    a.parts = t.parts;
+    const int tile_rows = 16 * t.nt * t.rg;
+    a.queries = (tile_rows + a.group - 1) / a.group;
+    a.grow = tile_rows * kUnit / (a.group * (t.rg == kWaves ? kPromptStep : kStep));
+    a.whole = t.whole;
+    // What an item's start and end cost in steps.  64 wide, 64 requests of up
+    // to 16384: 54 us, counted as nothing 80, twice as much 57; 128 wide, a
+    // prompt of 4096 with 16 heads: 149 us, nothing 185, twice 162.
+    a.over = t.rg == kWaves ? 6 : 32;
+}
+
+// The front pass of a call: as one request a group, of about as many queries
+// as a group has.
+Cut cut_front(const pn_kv4_cache *c, int q_heads, int G, int64_t total_q, int64_t max_shared)
+{
+    return cut(c, q_heads, G, (total_q + G - 1) / G, max_shared * c->page_size, 0, 0);
+}
+
+size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+// Bytes of the groups' sums, of their maxima and weights, of the requests' skips.
+size_t front_bytes(const pn_kv4_cache *c, int q_heads, int64_t total_q) { return (size_t)total_q * q_heads * c->dim * sizeof(float); }
+size_t front_ml_bytes(int q_heads, int64_t total_q) { return round16((size_t)total_q * q_heads * sizeof(float2)); }
+size_t skip_bytes(int B) { return round16((size_t)B * sizeof(int32_t)); }
 
 }  // namespace
 
@@ -1704,11 +1906,11 @@ extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, i
                                  int B, int64_t total_q, int64_t max_q, int64_t max_kv, float scale, int window,
                                  int sinks, uint16_t *out, int64_t ldo, void *ws, size_t ws_bytes, void *stream)
 {
-    AttnArgs a;
+    AttnArgs a = {};
     if (const pn_status st = check_cache(cache, &a.c)) return st;
     if (!q || !q_start || !kv_len || !table || !out || (!ws && ws_bytes)) return PN_EINVAL;
     if (!sizes_ok(cache, q_heads, B, total_q, max_q, max_kv, sinks)) return PN_ESHAPE;
-    if (!(__builtin_fabsf(scale) <= 0x1.fffffep127f)) return PN_ESHAPE;  // infinite or NaN
+    if (!scale_ok(scale)) return PN_ESHAPE;
     const int64_t cols = (int64_t)q_heads * cache->dim;
     if (ldq < cols || ldo < cols) return PN_ESHAPE;
     const int64_t pages = (max_kv + cache->page_size - 1) / cache->page_size;
@@ -1720,22 +1922,11 @@ extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, i
     if (!sizes_fit(cache, q_heads, B, total_q, max_q, max_kv)) return PN_EUNSUPPORTED;
     if (total_q == 0) return PN_OK;
     Cut t = cut(cache, q_heads, B, max_q, max_kv, window, sinks);
-    if (!t.whole && ws_bytes < t.workers * t.part) {
-        // As many workgroups as there is room for, while that leaves most of
-        // the device at work; else every item is one workgroup's.
-        const int fit = (int)(ws_bytes / t.part);
-        if (fit >= t.workers / 4) t.workers = fit;
-        else t.whole = true;
-    }
     a.q = q;
     a.q_start = q_start;
     a.kv_len = kv_len;
     a.table = table;
     a.out = out;
-    a.part = (float *)ws;
-    const size_t groups = 2 * (size_t)t.workers * t.nt * t.rg;
-    a.part_ml = (float2 *)(a.part + groups * cache->dim * 16);
-    a.cuts = (Cutoff *)(a.part_ml + groups * 16);
     a.ldq = ldq;
     a.ldo = ldo;
     a.ld_table = ld_table;
@@ -1748,25 +1939,94 @@ extern "C" pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, i
     a.max_pages = (int)pages;
     a.window = window;
     a.sinks = sinks;
-    a.workers = t.workers;
-    a.two = t.two;
-    a.parts = t.parts;
-    const int tile_rows = 16 * t.nt * t.rg;
-    a.queries = (tile_rows + a.group - 1) / a.group;
-    a.grow = tile_rows * kUnit / (a.group * (t.rg == kWaves ? kPromptStep : kStep));
-    a.whole = t.whole;
-    // What an item's start and end cost in steps.  64 wide, 64 requests of up
-    // to 16384: 54 us, counted as nothing 80, twice as much 57; 128 wide, a
-    // prompt of 4096 with 16 heads: 149 us, nothing 185, twice 162.
-    a.over = t.rg == kWaves ? 6 : 32;
-    a.negate = scale < 0.0f;
-    // Not 0: a masked score is -inf, whose product with c2 has to stay so.
-    a.c2 = __builtin_fmaxf(__builtin_fabsf(scale) * 1.4426950408889634f, 0x1p-100f);
-    a.slack = 4.0f / a.c2;
-    const hipStream_t s = (hipStream_t)stream;
-    const pn_status st = cache->dim == 64    ? launch_rows<64>(a, t, s)
-                         : cache->dim == 128 ? launch_rows<128>(a, t, s)
-                                             : launch_rows<256>(a, t, s);
+    set_scale(a, scale);
+    set_cut(a, cache, t, ws, ws_bytes);
+    const pn_status st = launch_pass<kWhole>(a, t, cache->dim, (hipStream_t)stream);
     if (st == PN_OK) g_last_variant = t.rg == kWaves ? kVarKv4Prompt : kVarKv4Attn;
     return st;
+}
+
+extern "C" size_t pn_kv4_attn_shared_workspace(const pn_kv4_cache *cache, int q_heads, int B, int G, int64_t total_q,
+                                               int64_t max_q, int64_t max_kv, int64_t max_shared)
+{
+    Kv4 c;
+    if (check_cache(cache, &c) || !sizes_ok(cache, q_heads, B, total_q, max_q, max_kv, 0) || G < 1 || max_shared < 1 ||
+        total_q == 0)
+        return 0;
+    if (max_q > total_q) max_q = total_q;
+    if (!shared_fit(cache, q_heads, B, G, total_q, max_q, max_kv, max_shared)) return 0;
+    const Cut f = cut_front(cache, q_heads, G, total_q, max_shared), t = cut(cache, q_heads, B, max_q, max_kv, 0, 0);
+    const size_t parts_f = f.whole ? 0 : f.workers * f.part, parts_t = t.whole ? 0 : t.workers * t.part;
+    return front_bytes(cache, q_heads, total_q) + front_ml_bytes(q_heads, total_q) + skip_bytes(B) +
+           (parts_f > parts_t ? parts_f : parts_t);
+}
+
+extern "C" pn_status pn_kv4_attn_shared(const pn_kv4_cache *cache, const uint16_t *q, int64_t ldq, int q_heads,
+                                        const int32_t *q_start, const int32_t *kv_len, const int32_t *table,
+                                        int64_t ld_table, int B, const int32_t *g_start, const int32_t *prefix,
+                                        int64_t ld_prefix, const int32_t *shared, int G, int64_t total_q, int64_t max_q,
+                                        int64_t max_kv, int64_t max_shared, float scale, uint16_t *out, int64_t ldo,
+                                        void *ws, size_t ws_bytes, void *stream)
+{
+    AttnArgs a = {};
+    if (const pn_status st = check_cache(cache, &a.c)) return st;
+    if (!q || !q_start || !kv_len || !table || !g_start || !prefix || !shared || !out) return PN_EINVAL;
+    if (!sizes_ok(cache, q_heads, B, total_q, max_q, max_kv, 0) || G < 1 || max_shared < 1) return PN_ESHAPE;
+    if (!scale_ok(scale)) return PN_ESHAPE;
+    const int64_t cols = (int64_t)q_heads * cache->dim;
+    if (ldq < cols || ldo < cols) return PN_ESHAPE;
+    const int64_t pages = (max_kv + cache->page_size - 1) / cache->page_size;
+    if (ld_table < pages || ld_prefix < max_shared) return PN_ESHAPE;
+    const void *words[] = {q_start, kv_len, table, g_start, prefix, shared};
+    for (const void *p : words)
+        if (!aligned(p, 4)) return PN_EALIGN;
+    if (!aligned(q, 16) || !aligned(out, 16) || ldq % 8 || ldo % 8 || !aligned(ws, 16)) return PN_EALIGN;
+    if (max_q > total_q) max_q = total_q;  // no request has more
+    if (max_shared > pages) max_shared = pages;
+    if (!shared_fit(cache, q_heads, B, G, total_q, max_q, max_kv, max_shared)) return PN_EUNSUPPORTED;
+    if (total_q == 0) return PN_OK;
+    const size_t fixed = front_bytes(cache, q_heads, total_q) + front_ml_bytes(q_heads, total_q) + skip_bytes(B);
+    if (!ws) return PN_EINVAL;
+    if (ws_bytes < fixed) return PN_ESHAPE;
+    a.front = (float *)ws;
+    a.front_ml = (float2 *)((uint8_t *)ws + front_bytes(cache, q_heads, total_q));
+    a.skip = (int32_t *)((uint8_t *)a.front_ml + front_ml_bytes(q_heads, total_q));
+    void *parts = (uint8_t *)ws + fixed;
+    a.g_start = g_start;
+    a.g_pages = shared;
+    a.requests = B;
+    a.groups = G;
+    a.max_shared = (int)max_shared;
+    a.q = q;
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.out = out;
+    a.ldq = ldq;
+    a.ldo = ldo;
+    a.total_q = total_q;
+    a.max_kv = max_kv;
+    a.q_heads = q_heads;
+    a.group = q_heads / cache->heads;
+    set_scale(a, scale);
+    const hipStream_t s = (hipStream_t)stream;
+
+    Cut t = cut_front(cache, q_heads, G, total_q, max_shared);
+    a.table = prefix;
+    a.ld_table = ld_prefix;
+    a.max_pages = (int)max_shared;
+    a.max_q = total_q;  // of a group
+    a.B = G;
+    set_cut(a, cache, t, parts, ws_bytes - fixed);
+    if (const pn_status st = launch_pass<kFront>(a, t, cache->dim, s)) return st;
+
+    t = cut(cache, q_heads, B, max_q, max_kv, 0, 0);
+    a.table = table;
+    a.ld_table = ld_table;
+    a.max_pages = (int)pages;
+    a.max_q = max_q;
+    a.B = B;
+    set_cut(a, cache, t, parts, ws_bytes - fixed);
+    if (const pn_status st = launch_pass<kTail>(a, t, cache->dim, s)) return st;
+    g_last_variant = kVarKv4AttnShared;
+    return PN_OK;
 }

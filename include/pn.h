@@ -468,6 +468,38 @@ pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, int64_t ldq,
                       int64_t max_q, int64_t max_kv, float scale, int window, int sinks, uint16_t *out, int64_t ldo,
                       void *ws, size_t ws_bytes, void *stream);
 
+/* The same for requests that share a long prefix (a system prompt, a document):
+ * its keys and values are read and multiplied once for all of a group's
+ * queries, and joined with each request's own.  Group g is requests g_start[g]
+ * .. g_start[g+1] - 1, whose first shared[g] pages are prefix[g][0 ..
+ * shared[g] - 1]; requests outside of all groups have no prefix.
+ *   out as pn_kv4_attn (window 0), over the tokens t <= p: those below
+ *   shared[g] * page_size from the pages in prefix[g], the others from the
+ *   pages in the request's own row of table, at their own columns
+ * Columns below shared[g] of a table row are not read, unless a query of the
+ * request stands inside the shared pages: then all of that request's pages are
+ * its own row's (as pn_kv4_plan's rows hold them).  A prefix ends with a page;
+ * tokens behind its last whole page are each request's own.
+ *   g_start    : int32 [G + 1], not decreasing;  shared: int32 [G], below 1: none
+ *   prefix     : int32, G rows of ld_prefix >= max_shared
+ *   max_shared : >= 1, at least every shared[g] (of a larger one the first
+ *                max_shared pages are shared)
+ *   other arguments as for pn_kv4_attn
+ *   ws         : device, 16-byte aligned, at least total_q * q_heads * (4 dim
+ *                + 8) + 4 B bytes and the rounding of parts of it to 16 (else
+ *                PN_ESHAPE): room for the groups' sums.  What
+ *                pn_kv4_attn_shared_workspace says leaves room for splits, too
+ * PN_EUNSUPPORTED: as pn_kv4_attn; G > 65535, max_shared * page_size > 2^30 - 1
+ * or total_q * q_heads / heads > 2^29 - 1. */
+size_t pn_kv4_attn_shared_workspace(const pn_kv4_cache *cache, int q_heads, int B, int G, int64_t total_q,
+                                    int64_t max_q, int64_t max_kv, int64_t max_shared);
+pn_status pn_kv4_attn_shared(const pn_kv4_cache *cache, const uint16_t *q, int64_t ldq, int q_heads,
+                             const int32_t *q_start, const int32_t *kv_len, const int32_t *table, int64_t ld_table,
+                             int B, const int32_t *g_start, const int32_t *prefix, int64_t ld_prefix,
+                             const int32_t *shared, int G, int64_t total_q, int64_t max_q, int64_t max_kv,
+                             int64_t max_shared, float scale, uint16_t *out, int64_t ldo, void *ws, size_t ws_bytes,
+                             void *stream);
+
 /* Verification of drafted tokens against the target's probabilities, from
  * given random numbers u in [0, 1).  Request i has n = n_draft[i] drafts
  * (clamped to 0..k; NULL: k), target rows p_0 .. p_k and, with `draft`, rows
