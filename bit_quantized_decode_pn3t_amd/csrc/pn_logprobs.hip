@@ -5,15 +5,21 @@
 //   z_i = c (x_i - m), m = max x, c = scale log2(e);   S = sum exp2(z_i)
 //   ln p_i = ln 2 z_i - ln S,   entropy = ln S - ln 2 / S * sum exp2(z_i) z_i
 //
-// One pass over the logits.  A wave takes a span of a row and keeps, per lane,
-// the maximum so far, S (fp64, so that a row that is all but certain keeps the
-// rest of its sum) and the sum of the entropy; and, per wave, the 64 best
-// entries, sorted across the lanes.  An entry is tested against the K-th best;
-// those that pass are gathered in LDS and sorted in 64 at a time.  Entries are
-// ordered by one 64-bit key: the value, then the lower index.  Kernel
-// logp_spans leaves a span's sums and K keys in the workspace, logp_join, one
-// workgroup a row, joins them and looks the given tokens up.  No order of
-// results depends on timing.
+// One pass over the logits.  A lane keeps m, S (fp64, so that a row that is
+// all but certain keeps the rest of its sum) and the sum of the entropy.  A
+// wave keeps the 64 best entries, sorted across its lanes.
+// A step of 1024 entries is tested as a whole against the K-th best; entries
+// that pass are gathered in LDS and sorted in, 64 at a time.  The first step
+// starts from the K-th largest of the lanes' maxima, so that little more than
+// K entries pass.  Entries are ordered by one 64-bit key: the value, then the
+// lower index.  No order of results depends on timing.
+//
+// A workgroup's four waves step through a chunk of a row together (a row's
+// whole length where there are rows enough); the next step's loads, past the
+// caches, are in flight meanwhile.  Chunks of a row leave their sums and K
+// keys in the workspace, and logp_join joins them.
+#include <type_traits>
+
 #include "pn_device.h"
 #include "pn_kv4.h"
 
@@ -22,13 +28,12 @@ using namespace pn::host;
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
 constexpr int kTile = 1024;       // entries of a wave's step, 16 a lane
 constexpr float kLow = -__builtin_inff();
 constexpr float kBig = 0x1.fffffep127f;
+constexpr double kLn2 = 0.693147180559945309417;
 
-// What is left of a span: S and the entropy's sum relative to m.
+// What is left of a chunk: S and the entropy's sum relative to m.
 struct Sums {
     double s;
     float m, e;
@@ -39,63 +44,89 @@ struct LogpArgs {
     const int32_t *tokens;
     float *logp, *entropy, *top_logp;
     int32_t *top_ids;
-    Sums *sums;      // [row][span]
-    uint64_t *best;  // [row][span][K]
-    int64_t ld, ld_tok, ld_lp, ld_top, V, rows;
-    int32_t n_tok, K, spans, span;
-    float scale;
+    Sums *sums;      // [row][chunk]
+    uint64_t *best;  // [row][chunk][K]
+    int64_t ld, ld_tok, ld_lp, ld_top, V;
+    int32_t n_tok, K, chunks, chunk;
+    float scale, c;  // c = scale log2(e)
 };
 
 // NaN counts as -inf, +inf as the largest finite value.
-__device__ __forceinline__ float clean(float v) { return fminf(v == v ? v : kLow, kBig); }
+__device__ __forceinline__ float clean(float v) { return v == v ? (v < kBig ? v : kBig) : kLow; }
 
 // Larger for what comes first; 0 for nothing.  v is not NaN; -0 is +0.
-__device__ __forceinline__ uint64_t key_of(float v, uint32_t i)
+__device__ __forceinline__ uint32_t order_of(float v)
 {
     const uint32_t b = __float_as_uint(v + 0.0f);
-    return (uint64_t)((int32_t)b < 0 ? ~b : b | 0x80000000u) << 32 | (uint32_t)~i;
+    return (int32_t)b < 0 ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ float value_of(uint64_t key)
-{
-    const uint32_t b = (uint32_t)(key >> 32);
-    return __uint_as_float((int32_t)b < 0 ? b & 0x7fffffffu : ~b);
-}
+__device__ __forceinline__ float value_at(uint32_t order) { return __uint_as_float((int32_t)order < 0 ? order & 0x7fffffffu : ~order); }
+__device__ __forceinline__ uint64_t key_of(float v, uint32_t i) { return (uint64_t)order_of(v) << 32 | (uint32_t)~i; }
+__device__ __forceinline__ float value_of(uint64_t key) { return value_at((uint32_t)(key >> 32)); }
 __device__ __forceinline__ uint32_t index_of(uint64_t key) { return ~(uint32_t)key; }
 
-__device__ __forceinline__ uint64_t shuffle_xor(uint64_t v, int d)
+// The value of lane ^ X: data-parallel moves within 16 lanes, swaps of rows
+// and halves beyond them (a shuffle through LDS takes ten times as long).
+template <int CTRL> __device__ __forceinline__ uint32_t dpp(uint32_t v)
 {
-    return (uint64_t)(uint32_t)__shfl_xor((int)(v >> 32), d, 64) << 32 | (uint32_t)__shfl_xor((int)v, d, 64);
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
 }
-__device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint64_t smaller(uint64_t a, uint64_t b) { return a < b ? a : b; }
-
-// A bitonic sequence of 64 keys into descending order, lane 0 first.
-__device__ __forceinline__ uint64_t merge_down(uint64_t v, int lane)
+template <int X> __device__ __forceinline__ uint32_t across(uint32_t v, int lane)
 {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-        const uint64_t o = shuffle_xor(v, d);
-        v = lane & d ? smaller(v, o) : larger(v, o);
-    }
+    if constexpr (X == 1) return dpp<0xb1>(v);        // quad_perm 1 0 3 2
+    else if constexpr (X == 2) return dpp<0x4e>(v);   // quad_perm 2 3 0 1
+    else if constexpr (X == 3) return dpp<0x1b>(v);   // quad_perm 3 2 1 0
+    else if constexpr (X == 7) return dpp<0x141>(v);  // row_half_mirror
+    else if constexpr (X == 15) return dpp<0x140>(v); // row_mirror
+    else if constexpr (X == 8) return dpp<0x128>(v);  // row_ror 8
+    else if constexpr (X == 4) return across<7>(across<3>(v, lane), lane);
+    else if constexpr (X == 16) {
+        auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return lane & 16 ? s[0] : s[1];
+    } else if constexpr (X == 32) {
+        auto s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return lane & 32 ? s[0] : s[1];
+    } else if constexpr (X == 31) return across<16>(across<15>(v, lane), lane);
+    else return across<32>(across<31>(v, lane), lane);  // 63
+}
+template <int X> __device__ __forceinline__ uint64_t across(uint64_t v, int lane)
+{
+    return (uint64_t)across<X>((uint32_t)(v >> 32), lane) << 32 | across<X>((uint32_t)v, lane);
+}
+template <typename T> __device__ __forceinline__ T larger(T a, T b) { return a > b ? a : b; }
+
+// Lanes without bit H of lanes that differ in X keep the larger.
+template <int X, int H, typename T> __device__ __forceinline__ T exchange(T v, int lane)
+{
+    const T o = across<X>(v, lane);
+    return (v > o) == ((lane & H) == 0) ? v : o;
+}
+// A bitonic sequence of 2 D keys in descending order.
+template <int D, typename T> __device__ __forceinline__ T merge_down(T v, int lane)
+{
+    v = exchange<D, D>(v, lane);
+    if constexpr (D > 1) v = merge_down<D / 2>(v, lane);
     return v;
 }
-__device__ __forceinline__ uint64_t sort_down(uint64_t v, int lane)
+// The wave's 64 in descending order: sorted runs of N meet mirrored.
+template <int N = 2, typename T> __device__ __forceinline__ T sort_down(T v, int lane)
 {
-#pragma unroll
-    for (int k = 2; k < 64; k <<= 1)
-#pragma unroll
-        for (int d = k >> 1; d > 0; d >>= 1) {
-            const uint64_t o = shuffle_xor(v, d);
-            v = ((lane & d) != 0) == ((lane & k) != 0) ? larger(v, o) : smaller(v, o);
-        }
-    return merge_down(v, lane);
+    v = exchange<N - 1, N / 2>(v, lane);
+    if constexpr (N > 2) v = merge_down<N / 4>(v, lane);
+    if constexpr (N < 64) v = sort_down<2 * N>(v, lane);
+    return v;
+}
+// The best 64 of two sorted lists.
+__device__ __forceinline__ uint64_t best_of(uint64_t a, uint64_t b, int lane)
+{
+    return merge_down<32>(larger(a, across<63>(b, lane)), lane);
 }
 
 // The best 64 keys of a wave, and a buffer of those that may join them.
 struct Best {
     uint64_t list;   // this lane's of the sorted list
-    uint64_t least;  // the K-th best
-    float value;     // its value
+    uint64_t least;  // the K-th best, 0 as long as there are fewer
+    float value;     // what an entry has to reach
     int count;       // in the buffer
     uint64_t *buf;   // 128 keys of LDS, the wave's own
 
@@ -109,15 +140,13 @@ struct Best {
     // The first `many` of the buffer, 64 at most, into the list.
     __device__ __forceinline__ void take(int many, int K, int lane)
     {
-        const uint64_t v = sort_down(lane < many ? buf[lane] : 0, lane);
-        const uint64_t back = (uint64_t)(uint32_t)__shfl((int)(v >> 32), 63 - lane, 64) << 32 | (uint32_t)__shfl((int)v, 63 - lane, 64);
-        list = merge_down(larger(list, back), lane);
+        list = best_of(list, sort_down(lane < many ? buf[lane] : 0, lane), lane);
         least = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(list >> 32), K - 1) << 32 |
                 (uint32_t)__builtin_amdgcn_readlane((int)list, K - 1);
-        value = least ? value_of(least) : kLow;
+        if (least) value = fmaxf(value, value_of(least));
         const int rest = count - many;
-        const uint64_t v2 = lane < rest ? buf[64 + lane] : 0;
-        if (lane < rest) buf[lane] = v2;
+        const uint64_t v = lane < rest ? buf[64 + lane] : 0;
+        if (lane < rest) buf[lane] = v;
         count = rest;
     }
     __device__ __forceinline__ void push(uint64_t key, bool ok, int K, int lane)
@@ -136,16 +165,16 @@ struct Best {
     }
 };
 
-// A lane's running sums.
+// A lane's running sums; m is -inf as long as there is nothing.
 struct Running {
     double s;
     float m, e;
-    __device__ __forceinline__ void raise(float to, float c2)
+    __device__ __forceinline__ void raise(float to, float c)
     {
         if (to > m) {
-            const float f = __builtin_amdgcn_exp2f((m - to) * c2);
-            if (f > 0.0f) {  // (nothing so far, or all of it too small: as nothing)
-                e = f * (e - (to - m) * c2 * (float)s);
+            const float d = (m - to) * c, f = __builtin_amdgcn_exp2f(d);
+            if (f > 0.0f) {  // (else there is nothing, or all of it is too small)
+                e = f * __builtin_fmaf(d, (float)s, e);
                 s *= (double)f;
             } else {
                 e = 0.0f;
@@ -154,199 +183,244 @@ struct Running {
             m = to;
         }
     }
-    // v <= m
-    __device__ __forceinline__ void add(float v, float c2)
-    {
-        const float z = fmaxf((v - m) * c2, -kBig);
-        const float w = __builtin_amdgcn_exp2f(z);
-        s += (double)w;
-        e = __builtin_fmaf(w, z, e);
-    }
 };
 
 typedef float float4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef _Float16 half8_a2 __attribute__((ext_vector_type(8), aligned(2)));
 
-// A lane's 16 entries of a tile: vector j (of 4 or 8 entries) starts at
-// place(j); entries past `end` are -inf.
+// A lane's 16 entries of a step, as loaded: entry e is place(lane, e) of the
+// step; those at `end` and behind it are -inf.
 template <bool HALF> struct Tile {
     static constexpr int kVec = HALF ? 8 : 4;
+    using Vec = typename std::conditional<HALF, half8_a2, float4_a4>::type;
+    using One = typename std::conditional<HALF, _Float16, float>::type;
+    Vec w[16 / kVec];
     __device__ static constexpr int place(int lane, int e) { return (lane + 64 * (e / kVec)) * kVec + e % kVec; }
-    __device__ static __forceinline__ void load(float (&v)[16], const void *row, int64_t at, int64_t end, int lane)
+    __device__ __forceinline__ float at(int e) const { return (float)w[e / kVec][e % kVec]; }
+    __device__ __forceinline__ void load(const One *row, int64_t from, int64_t end, int lane)
     {
-        if (at + kTile <= end) {
-            if constexpr (HALF) {
-                half8_a2 w[2];
+        if (from + kTile <= end) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) w[j] = *(const half8_a2 *)((const _Float16 *)row + at + place(lane, 8 * j));
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = (float)w[e / 8][e % 8];
-            } else {
-                float4_a4 w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = *(const float4_a4 *)((const float *)row + at + place(lane, 4 * j));
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = w[e / 4][e % 4];
-            }
+            for (int j = 0; j < 16 / kVec; ++j) w[j] = __builtin_nontemporal_load((const Vec *)(row + from + place(lane, kVec * j)));
         } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const int64_t i = at + place(lane, e);
-                v[e] = kLow;
-                if (i < end) v[e] = HALF ? (float)((const _Float16 *)row)[i] : ((const float *)row)[i];
+                const int64_t i = from + place(lane, e);
+                One v = (One)kLow;
+                if (i < end) v = row[i];
+                w[e / kVec][e % kVec] = v;
             }
         }
     }
 };
 
+// One step into the wave's sums and best.
+template <bool HALF>
+__device__ __forceinline__ void step(const LogpArgs &a, const Tile<HALF> &tile, int64_t from, Running &r, Best &best, int lane)
+{
+    float v[16], top = kLow, low = kLow;
+    asm("" : "+s"(low));  // the compiler takes the median with a constant -inf for a minimum, which drops NaNs upwards
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        v[e] = __builtin_amdgcn_fmed3f(tile.at(e), low, kBig);  // as clean(): of a NaN the least of the others
+        top = fmaxf(top, v[e]);
+    }
+    if (top > kLow) {
+        r.raise(top, a.c);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float z = fmaxf((v[e] - r.m) * a.c, -kBig);  // not -inf, which times 0 is NaN
+            const float w = __builtin_amdgcn_exp2f(z);
+            r.s += (double)w;
+            r.e = __builtin_fmaf(w, z, r.e);
+        }
+    }
+    if (a.K < 1) return;
+    if (best.least == 0 && best.count == 0) {  // the first step, or only masked ones so far
+        const uint32_t kth = (uint32_t)__builtin_amdgcn_readlane((int)sort_down(order_of(top), lane), a.K - 1);
+        best.value = value_at(kth);
+    }
+    if (!__ballot(top > kLow && top >= best.value)) return;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const bool in = v[e] > kLow && v[e] >= best.value;
+        if (__ballot(in)) best.push(key_of(v[e], (uint32_t)(from + Tile<HALF>::place(lane, e))), in, a.K, lane);
+    }
+}
+
+// A wave's steps of a row: from `from` on, `stride` apart, the next one's loads in flight.
+template <bool HALF>
+__device__ __forceinline__ void scan(const LogpArgs &a, const void *x, int64_t from, int64_t stride, int64_t end, Running &r,
+                                     Best &best, int lane)
+{
+    using One = typename Tile<HALF>::One;
+    Tile<HALF> now, next;
+    if (from < end) now.load((const One *)x, from, end, lane);
+    for (; from < end; from += stride) {
+        if (from + stride < end) next.load((const One *)x, from + stride, end, lane);
+        step<HALF>(a, now, from, r, best, lane);
+        now = next;
+    }
+}
+
 // The wave's lanes as one, in every lane.
-__device__ __forceinline__ Running join_lanes(Running r, float c2)
+__device__ __forceinline__ Running join_lanes(Running r, float c, int lane)
 {
     float m = r.m;
+    uint64_t s;
+#define PN_MAX(X) m = fmaxf(m, __uint_as_float(across<X>(__float_as_uint(m), lane)))
+#define PN_ADD(X) s = __builtin_bit_cast(uint64_t, __builtin_bit_cast(double, s) + __builtin_bit_cast(double, across<X>(s, lane)))
+    PN_MAX(1); PN_MAX(2); PN_MAX(7); PN_MAX(15); PN_MAX(16); PN_MAX(32);
+    r.raise(m, c);
+    s = __builtin_bit_cast(uint64_t, r.s);
+    PN_ADD(1); PN_ADD(2); PN_ADD(7); PN_ADD(15); PN_ADD(16); PN_ADD(32);
+#undef PN_MAX
+#undef PN_ADD
+    r.e = wave_sum(r.e);
+    r.s = __builtin_bit_cast(double, s);
+    return r;
+}
+
+template <bool HALF> __device__ __forceinline__ float logit(const LogpArgs &a, int64_t row, int32_t token)
+{
+    if (token < 0 || token >= a.V) return kLow;
+    const int64_t at = row * a.ld + token;
+    return clean(HALF ? (float)((const _Float16 *)a.x)[at] : ((const float *)a.x)[at]);
+}
+
+constexpr int kWaves = 4;
+
+// A workgroup's sums and lists as one: the sums in every thread, the list in
+// the first wave.
+__device__ __forceinline__ Running join_waves(const LogpArgs &a, Running r, Best &best)
+{
+    __shared__ uint64_t lists[kWaves / 2][64];
+    __shared__ Sums part[kWaves];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    if (a.K > 0) best.finish(a.K, lane);
+    r = join_lanes(r, a.c, lane);
+    if (lane == 0) part[wave] = {r.s, r.m, r.e};
+    if (a.K > 0 && wave >= 2) lists[wave - 2][lane] = best.list;
+    __syncthreads();
+    if (a.K > 0 && wave < 2) best.list = best_of(best.list, lists[wave][lane], lane);
+    r = {0.0, kLow, 0.0f};
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
-    r.raise(m, c2);
+    for (int w = 0; w < kWaves; ++w) r.m = fmaxf(r.m, part[w].m);
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        r.s += __shfl_xor(r.s, d, 64);
-        r.e += __shfl_xor(r.e, d, 64);
+    for (int w = 0; w < kWaves; ++w) {
+        Running o = {part[w].s, part[w].m, part[w].e};
+        o.raise(r.m, a.c);
+        r.s += o.s;
+        r.e += o.e;
+    }
+    if (a.K > 0) {
+        if (wave == 1) lists[1][lane] = best.list;
+        __syncthreads();
+        if (wave == 0) best.list = best_of(best.list, lists[1][lane], lane);
     }
     return r;
 }
 
+// The answers of a row.
 template <bool HALF>
-__global__ __launch_bounds__(kThreads) void logp_spans(LogpArgs a)
+__device__ __forceinline__ void answer(const LogpArgs &a, int64_t row, Running r, Best &best)
+{
+    const int tid = threadIdx.x;
+    // the first given token's logit on its way meanwhile
+    int32_t token = -1;
+    if (tid < a.n_tok) token = a.tokens[row * a.ld_tok + tid];
+    float x = logit<HALF>(a, row, token);
+    r = join_waves(a, r, best);
+    const bool any = r.m > kLow;
+    const double log_s = any ? log(r.s) : 0.0;
+    if (tid == 0 && a.entropy) a.entropy[row] = any ? (float)(log_s - kLn2 * (double)r.e / r.s) : 0.0f;
+    auto logp = [&](float v) { return v > kLow ? (float)(((double)v - (double)r.m) * (double)a.scale - log_s) : kLow; };
+    for (int j = tid; j < a.n_tok; j += 64 * kWaves) {
+        if (j != tid) x = logit<HALF>(a, row, a.tokens[row * a.ld_tok + j]);
+        a.logp[row * a.ld_lp + j] = logp(x);
+    }
+    if (tid < a.K) {
+        a.top_ids[row * a.ld_top + tid] = best.list ? (int32_t)index_of(best.list) : -1;
+        a.top_logp[row * a.ld_top + tid] = best.list ? logp(value_of(best.list)) : kLow;
+    }
+}
+
+// WHOLE: a chunk is a row.
+template <bool HALF, bool WHOLE>
+__global__ __launch_bounds__(64 * kWaves) void logp_scan(LogpArgs a)
 {
     __shared__ uint64_t buf[kWaves][128];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int64_t unit = (int64_t)blockIdx.x * kWaves + wave;
-    const int64_t row = unit / a.spans;
-    const int span = (int)(unit - row * a.spans);
-    if (row >= a.rows) return;  // no barrier in this kernel
-    const void *x = (const uint8_t *)a.x + row * a.ld * (HALF ? 2 : 4);
-    const int64_t lo = (int64_t)span * a.span, hi = lo + a.span < a.V ? lo + a.span : a.V;
-    const float c2 = a.scale * 1.4426950408889634f;
+    const int64_t row = WHOLE ? blockIdx.x : blockIdx.x / (unsigned)a.chunks;
+    const int64_t lo = WHOLE ? 0 : (int64_t)(blockIdx.x % (unsigned)a.chunks) * a.chunk;
+    const int64_t hi = WHOLE || lo + a.chunk > a.V ? a.V : lo + a.chunk;
     Running r = {0.0, kLow, 0.0f};
     Best best;
     best.init(buf[wave]);
-    for (int64_t at = lo; at < hi; at += kTile) {
-        float v[16];
-        Tile<HALF>::load(v, x, at, hi, lane);
-        float top = kLow;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            v[e] = clean(v[e]);
-            top = fmaxf(top, v[e]);
-        }
-        if (top > kLow) {
-            r.raise(top, c2);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) r.add(v[e], c2);
-        }
-        if (a.K > 0 && __ballot(top > kLow && top >= best.value)) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (__ballot(v[e] > kLow && v[e] >= best.value))
-                    best.push(key_of(v[e], (uint32_t)(at + Tile<HALF>::place(lane, e))), v[e] > kLow, a.K, lane);
-        }
-    }
-    r = join_lanes(r, c2);
-    if (lane == 0) a.sums[unit] = {r.s, r.m, r.e};
-    if (a.K > 0) {
-        best.finish(a.K, lane);
-        if (lane < a.K) a.best[unit * a.K + lane] = best.list;
+    scan<HALF>(a, (const uint8_t *)a.x + row * a.ld * (HALF ? 2 : 4), lo + wave * kTile, kWaves * kTile, hi, r, best, lane);
+    if constexpr (WHOLE) {
+        answer<HALF>(a, row, r, best);
+    } else {
+        r = join_waves(a, r, best);
+        if (threadIdx.x == 0) a.sums[blockIdx.x] = {r.s, r.m, r.e};
+        if ((int)threadIdx.x < a.K) a.best[(int64_t)blockIdx.x * a.K + threadIdx.x] = best.list;
     }
 }
 
 template <bool HALF>
-__global__ __launch_bounds__(kThreads) void logp_join(LogpArgs a)
+__global__ __launch_bounds__(64 * kWaves) void logp_join(LogpArgs a)
 {
     __shared__ uint64_t buf[kWaves][128];
-    __shared__ Sums part[kWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int64_t row = blockIdx.x;
-    const float c2 = a.scale * 1.4426950408889634f;
     Running r = {0.0, kLow, 0.0f};
-    for (int i = tid; i < a.spans; i += kThreads) {
-        const Sums o = a.sums[row * a.spans + i];
-        if (o.m > kLow) {
-            Running other = {o.s, o.m, o.e};
-            const float m = fmaxf(r.m, o.m);
-            r.raise(m, c2);
-            other.raise(m, c2);
-            r.s += other.s;
-            r.e += other.e;
-        }
+    for (int i = tid; i < a.chunks; i += 64 * kWaves) {
+        const Sums p = a.sums[row * a.chunks + i];
+        Running o = {p.s, p.m, p.e};
+        const float m = fmaxf(r.m, o.m);
+        r.raise(m, a.c);
+        o.raise(m, a.c);
+        r.s += o.s;
+        r.e += o.e;
     }
     Best best;
     best.init(buf[wave]);
     if (a.K > 0) {
-        const uint64_t *keys = a.best + row * a.spans * a.K;
-        const int64_t many = (int64_t)a.spans * a.K;
-        for (int64_t i = 64 * wave; i < many; i += kThreads) {
+        const uint64_t *keys = a.best + row * a.chunks * a.K;
+        const int64_t many = (int64_t)a.chunks * a.K;
+        for (int64_t i = 64 * wave; i < many; i += 64 * kWaves) {
             const uint64_t key = i + lane < many ? keys[i + lane] : 0;
             best.push(key, key != 0, a.K, lane);
         }
-        best.finish(a.K, lane);
     }
-    r = join_lanes(r, c2);
-    if (lane == 0) part[wave] = {r.s, r.m, r.e};
-    __syncthreads();
-    buf[wave][lane] = best.list;
-    r = {0.0, kLow, 0.0f};
-    float m = kLow;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) m = fmaxf(m, part[w].m);
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        Running o = {part[w].s, part[w].m, part[w].e};
-        if (o.m > kLow) {
-            o.raise(m, c2);
-            r.s += o.s;
-            r.e += o.e;
-        }
-    }
-    const bool any = m > kLow;
-    const double log_s = any ? log(r.s) : 0.0;
-    if (tid == 0 && a.entropy) a.entropy[row] = any ? (float)(log_s - 0.6931471805599453 * (double)r.e / r.s) : 0.0f;
-    auto logp = [&](float v) {
-        return v > kLow ? (float)(((double)v - (double)m) * (double)a.scale - log_s) : kLow;
-    };
-    for (int j = tid; j < a.n_tok; j += kThreads) {
-        const int32_t t = a.tokens[row * a.ld_tok + j];
-        float v = kLow;
-        if (t >= 0 && t < a.V) {
-            const int64_t at = row * a.ld + t;
-            v = clean(HALF ? (float)((const _Float16 *)a.x)[at] : ((const float *)a.x)[at]);
-        }
-        a.logp[row * a.ld_lp + j] = logp(v);
-    }
-    if (a.K < 1) return;
-    __syncthreads();
-    if (wave > 0) return;
-    uint64_t list = best.list;
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) list = merge_down(larger(list, buf[w][63 - lane]), lane);
-    if (lane < a.K) {
-        a.top_ids[row * a.ld_top + lane] = list ? (int32_t)index_of(list) : -1;
-        a.top_logp[row * a.ld_top + lane] = list ? logp(value_of(list)) : kLow;
-    }
+    answer<HALF>(a, row, r, best);
 }
 
-// Entries of a wave's span: enough waves to fill the device where there are
-// few rows, long spans (few records to join) where there are many.
-int span_of(int64_t rows, int64_t V)
+// Entries of a chunk: four workgroups a compute unit, but at least a step a wave.
+int64_t chunk_of(int64_t rows, int64_t V)
 {
-    const int64_t waves = (int64_t)device_cus() * 32;
-    int64_t span = (rows * V + waves - 1) / waves;
-    span = (span + kTile - 1) / kTile * kTile;
-    return (int)(span < kTile ? kTile : span > 16 * kTile ? 16 * kTile : span);
+    const int64_t groups = (int64_t)device_cus() * 4, least = kWaves * kTile;
+    const int64_t chunk = ((rows * V + groups - 1) / groups + least - 1) / least * least;
+    return chunk < V ? chunk : V;
 }
 
 bool sizes_fit(int64_t rows, int64_t V, int K)
 {
-    const int64_t spans = (V + kTile - 1) / kTile;
-    return rows <= INT32_MAX && V <= INT32_MAX && K <= PN_LOGPROBS_MAX_TOP && rows * spans <= INT32_MAX;
+    const int64_t tiles = (V + kTile - 1) / kTile;
+    return rows <= INT32_MAX && V <= INT32_MAX && K <= PN_LOGPROBS_MAX_TOP && rows * tiles <= INT32_MAX;
+}
+
+template <bool HALF> pn_status launch(const LogpArgs &a, int64_t rows, hipStream_t s)
+{
+    const dim3 blocks((unsigned)(rows * a.chunks)), threads(64 * kWaves);
+    if (a.chunks == 1) {
+        hipLaunchKernelGGL((logp_scan<HALF, true>), blocks, threads, 0, s, a);
+        return hipGetLastError() == hipSuccess ? PN_OK : PN_ELAUNCH;
+    }
+    hipLaunchKernelGGL((logp_scan<HALF, false>), blocks, threads, 0, s, a);
+    if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
+    hipLaunchKernelGGL((logp_join<HALF>), dim3((unsigned)rows), threads, 0, s, a);
+    return hipGetLastError() == hipSuccess ? PN_OK : PN_ELAUNCH;
 }
 
 }  // namespace
@@ -354,9 +428,9 @@ bool sizes_fit(int64_t rows, int64_t V, int K)
 extern "C" size_t pn_logprobs_workspace(int64_t rows, int64_t V, int K)
 {
     if (rows < 1 || V < 1 || K < 0 || !sizes_fit(rows, V, K)) return 0;
-    const int span = span_of(rows, V);
-    const size_t spans = (size_t)((V + span - 1) / span);
-    return (size_t)rows * spans * (sizeof(Sums) + (size_t)K * sizeof(uint64_t));
+    const int64_t chunk = chunk_of(rows, V);
+    const size_t chunks = (size_t)((V + chunk - 1) / chunk);
+    return (size_t)rows * chunks * (sizeof(Sums) + (size_t)K * sizeof(uint64_t));
 }
 
 extern "C" pn_status pn_logprobs(const void *logits, int row_type, int64_t ld, int64_t rows, int64_t V, float scale,
@@ -383,28 +457,20 @@ extern "C" pn_status pn_logprobs(const void *logits, int row_type, int64_t ld, i
     a.entropy = entropy;
     a.top_logp = top_logp;
     a.top_ids = top_ids;
-    a.span = span_of(rows, V);
-    a.spans = (int)((V + a.span - 1) / a.span);
+    a.chunk = (int32_t)chunk_of(rows, V);
+    a.chunks = (int32_t)((V + a.chunk - 1) / a.chunk);
     a.sums = (Sums *)ws;
-    a.best = (uint64_t *)(a.sums + rows * a.spans);
+    a.best = (uint64_t *)(a.sums + rows * a.chunks);
     a.ld = ld;
     a.ld_tok = ld_tok;
     a.ld_lp = ld_lp;
     a.ld_top = ld_top;
     a.V = V;
-    a.rows = rows;
     a.n_tok = n_tok;
     a.K = K;
     a.scale = scale;
-    const hipStream_t s = (hipStream_t)stream;
-    const unsigned blocks = (unsigned)((rows * a.spans + kWaves - 1) / kWaves);
-    const bool half = row_type == PN_ROWS_F16;
-    if (half) hipLaunchKernelGGL((logp_spans<true>), dim3(blocks), dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((logp_spans<false>), dim3(blocks), dim3(kThreads), 0, s, a);
-    if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
-    if (half) hipLaunchKernelGGL((logp_join<true>), dim3((unsigned)rows), dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((logp_join<false>), dim3((unsigned)rows), dim3(kThreads), 0, s, a);
-    if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
-    g_last_variant = kVarLogprobs;
-    return PN_OK;
+    a.c = scale * 1.4426950408889634f;
+    const pn_status st = row_type == PN_ROWS_F16 ? launch<true>(a, rows, (hipStream_t)stream) : launch<false>(a, rows, (hipStream_t)stream);
+    if (st == PN_OK) g_last_variant = kVarLogprobs;
+    return st;
 }
