@@ -14,7 +14,7 @@ LIB = os.path.join(HERE, "libpn.so")
 SOURCES = [os.path.join(HERE, "csrc", n) for n in ("pn_kernels.hip", "pn_gemv_rows.hip", "pn_smallm.hip", "pn_probe.hip",
                                                                "pn_rotate.hip", "pn_prefill.hip", "pn_kv4_plan.hip",
                                                                "pn_kv4_store.hip", "pn_kv4_attn.hip", "pn_spec.hip",
-                                                               "pn_norm.hip", "pn_logprobs.hip")]
+                                                               "pn_kv4_shared.hip", "pn_norm.hip", "pn_logprobs.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

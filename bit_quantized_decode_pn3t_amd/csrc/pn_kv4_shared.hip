@@ -1,0 +1,153 @@
+// pn_kv4_shared.hip - attention for requests that share a long prefix
+// (pn_kv4_attn_shared), for AMD Instinct MI355X (gfx950).
+//
+//   out = (sum_front w v + sum_own w v) / (sum_front w + sum_own w)
+//
+// The first launch (kFront) takes the queries of a whole group as the rows of
+// one attention over the shared keys, which every one of them sees whole: a key
+// is unpacked and multiplied for all rows of a tile at once.  The rows' sums
+// stay in fp32, relative to their own maxima, and in as many parts as
+// workgroups shared a tile's keys.  The second launch gives each request's
+// queries its own keys and joins them with those parts.
+#include "pn_kv4_attn.h"
+
+namespace {
+
+// The launches of a call.
+struct Plan {
+    Cut front, own;
+    bool line;        // the requests' own keys are dealt as a line (kTail), not a workgroup an item (kOwn)
+    int tiles;        // kOwn: of a request
+    int64_t tile;     // rows of kFront's tiles
+    size_t sums, ml, members, items, front_parts, own_parts;  // bytes
+    size_t bytes() const { return sums + ml + members + items + front_parts + own_parts; }
+};
+
+size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+Plan plan(const pn_kv4_cache *c, int q_heads, int B, int G, int64_t total_q, int64_t max_q, int64_t max_kv, int64_t max_shared)
+{
+    Plan p;
+    const int group = q_heads / c->heads, most = c->dim == 256 ? 2 : 4;
+    // As one request a group, of about as many queries as a group has.
+    p.front = cut(c, q_heads, G, (total_q + G - 1) / G, max_shared * c->page_size, 0, 0);
+    p.tile = 16 * p.front.nt * p.front.rg;
+    p.own = cut(c, q_heads, B, max_q, max_kv, 0, 0);
+    const int64_t row_groups = (max_q * group + 15) / 16, tails = max_kv - max_shared * c->page_size;
+    p.tiles = (int)((row_groups + most - 1) / most);
+    p.line = p.own.rg > 1 || tails > 4096;
+    if (!p.line) {
+        p.own.nt = (int)((row_groups + p.tiles - 1) / p.tiles);
+        p.own.whole = true;
+    }
+    p.sums = (size_t)total_q * q_heads * c->dim * sizeof(float);
+    p.ml = round16((size_t)total_q * q_heads * sizeof(float2));
+    p.members = (size_t)B * sizeof(Member);
+    p.items = round16((size_t)(total_q * group / p.tile + G + 1) * c->heads * sizeof(int2));
+    p.front_parts = p.front.whole ? 0 : round16(p.front.workers * p.front.part);
+    p.own_parts = p.own.whole ? 0 : round16(p.own.workers * p.own.part);
+    return p;
+}
+
+bool shared_fit(const pn_kv4_cache *c, int q_heads, int B, int G, int64_t total_q, int64_t max_q, int64_t max_kv,
+                int64_t max_shared)
+{
+    const int64_t rows = total_q * (q_heads / c->heads);
+    return sizes_fit(c, q_heads, B, total_q, max_q, max_kv) && G <= 65535 && max_shared <= INT32_MAX / 2 / c->page_size &&
+           rows <= INT32_MAX / 4 && (max_q * (q_heads / c->heads) / 16 + 1) * B * c->heads <= INT32_MAX;
+}
+
+bool raise_shared() { return raise_pass<kFront>() && raise_pass<kTail>() && raise_pass<kOwn>(); }
+
+}  // namespace
+
+extern "C" size_t pn_kv4_attn_shared_workspace(const pn_kv4_cache *cache, int q_heads, int B, int G, int64_t total_q,
+                                               int64_t max_q, int64_t max_kv, int64_t max_shared)
+{
+    Kv4 c;
+    if (check_cache(cache, &c) || !sizes_ok(cache, q_heads, B, total_q, max_q, max_kv, 0) || G < 1 || max_shared < 1 ||
+        total_q == 0)
+        return 0;
+    if (max_q > total_q) max_q = total_q;
+    const int64_t pages = (max_kv + cache->page_size - 1) / cache->page_size;
+    if (max_shared > pages) max_shared = pages;
+    if (!shared_fit(cache, q_heads, B, G, total_q, max_q, max_kv, max_shared)) return 0;
+    return plan(cache, q_heads, B, G, total_q, max_q, max_kv, max_shared).bytes();
+}
+
+extern "C" pn_status pn_kv4_attn_shared(const pn_kv4_cache *cache, const uint16_t *q, int64_t ldq, int q_heads,
+                                        const int32_t *q_start, const int32_t *kv_len, const int32_t *table,
+                                        int64_t ld_table, int B, const int32_t *g_start, const int32_t *prefix,
+                                        int64_t ld_prefix, const int32_t *shared, int G, int64_t total_q, int64_t max_q,
+                                        int64_t max_kv, int64_t max_shared, float scale, uint16_t *out, int64_t ldo,
+                                        void *ws, size_t ws_bytes, void *stream)
+{
+    AttnArgs a = {};
+    if (const pn_status st = check_cache(cache, &a.c)) return st;
+    if (!q || !q_start || !kv_len || !table || !g_start || !prefix || !shared || !out || (!ws && total_q > 0)) return PN_EINVAL;
+    if (!sizes_ok(cache, q_heads, B, total_q, max_q, max_kv, 0) || G < 1 || max_shared < 1) return PN_ESHAPE;
+    if (!scale_ok(scale)) return PN_ESHAPE;
+    const int64_t cols = (int64_t)q_heads * cache->dim;
+    if (ldq < cols || ldo < cols) return PN_ESHAPE;
+    const int64_t pages = (max_kv + cache->page_size - 1) / cache->page_size;
+    if (ld_table < pages || ld_prefix < max_shared) return PN_ESHAPE;
+    const void *words[] = {q_start, kv_len, table, g_start, prefix, shared};
+    for (const void *p : words)
+        if (!aligned(p, 4)) return PN_EALIGN;
+    if (!aligned(q, 16) || !aligned(out, 16) || ldq % 8 || ldo % 8 || !aligned(ws, 16)) return PN_EALIGN;
+    if (max_q > total_q) max_q = total_q;  // no request has more
+    if (max_shared > pages) max_shared = pages;
+    if (!shared_fit(cache, q_heads, B, G, total_q, max_q, max_kv, max_shared)) return PN_EUNSUPPORTED;
+    if (total_q == 0) return PN_OK;
+    Plan p = plan(cache, q_heads, B, G, total_q, max_q, max_kv, max_shared);
+    if (ws_bytes < p.bytes()) return PN_ESHAPE;
+    if (!once_per_device(kAttrKv4Shared, raise_shared)) return PN_ELAUNCH;
+
+    uint8_t *at = (uint8_t *)ws;
+    auto take = [&](size_t n) { uint8_t *x = at; at += n; return x; };
+    a.front = (float *)take(p.sums);
+    a.front_ml = (float2 *)take(p.ml);
+    a.members = (Member *)take(p.members);
+    a.items = (int2 *)take(p.items);
+    uint8_t *front_parts = take(p.front_parts), *own_parts = take(p.own_parts);
+    a.g_start = g_start;
+    a.g_pages = shared;
+    a.requests = B;
+    a.groups = G;
+    a.max_shared = (int)max_shared;
+    a.q = q;
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.out = out;
+    a.ldq = ldq;
+    a.ldo = ldo;
+    a.total_q = total_q;
+    a.max_kv = max_kv;
+    a.q_heads = q_heads;
+    a.group = q_heads / cache->heads;
+    set_scale(a, scale);
+    const hipStream_t s = (hipStream_t)stream;
+
+    a.table = prefix;
+    a.ld_table = ld_prefix;
+    a.max_pages = (int)max_shared;
+    a.max_q = total_q;  // of a group
+    a.B = G;
+    a.f_tile = a.f_rows = (int)p.tile;
+    a.f_floats = (int)p.tile * cache->dim;
+    set_cut(a, cache, p.front, front_parts, p.front_parts);
+    a.f_part = a.part;
+    a.f_part_ml = a.part_ml;
+    if (const pn_status st = launch_pass<kFront>(a, p.front, cache->dim, s)) return st;
+
+    a.table = table;
+    a.ld_table = ld_table;
+    a.max_pages = (int)pages;
+    a.max_q = max_q;
+    a.B = B;
+    a.tiles = p.tiles;
+    set_cut(a, cache, p.own, own_parts, p.own_parts);
+    const pn_status st = p.line ? launch_pass<kTail>(a, p.own, cache->dim, s) : launch_pass<kOwn>(a, p.own, cache->dim, s);
+    if (st == PN_OK) g_last_variant = kVarKv4AttnShared;
+    return st;
+}

@@ -485,12 +485,11 @@ pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, int64_t ldq,
  *   max_shared : >= 1, at least every shared[g] (of a larger one the first
  *                max_shared pages are shared)
  *   other arguments as for pn_kv4_attn
- *   ws         : device, 16-byte aligned, at least total_q * q_heads * (4 dim
- *                + 8) + 4 B bytes and the rounding of parts of it to 16 (else
- *                PN_ESHAPE): room for the groups' sums.  What
- *                pn_kv4_attn_shared_workspace says leaves room for splits, too
- * PN_EUNSUPPORTED: as pn_kv4_attn; G > 65535, max_shared * page_size > 2^30 - 1
- * or total_q * q_heads / heads > 2^29 - 1. */
+ *   ws         : device, 16-byte aligned, at least what
+ *                pn_kv4_attn_shared_workspace says (else PN_ESHAPE); calls that
+ *                may overlap need their own
+ * PN_EUNSUPPORTED: as pn_kv4_attn; G > 65535, max_shared * page_size > 2^30 - 1,
+ * total_q * q_heads / heads > 2^29 - 1 or B * q_heads * (max_q / 16 + 1) > 2^31 - 1. */
 size_t pn_kv4_attn_shared_workspace(const pn_kv4_cache *cache, int q_heads, int B, int G, int64_t total_q,
                                     int64_t max_q, int64_t max_kv, int64_t max_shared);
 pn_status pn_kv4_attn_shared(const pn_kv4_cache *cache, const uint16_t *q, int64_t ldq, int q_heads,

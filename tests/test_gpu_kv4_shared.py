@@ -26,7 +26,7 @@ def _gpu():
     yield
 
 
-def run(seed, q_lens, tails, sizes, prefix_pages, dim, page, heads, group, ws_extra=32 << 20, scale=None, sharp=1.0,
+def run(seed, q_lens, tails, sizes, prefix_pages, dim, page, heads, group, scale=None, sharp=1.0,
         wild=False, holes=(), own_columns=True, g0=0, inside=(), max_shared=None, max_kv=None, spoil=True, gap=0):
     """Requests in groups of `sizes` (from request g0 on), the rest alone; tails: each one's own keys.
     inside: requests whose length is less than their prefix.  own_columns: table rows hold the prefix's pages too."""
@@ -86,9 +86,7 @@ def run(seed, q_lens, tails, sizes, prefix_pages, dim, page, heads, group, ws_ex
     q = (g.standard_normal((T + gap, ld)) * sharp).astype(np.float16)
     cache = B.KV4Cache(dev(pages), num_pages, page, heads, dim)
     max_q = max(max(q_lens), 1)
-    fixed = T * q_heads * (4 * dim + 8) + 4 * n + 32
-    need_ws = B.pn_kv4_attn_shared_workspace(cache, q_heads, n, len(sizes), T, max_q, top, most)
-    size = fixed + ws_extra if ws_extra is not None else need_ws
+    size = B.pn_kv4_attn_shared_workspace(cache, q_heads, n, len(sizes), T, max_q, top, most)
     ws = torch.full(((size + 15) // 16 * 4 + 64,), float("nan"), device="cuda")
     out = torch.full((T + gap, ld), 9.0, dtype=torch.float16, device="cuda")
     args = [cache, dev(q), ld, q_heads, i32(q_start), i32(kv), i32(table), width, n, i32(start), i32(prefix),
@@ -132,11 +130,10 @@ def test_groups_and_others(dim, page, heads, group):
 
 
 @pytest.mark.parametrize("dim,page,heads,group", SHAPES)
-@pytest.mark.parametrize("extra", [0, 1 << 20, None])
-def test_long_prefix(dim, page, heads, group, extra):
-    """Keys split over workgroups, or not where the workspace has no room."""
-    say("shared long dim=%d page=%d extra=%s" % (dim, page, extra))
-    run([3, dim], [1, 2, 1], [70, 3, 200], [3], [3000 // page], dim, page, heads, group, ws_extra=extra)
+def test_long_prefix(dim, page, heads, group):
+    """Keys split over workgroups."""
+    say("shared long dim=%d page=%d" % (dim, page))
+    run([3, dim], [1, 2, 1], [70, 3, 200], [3], [3000 // page], dim, page, heads, group)
 
 
 @pytest.mark.parametrize("dim,heads,group,members,q", [(64, 1, 16, 40, 1), (64, 2, 4, 12, 13), (128, 2, 6, 60, 1),
@@ -153,6 +150,19 @@ def test_many_rows(dim, heads, group, members, q):
 def test_long_tails_and_prompts(dim, group):
     """Tails longer than the prefix; a prompt chunk behind it next to single tokens."""
     run([5, dim], [1, 300, 1], [900, 420, 33], [3], [8], dim, 32, 1, group, own_columns=False)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("q", [1, 20])
+def test_tails_split_over_workgroups(dim, q):
+    """Tails long enough to be dealt in parts: few rows and many."""
+    run([21, dim, q], [q, q, 1], [5000, 300, 4200], [2], [20], dim, 32, 1, 16 if q > 1 else 3, own_columns=False)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_several_row_tiles(dim):
+    """Requests of more rows than a workgroup takes of them, over a prefix in parts."""
+    run([22, dim], [9, 1, 7], [30, 1, 12], [3], [64], dim, 32, 2, 8, own_columns=False)
 
 
 def test_queries_inside_the_prefix():
@@ -214,7 +224,7 @@ def test_offsets_out_of_order_stay_inside():
 
 @pytest.mark.parametrize("dim,members", [(128, 5), (128, 70), (256, 70)])
 def test_stream_and_graph(dim, members):
-    args, got = run([20, dim], [1] * members, [30] * members, [members], [70], dim, 16, 1, 6, ws_extra=None)
+    args, got = run([20, dim], [1] * members, [30] * members, [members], [70], dim, 16, 1, 6)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     graph = torch.cuda.CUDAGraph()

@@ -14,7 +14,7 @@ def cache(pages=FAKE, num=4, page=16, heads=2, dim=64):
 
 ARGS = dict(q=FAKE, ldq=256, q_heads=4, q_start=FAKE, kv_len=FAKE, table=FAKE, ld_table=8, B=3, g_start=FAKE, prefix=FAKE,
             ld_prefix=4, shared=FAKE, G=1, total_q=3, max_q=1, max_kv=128, max_shared=4, scale=0.125, out=FAKE, ldo=256,
-            ws=FAKE, ws_bytes=1 << 20)
+            ws=FAKE, ws_bytes=1 << 28)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -24,7 +24,7 @@ ARGS = dict(q=FAKE, ldq=256, q_heads=4, q_start=FAKE, kv_len=FAKE, table=FAKE, l
     (dict(ldq=260), EALIGN), (dict(ldo=260), EALIGN), (dict(ldq=248), ESHAPE), (dict(ldo=248), ESHAPE),
     (dict(q_heads=3), ESHAPE), (dict(q_heads=1), ESHAPE), (dict(B=0), ESHAPE), (dict(G=0), ESHAPE),
     (dict(total_q=-1), ESHAPE), (dict(max_q=0), ESHAPE), (dict(max_kv=0), ESHAPE), (dict(max_shared=0), ESHAPE),
-    (dict(ld_table=7), ESHAPE), (dict(ld_prefix=3), ESHAPE), (dict(ws_bytes=3 * 4 * (4 * 64 + 8)), ESHAPE),
+    (dict(ld_table=7), ESHAPE), (dict(ld_prefix=3), ESHAPE), (dict(ws_bytes=3 * 4 * (4 * 64 + 8)), ESHAPE), (dict(ws_bytes=0), ESHAPE),
     (dict(scale=float("nan")), ESHAPE), (dict(scale=float("inf")), ESHAPE), (dict(scale=-float("inf")), ESHAPE),
     (dict(B=65536), EUNSUPPORTED), (dict(G=65536), EUNSUPPORTED), (dict(total_q=1 << 30), EUNSUPPORTED),
     (dict(total_q=1 << 28), EUNSUPPORTED), (dict(max_kv=1 << 30, ld_table=1 << 26), EUNSUPPORTED),
