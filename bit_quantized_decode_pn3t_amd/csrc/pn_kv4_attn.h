@@ -73,6 +73,7 @@ using namespace pn::host;
 namespace {
 
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef float float2_t __attribute__((ext_vector_type(2)));
 typedef float float4_t __attribute__((ext_vector_type(4)));
 typedef unsigned short ushort2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
@@ -123,6 +124,7 @@ struct AttnArgs {
     const float2 *f_part_ml;
     int32_t f_tile, f_rows, f_floats;  // rows of a tile of kFront; rows and floats of a part
     int32_t requests, groups, max_shared;
+    int32_t least;           // kFront: steps of a workgroup at least
     int32_t tiles;           // kOwn: of a request
     float c2;                // |scale| log2(e), above 0
     float slack;             // 4 / c2
@@ -390,7 +392,8 @@ __device__ __forceinline__ bool line_part(const AttnArgs &a, LineLds &s, Line &t
     const int32_t used = a.two && total < (int64_t)a.workers * (kTwo * kUnit) ? a.workers / 2 : a.workers;
     const int32_t dealt = used - used / 64;
     t.share = quotient(total + dealt - 1, dealt);
-    if (t.share < kShare * kUnit && !a.whole) t.share = kShare * kUnit;
+    const int64_t least = (PASS == kFront ? a.least : kShare) * kUnit;
+    if (t.share < least && !a.whole) t.share = least;
     t.lo = blockIdx.x * t.share;
     t.hi = t.lo + t.share < total ? t.lo + t.share : total;
     if (tid == 0 && !a.whole) a.cuts[blockIdx.x].parts = 0;
@@ -944,6 +947,185 @@ __device__ __forceinline__ void advance(State<D, NT> &st, const uint8_t *from, c
     }
 }
 
+// The same for rows that see every key that is there (kFront).  seen: tokens of
+// each tile that are; `some` are not.  Fewer instructions where the arithmetic
+// is what counts: maxima are looked at lane by lane and joined across lanes only
+// when one passes the running maximum by the slack, and the weights' sums are a
+// product with ones (of the rounded weights, and over all lanes: l is the row's).
+struct Seen {
+    bool some;
+    int32_t n[2];
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void advance_front(State<D, NT> &st, const uint8_t *from, const half8_t *q, const AttnArgs &a,
+                                              const Seen &seen, int lane)
+{
+    using G = Ring<D>;
+    constexpr int R = G::R;
+    const int r = lane & 15, g = lane >> 4;
+
+    // scores
+    float4_t sc[NT][2];
+    uint32_t ks[2][2 * R];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) read_words(ks[i], from + G::kScales + 256 * i + 8 * R * g);
+#pragma unroll
+    for (int b = 0; b < R; ++b) {
+        half8_t k[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint8_t *row = from + i * G::kTile;
+            const uint2 x = *(const uint2 *)(R == 1 ? row + 32 * r + 8 * g
+                                                    : row + 16 * G::piece(r, (R / 2) * g + b / 2) + 8 * (b & 1));
+            k[i][0] = codes8(x.x);
+            k[i][1] = codes8(x.y);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const half8_t q0 = q[(n * 2 * R + 2 * b) * 64 + lane], q1 = q[(n * 2 * R + 2 * b + 1) * 64 + lane];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float4_t c = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[i][0], q0, (float4_t){0, 0, 0, 0}, 0, 0, 0);
+                c = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[i][1], q1, c, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    sc[n][i][j] = __builtin_fmaf(c[j], half_at(ks[i], R * j + b), b == 0 ? 0.0f : sc[n][i][j]);
+            }
+        }
+        keep_order();
+    }
+
+    // Value scales of the lane's tokens; 0 for those that are not there.
+    uint32_t d[2][2 * R];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) read_words(d[i], from + G::kScales + 256 * i + 32 * R + 8 * R * g);
+    // The scales against the cap: lane r looks at one word of its group's 4 R.
+    const int x = r & (4 * R - 1), xi = x / (2 * R), xh = x % (2 * R);
+    uint32_t word = *(const uint32_t *)(from + G::kScales + 256 * xi + 32 * R + 8 * R * g + 4 * xh) & 0x7fff7fffu;
+    if (seen.some) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool ok = 4 * g + (j & 3) < seen.n[j >> 2];
+#pragma unroll
+            for (int b = 0; b < R; ++b) {
+                const int h = R * (j & 3) + b;
+                if (!ok) d[j >> 2][h >> 1] &= h & 1 ? 0x0000ffffu : 0xffff0000u;
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) sc[n][j >> 2][j & 3] = ok ? sc[n][j >> 2][j & 3] : -__builtin_inff();
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+            if (4 * g + (2 * xh + y) / R >= (xi ? seen.n[1] : seen.n[0])) word &= y ? 0x0000ffffu : 0xffff0000u;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2 * R; ++j) asm("" : "+v"(d[i][j]));  // words, not halves
+    uint32_t big = (word >> 16) > (word & 0xffffu) ? word >> 16 : word & 0xffffu;
+    if (__ballot(big > st.cap)) {
+#pragma unroll
+        for (int x2 = 1; x2 < 64; x2 <<= 1) {
+            const uint32_t y = __shfl_xor(big, x2, 64);
+            big = y > big ? y : big;
+        }
+        float up;
+        fit_scales(big, up, st.cap);
+        const float f = up / st.up;  // the first time O is 0
+        st.up = up;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int b = 0; b < R; ++b)
+#pragma unroll
+                for (int i2 = 0; i2 < 4; ++i2) st.o[n][b][i2] *= f;
+    }
+
+    keep_order();
+    // weights
+    float mx[NT], more = kLowest;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        mx[n] = max3(sc[n][0][0], sc[n][0][1], sc[n][0][2]);
+        mx[n] = max3(mx[n], sc[n][0][3], sc[n][1][0]);
+        mx[n] = max3(mx[n], sc[n][1][1], sc[n][1][2]);
+        mx[n] = max2(mx[n], sc[n][1][3]);
+        more = max2(more, mx[n] - st.m[n]);
+    }
+    if (__ballot(more > a.slack)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float top = group_max(mx[n]);
+            const float f = top > st.m[n] ? __builtin_amdgcn_exp2f((st.m[n] - top) * a.c2) : 1.0f;
+            st.m[n] = max2(st.m[n], top);
+            st.l[n] *= f;
+#pragma unroll
+            for (int b = 0; b < R; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) st.o[n][b][i] *= f;
+        }
+    }
+    half8_t p[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const float mm = kBias - st.m[n] * a.c2;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const float2_t w = {__builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][j >> 2][j & 3], a.c2, mm)),
+                                __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][j >> 2][(j & 3) + 1], a.c2, mm))};
+            const half2_t w2 = __builtin_convertvector(w, half2_t);
+            p[n][j] = w2[0], p[n][j + 1] = w2[1];
+        }
+    }
+
+    // values
+    const half8_t ones = {1, 1, 1, 1, 1, 1, 1, 1};
+    const uint32_t sel = r < 8 ? 0x05040100u : 0x07060302u;  // even (low) or odd (high) elements of a token pair
+    const half2_t up2 = {(_Float16)st.up, (_Float16)st.up};
+    float4_t sum[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) sum[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, p[n], (float4_t){0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+    for (int b = 0; b < R; ++b) {
+        uint32_t v[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            read_words(v[i], from + G::kV + i * G::kTile + 16 * (g * (D / 8) + 8 * b + (r & 7)));
+        half8_t va[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            // the scales of the token pair for this block
+            const int i2 = u >> 1, t = 2 * (u & 1), word2 = R * t / 2 + b / 2, next = R / 2;
+            const half2_t sc2 = up2 * as_half2(R == 1 ? d[i2][u & 1]
+                                                      : __builtin_amdgcn_perm(d[i2][word2 + next], d[i2][word2],
+                                                                              b & 1 ? 0x07060302u : 0x05040100u));
+            half2_t e[4];
+            Unpack<1>::run(__builtin_amdgcn_perm(v[i2][t + 1], v[i2][t], sel), e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                e[i] *= sc2;
+                va[i][2 * u] = e[i][0], va[i][2 * u + 1] = e[i][1];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                st.o[n][b][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(va[i], p[n], st.o[n][b][i], 0, 0, 0);
+        if (b == 0) {
+            // The other three results stay in use until the product has ended: left to themselves their
+            // registers would be free at once, for inline assembly that no one keeps apart from the product.
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                st.l[n] += sum[n][0];
+                asm volatile("" : "+v"(st.l[n]) : "v"(sum[n]));
+            }
+        }
+        keep_order();
+    }
+}
+
 // Lane (r, g) holds x[j] = element 64 b + 8 (4 (g & 1) + j) + 2 i + (g >> 1)
 // of row r.  As fp16 pairs: elements 2 i and 2 i + 1 of word 4 (g & 1) + j +
 // (g & 2) of the block, j < 2 (lanes below 32 take x[j], those above x[j + 2]).
@@ -1192,7 +1374,14 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
             // A row group sees less than its workgroup's tile.
             const bool none = RG > 1 && (e >= e1 || token0 > p1 ||
                                          (a.window > 0 && (int64_t)token0 + kStep - 1 + a.window <= p0 && token0 >= a.sinks));
-            if (!none) advance<D, NT>(st, from, q, a, mask, lane);
+            if constexpr (PASS == kFront) {
+                const int left = w.len - token0;  // 1 and up
+                const Seen seen = {!(mask.page[0] && mask.page[1] && left >= kStep),
+                                   {mask.page[0] ? left : 0, mask.page[1] ? left - 16 : 0}};
+                advance_front<D, NT>(st, from, q, a, seen, lane);
+            } else {
+                if (!none) advance<D, NT>(st, from, q, a, mask, lane);
+            }
             __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the stage has been read
             asm volatile("" ::: "memory");
             if constexpr (RG == 1)
@@ -1208,7 +1397,7 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
         // the fragments.
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float l = group_sum(st.l[n]);
+            const float l = PASS == kFront ? st.l[n] : group_sum(st.l[n]);
             if (g == 0) ml[wave][16 * n + r][0] = st.m[n], ml[wave][16 * n + r][1] = l;
         }
         float4_t *frag = (float4_t *)lds;  // [wave][4 b + i][lane]
@@ -1351,7 +1540,6 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
     const int part = keys ? unit % (D / 32) : unit % (D / 8);
     const int token = keys ? unit / (D / 32) : unit / (D / 8) * 4;  // of the step
     Line line;
-    if (PASS == kFront && blockIdx.x == 0) group_members(a);
     if (!line_part<kPromptStep, PASS>(a, line_lds, line, kRows)) return;
     for (int64_t x = line.lo; x < line.hi;) {
         Item item;
@@ -1690,20 +1878,6 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
             }
             continue;
         }
-        if constexpr (PASS == kFront) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float all_l = group_sum(l[n]);
-                const int row_at = row0 + 16 * n + r, i = row_at / a.group, q_head = head * a.group + row_at - i * a.group;
-                if (row_at < rows) {
-#pragma unroll
-                    for (int y = 0; y < 4 * R; ++y)
-                        *front_of<D>(a, w.q0 + i, q_head, y >> 2, y & 3, g) = o[n][y >> 2][y & 3] * down;
-                    if (g == 0) a.front_ml[(w.q0 + i) * a.q_heads + q_head] = make_float2(m[n], all_l);
-                }
-            }
-            continue;
-        }
         // By way of LDS into whole rows: a wave's rows lie where the
         // fragments were, a row's 16-byte pieces permuted by its number.
         lds_barrier();
@@ -1835,6 +2009,11 @@ struct Cut {
     size_t part;  // bytes that one workgroup's parts and record need
 };
 
+size_t part_bytes(const pn_kv4_cache *c, const Cut &t)
+{
+    return 2 * (size_t)t.rg * t.nt * (c->dim * 16 * sizeof(float) + 16 * sizeof(float2)) + sizeof(Cutoff);
+}
+
 Cut cut(const pn_kv4_cache *c, int q_heads, int B, int64_t max_q, int64_t max_kv, int window, int sinks)
 {
     Cut t;
@@ -1861,8 +2040,7 @@ Cut cut(const pn_kv4_cache *c, int q_heads, int B, int64_t max_q, int64_t max_kv
     const int64_t tile_rows = 16 * t.nt * t.rg, items = (int64_t)B * c->heads * ((rows + tile_rows - 1) / tile_rows);
     const int64_t longest = keys / (kShare * kStep) + 1;
     t.parts = (int)(items * longest < device_cus() ? longest : device_cus() / items);
-    const size_t groups = t.rg * t.nt;
-    t.part = 2 * groups * (c->dim * 16 * sizeof(float) + 16 * sizeof(float2)) + sizeof(Cutoff);
+    t.part = part_bytes(c, t);
     return t;
 }
 
@@ -1881,7 +2059,7 @@ template <int D, int PASS> bool raise_prompt()
 // Raise the LDS limits of a pass's kernels.
 template <int PASS> bool raise_pass()
 {
-    if constexpr (PASS != kOwn) {
+    if constexpr (PASS == kWhole || PASS == kTail) {
         if (!raise_one<256, 2, 4, PASS>() || !raise_prompt<64, PASS>() || !raise_prompt<128, PASS>()) return false;
     }
     return raise_one<64, 1, 1, PASS>() && raise_one<64, 2, 1, PASS>() && raise_one<64, 3, 1, PASS>() &&
@@ -1912,8 +2090,7 @@ pn_status launch_prompt(const AttnArgs &a, hipStream_t s)
 {
     hipLaunchKernelGGL((kv4_prompt<D, NT, PASS>), dim3((unsigned)a.workers), dim3(kThreads), (Prompt<D, NT>::kLds), s, a);
     if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
-    if constexpr (PASS == kFront) return PN_OK;
-    else if (!a.whole) {
+    if (!a.whole) {
         hipLaunchKernelGGL((kv4_join<D, 4, PASS>), dim3((unsigned)a.workers, D / 64, NT * kWaves), dim3(256), 0, s, a, NT * kWaves);
         if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
     }
@@ -1924,7 +2101,7 @@ template <int D, int PASS>
 pn_status launch_rows(const AttnArgs &a, const Cut &t, hipStream_t s)
 {
     constexpr int most = D == 256 ? 2 : 4;
-    if constexpr (PASS == kOwn) {
+    if constexpr (PASS == kOwn || PASS == kFront) {
         if (t.rg > 1) return PN_EUNSUPPORTED;
     } else if constexpr (D == 256) {
         if (t.rg > 1) return launch<D, most, 4, PASS>(a, s);
