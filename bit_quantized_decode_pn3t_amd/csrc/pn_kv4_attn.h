@@ -64,6 +64,8 @@
 // GFLOP): 536 us and 17.7.
 #pragma once
 
+#include <type_traits>
+
 #include "pn_kv4.h"
 #include "pn_device.h"
 
@@ -117,14 +119,13 @@ struct AttnArgs {
     // Of the passes of requests that share keys:
     const int32_t *g_start, *g_pages;  // the groups' first requests, the pages they share
     struct Member *members;  // [request]
-    int2 *items;             // [tile of a group][head]: first workgroup, its parts (0: one, in front)
-    float *front;            // [query][query head][D]: sums over the shared keys, in the products' order
-    float2 *front_ml;        // their maxima and sums of weights
-    const float *f_part;     // the parts of kFront's items, as `part` and `part_ml` are
+    int2 *items;             // [tile of a group][head]: first part, parts
+    const float *f_part;     // the parts that kFront left, as `part` and `part_ml` are
     const float2 *f_part_ml;
-    int32_t f_tile, f_rows, f_floats;  // rows of a tile of kFront; rows and floats of a part
+    int32_t f_tile;          // rows of a tile of kFront
     int32_t requests, groups, max_shared;
-    int32_t least;           // kFront: steps of a workgroup at least
+    int32_t least;           // kFront: steps of a part at least
+    int32_t grid;            // kFront: workgroups; `workers` of them, unless there are more items
     int32_t tiles;           // kOwn: of a request
     float c2;                // |scale| log2(e), above 0
     float slack;             // 4 / c2
@@ -132,9 +133,10 @@ struct AttnArgs {
 
 // What a launch computes.  kWhole: attention.  For requests that share their
 // first keys (pn_kv4_attn_shared): kFront, the queries of a whole group against
-// the keys that it shares, left as sums with their maxima; kTail and kOwn, each
-// request's queries against its own keys, joined with those sums.  kOwn: a
-// workgroup takes one request's row tile and head, not a part of the line.
+// the keys that it shares, left in parts as sums with their maxima; kTail and
+// kOwn, each request's queries against its own keys, joined with those parts.
+// kFront and kOwn give a workgroup one item (a part of one), kWhole and kTail a
+// part of the line.
 enum Pass { kWhole = 0, kFront = 1, kTail = 2, kOwn = 3 };
 constexpr bool joins(int pass) { return pass == kTail || pass == kOwn; }
 
@@ -392,8 +394,7 @@ __device__ __forceinline__ bool line_part(const AttnArgs &a, LineLds &s, Line &t
     const int32_t used = a.two && total < (int64_t)a.workers * (kTwo * kUnit) ? a.workers / 2 : a.workers;
     const int32_t dealt = used - used / 64;
     t.share = quotient(total + dealt - 1, dealt);
-    const int64_t least = (PASS == kFront ? a.least : kShare) * kUnit;
-    if (t.share < least && !a.whole) t.share = least;
+    if (t.share < kShare * kUnit && !a.whole) t.share = kShare * kUnit;
     t.lo = blockIdx.x * t.share;
     t.hi = t.lo + t.share < total ? t.lo + t.share : total;
     if (tid == 0 && !a.whole) a.cuts[blockIdx.x].parts = 0;
@@ -426,7 +427,6 @@ struct Item {
     Cost c;
     int32_t s0, s1, all;        // its part [s0, s1) of `all` (lengths on the line)
     int32_t head, tile0, rows;  // the tile's first row, the request's rows
-    int32_t parts;              // workgroups that work on it, where it starts here
     bool cut;
 };
 
@@ -487,13 +487,9 @@ __device__ __forceinline__ bool next_item(const AttnArgs &a, const LineLds &s, L
     m.cut = s0 > 0 || s1 < m.all;
     m.tile0 = tile * tile_rows;
     m.rows = m.c.w.qn * a.group;
-    m.parts = m.cut ? (int)quotient(first + one - 1, t.share) - (int)blockIdx.x + 1 : 0;
-    if (m.s0 == 0 && threadIdx.x == 0) {
-        if constexpr (PASS == kFront)
-            a.items[(int64_t)(front_tile(a, m.c.w.q0, t.b) + tile) * a.c.heads + m.head] = make_int2((int)blockIdx.x, m.parts);
-        else if (m.cut)
-            a.cuts[blockIdx.x] = {m.c.w.q0, m.tile0, m.rows, PASS == kTail ? (int32_t)((uint32_t)t.b << 16 | m.head) : m.head, m.parts};
-    }
+    if (m.s0 == 0 && m.cut && threadIdx.x == 0)
+        a.cuts[blockIdx.x] = {m.c.w.q0, m.tile0, m.rows, PASS == kTail ? (int32_t)((uint32_t)t.b << 16 | m.head) : m.head,
+                              (int)quotient(first + one - 1, t.share) - (int)blockIdx.x + 1};
     return true;
 }
 
@@ -509,9 +505,129 @@ __device__ __forceinline__ bool own_item(const AttnArgs &a, Line &t, Item &m, in
     m.rows = m.c.w.qn * a.group;
     m.s0 = 0;
     m.s1 = m.all = 1;
-    m.parts = 0;
     m.cut = false;
     return m.tile0 < m.rows;
+}
+
+// kFront: workgroup 0 notes the members; the others' parts, in order: group,
+// row tile, head, place along the keys.  All items are cut into parts of up to
+// T steps, T the least with which the parts are no more than the workgroups:
+// equal parts, one a workgroup, as an item's start and end cost as much as some
+// eight steps (parts of an even line, of two items in most workgroups: 64
+// requests behind 16384 tokens 53 us, this way 37).  More than 64 groups are
+// not searched for T: it is their mean.  False: no such part.
+struct FrontLds {
+    int64_t scan[kWaves];
+    int64_t steps;
+    int32_t b, found;
+};
+
+template <int STEP>
+__device__ __forceinline__ bool front_item(const AttnArgs &a, FrontLds &s, Line &t, Item &m, int tile_rows)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int64_t me = (int64_t)blockIdx.x - 1, most = a.workers - 1;
+    // items and steps of group b
+    auto size = [&](int b, int64_t &items, int64_t &steps) {
+        const Request w = request<kFront>(a, b);
+        items = (int64_t)((w.qn * a.group + tile_rows - 1) / tile_rows) * a.c.heads;
+        steps = (w.len + STEP - 1) / STEP;
+    };
+    auto wave_total = [&](int64_t v) {
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+        return v;
+    };
+    int64_t items = 0, steps = 0, T, before = 0;
+    if (a.groups <= 64) {  // every wave for itself
+        if (lane < a.groups) size(lane, items, steps);
+        T = quotient(wave_total(items * steps) + most - 1, most);
+        if (T < a.least) T = a.least;
+        int64_t high = steps;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t o = __shfl_xor(high, d, 64);
+            high = o > high ? o : high;
+        }
+        if (high < T) high = T;  // with it every item is one part
+        while (T < high) {
+            const int64_t mid = (T + high) >> 1;
+            if (wave_total(items * quotient(steps + mid - 1, mid)) <= most) high = mid;
+            else T = mid + 1;
+        }
+        const int64_t mine = items * quotient(steps + T - 1, T);
+        int64_t sum = mine;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t o = __shfl_up(sum, d, 64);
+            if (lane >= d) sum += o;
+        }
+        const uint64_t here = __ballot(me >= sum - mine && me < sum);
+        if (!here) return false;
+        t.b = __builtin_ctzll(here);
+        before = __shfl(sum - mine, t.b, 64);
+        steps = __shfl(steps, t.b, 64);
+    } else {
+        const int per = (a.groups + kThreads - 1) / kThreads, first = tid * per;
+        const int last = first + per < a.groups ? first + per : a.groups;
+        int64_t sum = 0;
+        for (int b = first; b < last; ++b) size(b, items, steps), sum += items * steps;
+        sum = wave_total(sum);
+        if (lane == 0) s.scan[wave] = sum;
+        if (tid == 0) s.found = 0;
+        __syncthreads();
+        T = 0;
+        for (int w = 0; w < kWaves; ++w) T += s.scan[w];
+        T = quotient(T + most - 1, most);
+        if (T < a.least) T = a.least;
+        sum = 0;
+        for (int b = first; b < last; ++b) size(b, items, steps), sum += items * quotient(steps + T - 1, T);
+        int64_t upto = sum;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t o = __shfl_up(upto, d, 64);
+            if (lane >= d) upto += o;
+        }
+        __syncthreads();
+        if (lane == 63) s.scan[wave] = upto;
+        __syncthreads();
+        for (int w = 0; w < wave; ++w) upto += s.scan[w];
+        if (me >= upto - sum && me < upto) {  // one thread at most
+            before = upto - sum;
+            for (int b = first; b < last; ++b) {
+                size(b, items, steps);
+                const int64_t n = items * quotient(steps + T - 1, T);
+                if (me < before + n) {
+                    s.scan[0] = before;
+                    s.steps = steps;
+                    s.b = b;
+                    s.found = 1;
+                    break;
+                }
+                before += n;
+            }
+        }
+        __syncthreads();
+        if (!s.found) return false;
+        t.b = s.b;
+        before = s.scan[0];
+        steps = s.steps;
+    }
+    t.b = uniform(t.b);
+    const int parts = uniform((int)quotient(steps + T - 1, T)), at = uniform((int)(me - before));
+    const int item = at / parts, part = at - item * parts;
+    m.head = item % a.c.heads;
+    const int tile = item / a.c.heads;
+    m.c.w = request<kFront>(a, t.b);
+    m.tile0 = tile * tile_rows;
+    m.rows = m.c.w.qn * a.group;
+    m.all = uniform((int)steps);
+    m.s0 = uniform((int)(part * T));
+    m.s1 = uniform((int)((part + 1) * T < steps ? (part + 1) * T : steps));
+    m.cut = true;
+    if (part == 0 && tid == 0)
+        a.items[(int64_t)(front_tile(a, m.c.w.q0, t.b) + tile) * a.c.heads + m.head] = make_int2((int)me, parts);
+    return true;
 }
 
 // ---------------------------------------------------------------------------
@@ -1169,23 +1285,14 @@ template <int D, int NT, int RG> struct Shape {
 // 73 and 80 us).
 template <int D, int NT, int RG> constexpr int waves_per_simd() { return D < 256 && NT == 1 && RG == 1 ? 4 : 2; }
 
-// A row's place in the shared keys' sums: product i of block y, lane group g.
-template <int D>
-__device__ __forceinline__ float4_t *front_of(const AttnArgs &a, int64_t query, int head, int y, int i, int g)
-{
-    return (float4_t *)(a.front + (query * a.q_heads + head) * D + ((4 * y + i) * 4 + g) * 4);
-}
-
-// The shared keys' sums for a row, whole or in parts, as lane (r, g) sees it.
+// The parts of the shared keys' sums for a row, as lane (r, g) sees them.
 struct FrontRow {
-    const float4_t *at, *next;       // of the first part, of those behind it
-    const float2 *at_ml, *next_ml;
-    int64_t step, step_ml;           // between those
-    int32_t parts, by;               // by: from one product to the next
-    float top;                       // the parts' largest maximum
-    float own, front;                // factors of the row's own sum and of the parts relative to top
-    __device__ __forceinline__ float2 ml(int j) const { return j == 0 ? *at_ml : next_ml[(j - 1) * step_ml]; }
-    __device__ __forceinline__ float4_t sum(int j, int y) const { return (j == 0 ? at : next + (j - 1) * step)[y * by]; }
+    const float4_t *at;   // of the first part
+    const float2 *ml;
+    int64_t step;         // from one part to the next; f_tile in ml
+    int32_t parts;
+    float top;            // their largest maximum
+    float own, front;     // factors of the row's own sum and of the parts relative to top
 };
 
 // Joined with the row's own (m, l).  Without a row nothing is read; all factors
@@ -1200,31 +1307,17 @@ __device__ __forceinline__ FrontRow front_row(const AttnArgs &a, int b, int64_t 
         const int head = q_head / a.group, row = (int32_t)(query - in.q0) * a.group + q_head - head * a.group;
         const int tile = row / a.f_tile, local = row - tile * a.f_tile;
         const int2 item = a.items[(int64_t)(in.tile + tile) * a.c.heads + head];
-        if (item.y == 0) {
-            f.at = f.next = front_of<D>(a, query, q_head, 0, 0, g);
-            f.at_ml = f.next_ml = a.front_ml + query * a.q_heads + q_head;
-            f.step = f.step_ml = 0;
-            f.by = 4;
-            f.parts = 1;
-        } else {
-            // the first workgroup has the item's start (its part 1), the others go on with it (their part 0)
-            const float4_t *lane = (const float4_t *)(a.f_part + 2 * item.x * (int64_t)a.f_floats) + (local >> 4) * (D * 4) + (local & 15) + 16 * g;
-            const float2 *ml = a.f_part_ml + 2 * item.x * (int64_t)a.f_rows + local;
-            f.step = a.f_floats / 2;
-            f.step_ml = 2 * a.f_rows;
-            f.at = lane + a.f_floats / 4;
-            f.next = lane + f.step;
-            f.at_ml = ml + a.f_rows;
-            f.next_ml = ml + f.step_ml;
-            f.by = 64;
-            f.parts = item.y;
-        }
+        f.step = (int64_t)a.f_tile * (D / 4);
+        f.at = (const float4_t *)a.f_part + item.x * f.step + (local >> 4) * (D * 4) + (local & 15) + 16 * g;
+        f.ml = a.f_part_ml + (int64_t)item.x * a.f_tile + local;
+        // (groups that overlap may leave an entry unwritten)
+        f.parts = item.x >= 0 && item.y > 0 && item.y < a.grid - item.x ? item.y : 0;
     }
     float top = kLowest, sum = 0.0f;
-    for (int j = g; j < f.parts; j += 4) top = max2(top, f.ml(j).x);
+    for (int j = g; j < f.parts; j += 4) top = max2(top, f.ml[(int64_t)j * a.f_tile].x);
     f.top = top = group_max(top);
     for (int j = g; j < f.parts; j += 4) {
-        const float2 x = f.ml(j);
+        const float2 x = f.ml[(int64_t)j * a.f_tile];
         sum += x.y * __builtin_amdgcn_exp2f((x.x - top) * a.c2);
     }
     sum = group_sum(sum);
@@ -1246,9 +1339,9 @@ __device__ __forceinline__ float4_t front_sum(const AttnArgs &a, const FrontRow 
         float w[kDeep];
 #pragma unroll
         for (int j = 0; j < kDeep; ++j) {
-            const bool in = j0 + j < f.parts;
-            x[j] = f.sum(in ? j0 + j : 0, y);
-            w[j] = in ? f.ml(j0 + j).x : kLowest;
+            const int64_t at = j0 + j < f.parts ? j0 + j : 0;
+            x[j] = f.at[at * f.step + 64 * y];
+            w[j] = f.ml[at * a.f_tile].x;
         }
 #pragma unroll
         for (int j = 0; j < kDeep; ++j)
@@ -1265,7 +1358,7 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
     constexpr int R = G::R, kRows = S::kRows, KW = S::KW;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // the ring, then the queries
     __shared__ float ml[kWaves][16 * NT][2];
-    __shared__ LineLds line_lds;
+    __shared__ typename std::conditional<PASS == kFront, FrontLds, LineLds>::type line_lds;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int rg = wave / KW, kg = wave % KW;
@@ -1274,8 +1367,11 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
     half8_t *queries = (half8_t *)(lds + S::kRing), *q = queries + rg * NT * 2 * R * 64;
 
     Line line;
-    if (PASS == kFront && blockIdx.x == 0) group_members(a);
-    if constexpr (PASS == kOwn) line.lo = 0, line.hi = 1;
+    if (PASS == kFront && blockIdx.x == 0) {
+        group_members(a);
+        return;
+    }
+    if constexpr (PASS == kOwn || PASS == kFront) line.lo = 0, line.hi = 1;
     else if (!line_part<kStep, PASS>(a, line_lds, line, kRows)) return;
     Offsets<D> off;
     off.set(lane, 1 << a.c.shift);
@@ -1285,6 +1381,9 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
         if constexpr (PASS == kOwn) {
             x = line.hi;
             if (!own_item(a, line, item, kRows)) continue;
+        } else if constexpr (PASS == kFront) {
+            x = line.hi;
+            if (!front_item<kStep>(a, line_lds, line, item, kRows)) continue;
         } else {
             if (!next_item<kStep, PASS>(a, line_lds, line, x, item, kRows)) continue;
         }
@@ -1300,8 +1399,8 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
 
         // The same part of the steps that this tile has.
         auto place = [&](int e) { return e < w.sink_steps ? e : e - w.sink_steps + w.lo; };
-        const int e1 = share_of(item.s1, item.all, w.steps);
-        int e = share_of(s0, item.all, w.steps);
+        const int e1 = PASS == kFront ? item.s1 : share_of(item.s1, item.all, w.steps);
+        int e = PASS == kFront ? s0 : share_of(s0, item.all, w.steps);
         const int turns = (e1 - e + KW - 1) / KW;  // the same for all waves
         e += kg;
         const int32_t max_pages = a.max_pages - w.skip;  // 0: no keys of its own, and no entry behind the row's end is read
@@ -1404,7 +1503,7 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
         const float down = 1.0f / st.up;
         // A share goes on with at most one item, its first (part 0), and
         // leaves at most one unfinished, its last (part 1).
-        const int part_at = 2 * (int)blockIdx.x + (s0 == 0 ? 1 : 0);
+        const int part_at = PASS == kFront ? (int)blockIdx.x - 1 : 2 * (int)blockIdx.x + (s0 == 0 ? 1 : 0);
         float4_t *part = (float4_t *)(a.part + (int64_t)part_at * S::kPart);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -1423,14 +1522,12 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
             if (joined) {
                 front = front_row<D>(a, b, w.q0 + i, q_head, live, m, all_l, g);
                 f *= front.own;
-            } else if (PASS != kFront && !cut) {
+            } else if (!cut) {
                 f = all_l > 0.0f ? f / all_l : 0.0f;
             }
             auto give = [&](float4_t v, int y, int i4) {  // block y, product i4
                 if (cut) {
                     if (live) part[((rg * NT + n) * 4 * R + 4 * y + i4) * 64 + lane] = v;
-                } else if constexpr (PASS == kFront) {
-                    if (live) *front_of<D>(a, w.q0 + i, q_head, y, i4, g) = v;
                 } else {
                     if (joined && live) v += front_sum(a, front, 4 * y + i4);
                     store_row(live ? out : nullptr, v, y, i4, g);
@@ -1471,8 +1568,6 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
                 }
             }
             if (cut && kg == 0 && g == 0) a.part_ml[(int64_t)part_at * kRows + (rg * NT + n) * 16 + r] = make_float2(m, all_l);
-            if (PASS == kFront && !cut && kg == 0 && g == 0 && live)
-                a.front_ml[(w.q0 + i) * a.q_heads + q_head] = make_float2(m, all_l);
         }
         __syncthreads();
     }
@@ -2071,7 +2166,7 @@ template <int PASS> bool raise_pass()
 template <int D, int NT, int RG, int PASS>
 pn_status launch(const AttnArgs &a, hipStream_t s)
 {
-    const unsigned workers = PASS == kOwn ? (unsigned)((int64_t)a.B * a.c.heads * a.tiles) : (unsigned)a.workers;
+    const unsigned workers = PASS == kOwn ? (unsigned)((int64_t)a.B * a.c.heads * a.tiles) : (unsigned)(PASS == kFront ? a.grid : a.workers);
     hipLaunchKernelGGL((kv4_attn<D, NT, RG, PASS>), dim3(workers), dim3(kThreads), (Shape<D, NT, RG>::kLds), s, a);
     if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
     if constexpr (PASS == kWhole || PASS == kTail) {
