@@ -533,23 +533,47 @@ __device__ __forceinline__ bool front_item(const AttnArgs &a, FrontLds &s, Line 
         items = (int64_t)((w.qn * a.group + tile_rows - 1) / tile_rows) * a.c.heads;
         steps = (w.len + STEP - 1) / STEP;
     };
-    auto wave_total = [&](int64_t v) {
+    auto wave_total = [&](int64_t v) {  // a sum over lanes, by moves within rows and between them
+        auto add = [](int64_t x, auto move) {
+            return x + (int64_t)((uint64_t)move((uint32_t)(x >> 32)) << 32 | move((uint32_t)x));
+        };
+        v = add(v, [](uint32_t x) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xb1, 0xf, 0xf, false); });
+        v = add(v, [](uint32_t x) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4e, 0xf, 0xf, false); });
+        v = add(v, [](uint32_t x) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xf, 0xf, false); });
+        v = add(v, [](uint32_t x) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xf, 0xf, false); });
+        int64_t total = 0;
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
-        return v;
+        for (int row = 0; row < 64; row += 16)
+            total += (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), row) << 32 |
+                               (uint32_t)__builtin_amdgcn_readlane((int)v, row));
+        return total;
     };
     int64_t items = 0, steps = 0, T, before = 0;
-    if (a.groups <= 64) {  // every wave for itself
-        if (lane < a.groups) size(lane, items, steps);
-        T = quotient(wave_total(items * steps) + most - 1, most);
+    if (a.groups == 1) {
+        size(0, items, steps);
+        if (items == 0) return false;
+        const int64_t parts = items < most ? quotient(most, items) : 1;
+        T = quotient(steps + parts - 1, parts);
         if (T < a.least) T = a.least;
-        int64_t high = steps;
+        if (me < 0 || me >= items * quotient(steps + T - 1, T)) return false;
+        t.b = 0;
+    } else if (a.groups <= 64) {  // every wave for itself
+        if (lane < a.groups) size(lane, items, steps);
+        // the mean, and what leaves each item room for one part more
+        const int64_t work = wave_total(items * steps), all = wave_total(items);
+        T = quotient(work + most - 1, most);
+        int64_t high = all < most ? quotient(work, most - all) + 1 : 0;
+        if (all >= most) {  // one part each
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int64_t o = __shfl_xor(high, d, 64);
-            high = o > high ? o : high;
+            for (int d = 1; d < 64; d <<= 1) {
+                const int64_t o = __shfl_xor(steps > high ? steps : high, d, 64);
+                high = o > high ? o : high;
+            }
+            T = high > steps ? high : steps;
+            T = uniform64(T);
+            high = T;
         }
-        if (high < T) high = T;  // with it every item is one part
+        if (T < a.least) T = a.least;
         while (T < high) {
             const int64_t mid = (T + high) >> 1;
             if (wave_total(items * quotient(steps + mid - 1, mid)) <= most) high = mid;
@@ -1507,7 +1531,7 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
         float4_t *part = (float4_t *)(a.part + (int64_t)part_at * S::kPart);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            __syncthreads();
+            lds_barrier();  // (not for the last rows' stores)
             float m = kLowest, all_l = 0.0f;
             for (int y = 0; y < KW; ++y) m = max2(m, ml[rg * KW + y][16 * n + r][0]);
             for (int y = 0; y < KW; ++y)
@@ -1536,7 +1560,7 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
             if constexpr (RG == 1) {  // each wave adds its share of all waves' fragments
 #pragma unroll
                 for (int y = 0; y < 4 * R; ++y) frag[(wave * 4 * R + y) * 64 + lane] = st.o[n][y >> 2][y & 3] * f;
-                __syncthreads();
+                lds_barrier();
 #pragma unroll
                 for (int y = wave >> 2; y < R; y += kWaves / 4) {
                     const int f4 = 4 * y + (wave & 3);
@@ -1551,7 +1575,7 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
                     for (int y = 0; y < 4 * R; ++y)
                         frag[((rg * (KW - 1) + kg - 1) * 4 * R + y) * 64 + lane] = st.o[n][y >> 2][y & 3] * f;
                 }
-                __syncthreads();
+                lds_barrier();
                 if (kg == 0) {
 #pragma unroll
                     for (int y = 0; y < 4 * R; ++y) {
@@ -1569,7 +1593,7 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<D, NT, RG>())) void kv4_a
             }
             if (cut && kg == 0 && g == 0) a.part_ml[(int64_t)part_at * kRows + (rg * NT + n) * 16 + r] = make_float2(m, all_l);
         }
-        __syncthreads();
+        lds_barrier();
     }
 }
 
