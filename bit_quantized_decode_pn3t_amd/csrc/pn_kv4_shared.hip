@@ -38,8 +38,9 @@ Plan plan(const pn_kv4_cache *c, int q_heads, int B, int G, int64_t total_q, int
     Plan p;
     const int group = q_heads / c->heads, most = c->dim == 256 ? 2 : 4;  // row groups of a wave that the registers hold
     int64_t tiles, each;
-    // A group has about as many queries as the mean.
-    spread(((total_q + G - 1) / G * group + 15) / 16, most, tiles, each);
+    // No group has more rows than there are; a tile takes no more than it needs.
+    spread((total_q * group + 15) / 16, most, tiles, each);
+    if (G > 1 && tiles > 1) each = most;
     p.front.nt = (int)each;
     p.front.rg = 1;
     p.front.two = c->dim < 256 && each == 1;
