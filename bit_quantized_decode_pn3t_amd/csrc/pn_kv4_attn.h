@@ -1398,189 +1398,189 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Item &item, int 
     half8_t *queries = (half8_t *)(lds + S::kRing), *q = queries + rg * NT * 2 * R * 64;
     auto ml_at = [&](int w, int row) { return ml + 2 * (w * 16 * NT + row); };
 
-            const int s0 = item.s0, head = item.head, tile0 = item.tile0, rows = item.rows;
-            const bool cut = item.cut;
+    const int s0 = item.s0, head = item.head, tile0 = item.tile0, rows = item.rows;
+    const bool cut = item.cut;
 
-            Work w{item.c.w};
-            span<kStep>(a, w, tile0 / a.group, ((tile0 + kRows < rows ? tile0 + kRows : rows) - 1) / a.group);
-            // the wave's own rows (none: nothing is visible)
-            const int row0 = tile0 + rg * 16 * NT;
-            const int last = (row0 + 16 * NT < rows ? row0 + 16 * NT : rows) - 1;
-            const int32_t p0 = row0 < rows ? w.first + row0 / a.group : -1, p1 = row0 < rows ? w.first + last / a.group : -1;
+    Work w{item.c.w};
+    span<kStep>(a, w, tile0 / a.group, ((tile0 + kRows < rows ? tile0 + kRows : rows) - 1) / a.group);
+    // the wave's own rows (none: nothing is visible)
+    const int row0 = tile0 + rg * 16 * NT;
+    const int last = (row0 + 16 * NT < rows ? row0 + 16 * NT : rows) - 1;
+    const int32_t p0 = row0 < rows ? w.first + row0 / a.group : -1, p1 = row0 < rows ? w.first + last / a.group : -1;
 
-            // The same part of the steps that this tile has.
-            auto place = [&](int e) { return e < w.sink_steps ? e : e - w.sink_steps + w.lo; };
-            const int e1 = PASS == kFront ? item.s1 : share_of(item.s1, item.all, w.steps);
-            int e = PASS == kFront ? s0 : share_of(s0, item.all, w.steps);
-            const int turns = (e1 - e + KW - 1) / KW;  // the same for all waves
-            e += kg;
-            const int32_t max_pages = a.max_pages - w.skip;  // 0: no keys of its own, and no entry behind the row's end is read
-            const int32_t *row = uniform_ptr(a.table + (int64_t)b * a.ld_table + (max_pages > 0 ? w.skip : 0));
-            const uint64_t head_base = (uint64_t)a.c.pages + (uint64_t)head * a.c.chunk;
-            const int32_t page_bytes = a.c.heads * a.c.chunk;
-            // pages of the steps in the ring, and of the next to be staged
-            Pages held[S::kAhead + 1];
-    #pragma unroll
-            for (int i = 0; i <= S::kAhead; ++i) held[i] = pages_of(a, row, max_pages, place(e + KW * i), e + KW * i < e1);
-            // the queries into LDS
-            for (int y = tid; y < RG * NT * 2 * R * 64; y += kThreads) {
-                const int at = tile0 + 16 * (y / (2 * R * 64)) + (y & 15), i = at / a.group;
-                const int e = 32 * (y / 64 % (2 * R)) + 8 * (y >> 4 & 3);
-                half8_t v = (half8_t)(_Float16)0.0f;
-                if (at < rows) v = *(const half8_t *)(a.q + (w.q0 + i) * a.ldq + (head * a.group + at - i * a.group) * D + e);
-                queries[y] = a.negate ? -v : v;
-            }
-            State<D, NT> st;
-    #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-    #pragma unroll
-                for (int y = 0; y < R; ++y)
-    #pragma unroll
-                    for (int i2 = 0; i2 < 4; ++i2) st.o[n][y][i2] = (float4_t){0, 0, 0, 0};
-                st.m[n] = kLowest;
-                st.l[n] = 0.0f;
-            }
-            st.up = 1.0f;
-            st.cap = 0;
+    // The same part of the steps that this tile has.
+    auto place = [&](int e) { return e < w.sink_steps ? e : e - w.sink_steps + w.lo; };
+    const int e1 = PASS == kFront ? item.s1 : share_of(item.s1, item.all, w.steps);
+    int e = PASS == kFront ? s0 : share_of(s0, item.all, w.steps);
+    const int turns = (e1 - e + KW - 1) / KW;  // the same for all waves
+    e += kg;
+    const int32_t max_pages = a.max_pages - w.skip;  // 0: no keys of its own, and no entry behind the row's end is read
+    const int32_t *row = uniform_ptr(a.table + (int64_t)b * a.ld_table + (max_pages > 0 ? w.skip : 0));
+    const uint64_t head_base = (uint64_t)a.c.pages + (uint64_t)head * a.c.chunk;
+    const int32_t page_bytes = a.c.heads * a.c.chunk;
+    // pages of the steps in the ring, and of the next to be staged
+    Pages held[S::kAhead + 1];
+#pragma unroll
+    for (int i = 0; i <= S::kAhead; ++i) held[i] = pages_of(a, row, max_pages, place(e + KW * i), e + KW * i < e1);
+    // the queries into LDS
+    for (int y = tid; y < RG * NT * 2 * R * 64; y += kThreads) {
+        const int at = tile0 + 16 * (y / (2 * R * 64)) + (y & 15), i = at / a.group;
+        const int e = 32 * (y / 64 % (2 * R)) + 8 * (y >> 4 & 3);
+        half8_t v = (half8_t)(_Float16)0.0f;
+        if (at < rows) v = *(const half8_t *)(a.q + (w.q0 + i) * a.ldq + (head * a.group + at - i * a.group) * D + e);
+        queries[y] = a.negate ? -v : v;
+    }
+    State<D, NT> st;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int y = 0; y < R; ++y)
+#pragma unroll
+            for (int i2 = 0; i2 < 4; ++i2) st.o[n][y][i2] = (float4_t){0, 0, 0, 0};
+        st.m[n] = kLowest;
+        st.l[n] = 0.0f;
+    }
+    st.up = 1.0f;
+    st.cap = 0;
 
-    #pragma unroll
-            for (int i = 0; i < S::kAhead; ++i)
-                stage<D, RG>(a, ring + i * G::kStage, off, held[i], place(e + KW * i), head_base, page_bytes, rg);
-            // the queries are there; a bare barrier, so that the loads fly on
-            __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
-            asm volatile("" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < S::kAhead; ++i)
+        stage<D, RG>(a, ring + i * G::kStage, off, held[i], place(e + KW * i), head_base, page_bytes, rg);
+    // the queries are there; a bare barrier, so that the loads fly on
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    int at = 0;  // stage of the step at work
+    for (int turn2 = 0; turn2 < turns && (RG > 1 || e < e1); ++turn2, e += KW) {
+        if constexpr (RG == 1) {
+            wait_loads<(S::kStages - 1) * 2 * (2 * G::kEach + 1)>();
+        } else {
+            // this wave's loads of the step have landed; after the
+            // barrier all have, and no wave reads the stage before it
+            if (rg & 1) wait_loads<(S::kStages - 2) * (G::kEach + 1)>();
+            else wait_loads<(S::kStages - 2) * G::kEach>();
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
-            int at = 0;  // stage of the step at work
-            for (int turn2 = 0; turn2 < turns && (RG > 1 || e < e1); ++turn2, e += KW) {
-                if constexpr (RG == 1) {
-                    wait_loads<(S::kStages - 1) * 2 * (2 * G::kEach + 1)>();
-                } else {
-                    // this wave's loads of the step have landed; after the
-                    // barrier all have, and no wave reads the stage before it
-                    if (rg & 1) wait_loads<(S::kStages - 2) * (G::kEach + 1)>();
-                    else wait_loads<(S::kStages - 2) * G::kEach>();
-                    __builtin_amdgcn_s_barrier();
-                    asm volatile("" ::: "memory");
-                    const int to = at > 0 ? at - 1 : S::kStages - 1;
-                    stage<D, RG>(a, ring + to * G::kStage, off, held[S::kAhead], place(e + KW * S::kAhead), head_base, page_bytes,
-                                 rg);
-                }
-                const int token0 = place(e) * kStep;
-                uint8_t *from = ring + at * G::kStage;
-                at = at + 1 < S::kStages ? at + 1 : 0;
-                Mask mask;
-                mask.page[0] = valid(a, held[0].p[0]) >= 0;
-                mask.page[1] = valid(a, held[0].p[1]) >= 0;
-                mask.token0 = token0;
-                mask.end = w.len;
-                mask.low = p0;
-                mask.high = p1;
-                mask.row0 = row0;
-                mask.rows = rows;
-                mask.first = w.first;
-                mask.some = !(mask.page[0] && mask.page[1] && token0 + kStep <= w.len && token0 + kStep - 1 <= p0 &&
-                              (a.window <= 0 || (int64_t)token0 + a.window > p1 || token0 + kStep <= a.sinks));
-                // A row group sees less than its workgroup's tile.
-                const bool none = RG > 1 && (e >= e1 || token0 > p1 ||
-                                             (a.window > 0 && (int64_t)token0 + kStep - 1 + a.window <= p0 && token0 >= a.sinks));
-                if constexpr (PASS == kFront) {
-                    const int left = w.len - token0;  // 1 and up
-                    const Seen seen = {!(mask.page[0] && mask.page[1] && left >= kStep),
-                                       {mask.page[0] ? left : 0, mask.page[1] ? left - 16 : 0}};
-                    advance_front<D, NT>(st, from, q, a, seen, lane);
-                } else {
-                    if (!none) advance<D, NT>(st, from, q, a, mask, lane);
-                }
-                __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the stage has been read
-                asm volatile("" ::: "memory");
-                if constexpr (RG == 1)
-                    stage<D, RG>(a, from, off, held[S::kAhead], place(e + KW * S::kAhead), head_base, page_bytes, rg);
-    #pragma unroll
-                for (int y = 0; y < S::kAhead; ++y) held[y] = held[y + 1];
-                const int s = e + KW * (S::kAhead + 1);
-                held[S::kAhead] = pages_of(a, row, max_pages, place(s), s < e1);
-            }
-            wait_loads<0>();  // nothing is written into the ring any more
+            const int to = at > 0 ? at - 1 : S::kStages - 1;
+            stage<D, RG>(a, ring + to * G::kStage, off, held[S::kAhead], place(e + KW * S::kAhead), head_base, page_bytes,
+                         rg);
+        }
+        const int token0 = place(e) * kStep;
+        uint8_t *from = ring + at * G::kStage;
+        at = at + 1 < S::kStages ? at + 1 : 0;
+        Mask mask;
+        mask.page[0] = valid(a, held[0].p[0]) >= 0;
+        mask.page[1] = valid(a, held[0].p[1]) >= 0;
+        mask.token0 = token0;
+        mask.end = w.len;
+        mask.low = p0;
+        mask.high = p1;
+        mask.row0 = row0;
+        mask.rows = rows;
+        mask.first = w.first;
+        mask.some = !(mask.page[0] && mask.page[1] && token0 + kStep <= w.len && token0 + kStep - 1 <= p0 &&
+                      (a.window <= 0 || (int64_t)token0 + a.window > p1 || token0 + kStep <= a.sinks));
+        // A row group sees less than its workgroup's tile.
+        const bool none = RG > 1 && (e >= e1 || token0 > p1 ||
+                                     (a.window > 0 && (int64_t)token0 + kStep - 1 + a.window <= p0 && token0 >= a.sinks));
+        if constexpr (PASS == kFront) {
+            const int left = w.len - token0;  // 1 and up
+            const Seen seen = {!(mask.page[0] && mask.page[1] && left >= kStep),
+                               {mask.page[0] ? left : 0, mask.page[1] ? left - 16 : 0}};
+            advance_front<D, NT>(st, from, q, a, seen, lane);
+        } else {
+            if (!none) advance<D, NT>(st, from, q, a, mask, lane);
+        }
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the stage has been read
+        asm volatile("" ::: "memory");
+        if constexpr (RG == 1)
+            stage<D, RG>(a, from, off, held[S::kAhead], place(e + KW * S::kAhead), head_base, page_bytes, rg);
+#pragma unroll
+        for (int y = 0; y < S::kAhead; ++y) held[y] = held[y + 1];
+        const int s = e + KW * (S::kAhead + 1);
+        held[S::kAhead] = pages_of(a, row, max_pages, place(s), s < e1);
+    }
+    wait_loads<0>();  // nothing is written into the ring any more
 
-            // Join the waves of the same rows: the rows' maxima and sums, then
-            // the fragments.
-    #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float l = PASS == kFront ? st.l[n] : group_sum(st.l[n]);
-                if (g == 0) ml_at(wave, 16 * n + r)[0] = st.m[n], ml_at(wave, 16 * n + r)[1] = l;
+    // Join the waves of the same rows: the rows' maxima and sums, then
+    // the fragments.
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const float l = PASS == kFront ? st.l[n] : group_sum(st.l[n]);
+        if (g == 0) ml_at(wave, 16 * n + r)[0] = st.m[n], ml_at(wave, 16 * n + r)[1] = l;
+    }
+    float4_t *frag = (float4_t *)lds;  // [wave][4 b + i][lane]
+    const float down = 1.0f / st.up;
+    // A share goes on with at most one item, its first (part 0), and
+    // leaves at most one unfinished, its last (part 1).
+    const int part_at = PASS == kFront ? (int)blockIdx.x - 1 : 2 * (int)blockIdx.x + (s0 == 0 ? 1 : 0);
+    float4_t *part = (float4_t *)(a.part + (int64_t)part_at * (PASS == kFront ? a.f_tile * D : S::kPart));
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        lds_barrier();  // (not for the last rows' stores)
+        float m = kLowest, all_l = 0.0f;
+        for (int y = 0; y < KW; ++y) m = max2(m, ml_at(rg * KW + y, 16 * n + r)[0]);
+        for (int y = 0; y < KW; ++y)
+            all_l += ml_at(rg * KW + y, 16 * n + r)[1] * __builtin_amdgcn_exp2f((ml_at(rg * KW + y, 16 * n + r)[0] - m) * a.c2);
+        float f = __builtin_amdgcn_exp2f((st.m[n] - m) * a.c2) * down;
+        const int row_at = row0 + 16 * n + r, i = row_at / a.group;
+        const bool live = row_at < rows;
+        const int q_head = head * a.group + row_at - i * a.group;
+        uint16_t *out = a.out + (w.q0 + i) * a.ldo + (int64_t)q_head * D;
+        FrontRow front;
+        const bool joined = joins(PASS) && !cut && w.skip > 0;  // the same for the item
+        if (joined) {
+            front = front_row<D>(a, b, w.q0 + i, q_head, live, m, all_l, g);
+            f *= front.own;
+        } else if (!cut) {
+            f = all_l > 0.0f ? f / all_l : 0.0f;
+        }
+        auto give = [&](float4_t v, int y, int i4) {  // block y, product i4
+            if (cut) {
+                if (live) part[((rg * NT + n) * 4 * R + 4 * y + i4) * 64 + lane] = v;
+            } else {
+                if (joined && live) v += front_sum(a, front, 4 * y + i4);
+                store_row(live ? out : nullptr, v, y, i4, g);
             }
-            float4_t *frag = (float4_t *)lds;  // [wave][4 b + i][lane]
-            const float down = 1.0f / st.up;
-            // A share goes on with at most one item, its first (part 0), and
-            // leaves at most one unfinished, its last (part 1).
-            const int part_at = PASS == kFront ? (int)blockIdx.x - 1 : 2 * (int)blockIdx.x + (s0 == 0 ? 1 : 0);
-            float4_t *part = (float4_t *)(a.part + (int64_t)part_at * (PASS == kFront ? a.f_tile * D : S::kPart));
-    #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                lds_barrier();  // (not for the last rows' stores)
-                float m = kLowest, all_l = 0.0f;
-                for (int y = 0; y < KW; ++y) m = max2(m, ml_at(rg * KW + y, 16 * n + r)[0]);
-                for (int y = 0; y < KW; ++y)
-                    all_l += ml_at(rg * KW + y, 16 * n + r)[1] * __builtin_amdgcn_exp2f((ml_at(rg * KW + y, 16 * n + r)[0] - m) * a.c2);
-                float f = __builtin_amdgcn_exp2f((st.m[n] - m) * a.c2) * down;
-                const int row_at = row0 + 16 * n + r, i = row_at / a.group;
-                const bool live = row_at < rows;
-                const int q_head = head * a.group + row_at - i * a.group;
-                uint16_t *out = a.out + (w.q0 + i) * a.ldo + (int64_t)q_head * D;
-                FrontRow front;
-                const bool joined = joins(PASS) && !cut && w.skip > 0;  // the same for the item
-                if (joined) {
-                    front = front_row<D>(a, b, w.q0 + i, q_head, live, m, all_l, g);
-                    f *= front.own;
-                } else if (!cut) {
-                    f = all_l > 0.0f ? f / all_l : 0.0f;
-                }
-                auto give = [&](float4_t v, int y, int i4) {  // block y, product i4
-                    if (cut) {
-                        if (live) part[((rg * NT + n) * 4 * R + 4 * y + i4) * 64 + lane] = v;
-                    } else {
-                        if (joined && live) v += front_sum(a, front, 4 * y + i4);
-                        store_row(live ? out : nullptr, v, y, i4, g);
-                    }
-                };
-                if constexpr (RG == 1) {  // each wave adds its share of all waves' fragments
-    #pragma unroll
-                    for (int y = 0; y < 4 * R; ++y) frag[(wave * 4 * R + y) * 64 + lane] = st.o[n][y >> 2][y & 3] * f;
-                    lds_barrier();
-    #pragma unroll
-                    for (int y = wave >> 2; y < R; y += kWaves / 4) {
-                        const int f4 = 4 * y + (wave & 3);
-                        float4_t v = frag[f4 * 64 + lane];
-    #pragma unroll
-                        for (int z = 1; z < kWaves; ++z) v += frag[(z * 4 * R + f4) * 64 + lane];
-                        give(v, y, wave & 3);
-                    }
-                } else {  // the first along the keys adds the others'
-                    if (kg > 0) {
-    #pragma unroll
-                        for (int y = 0; y < 4 * R; ++y)
-                            frag[((rg * (KW - 1) + kg - 1) * 4 * R + y) * 64 + lane] = st.o[n][y >> 2][y & 3] * f;
-                    }
-                    lds_barrier();
-                    if (kg == 0) {
-    #pragma unroll
-                        for (int y = 0; y < 4 * R; ++y) {
-                            float4_t v = st.o[n][y >> 2][y & 3] * f;
-    #pragma unroll
-                            for (int z = 0; z < KW - 1; ++z) v += frag[((rg * (KW - 1) + z) * 4 * R + y) * 64 + lane];
-                            if (joined) frag[(rg * (KW - 1) * 4 * R + y) * 64 + lane] = v;  // where the lane alone has read
-                            else give(v, y >> 2, y & 3);
-                        }
-                        if (joined) {
-    #pragma unroll 1
-                            for (int y = 0; y < 4 * R; ++y) give(frag[(rg * (KW - 1) * 4 * R + y) * 64 + lane], y >> 2, y & 3);
-                        }
-                    }
-                }
-                if (cut && kg == 0 && g == 0) a.part_ml[(int64_t)part_at * (PASS == kFront ? a.f_tile : kRows) + (rg * NT + n) * 16 + r] = make_float2(m, all_l);
+        };
+        if constexpr (RG == 1) {  // each wave adds its share of all waves' fragments
+#pragma unroll
+            for (int y = 0; y < 4 * R; ++y) frag[(wave * 4 * R + y) * 64 + lane] = st.o[n][y >> 2][y & 3] * f;
+            lds_barrier();
+#pragma unroll
+            for (int y = wave >> 2; y < R; y += kWaves / 4) {
+                const int f4 = 4 * y + (wave & 3);
+                float4_t v = frag[f4 * 64 + lane];
+#pragma unroll
+                for (int z = 1; z < kWaves; ++z) v += frag[(z * 4 * R + f4) * 64 + lane];
+                give(v, y, wave & 3);
+            }
+        } else {  // the first along the keys adds the others'
+            if (kg > 0) {
+#pragma unroll
+                for (int y = 0; y < 4 * R; ++y)
+                    frag[((rg * (KW - 1) + kg - 1) * 4 * R + y) * 64 + lane] = st.o[n][y >> 2][y & 3] * f;
             }
             lds_barrier();
+            if (kg == 0) {
+#pragma unroll
+                for (int y = 0; y < 4 * R; ++y) {
+                    float4_t v = st.o[n][y >> 2][y & 3] * f;
+#pragma unroll
+                    for (int z = 0; z < KW - 1; ++z) v += frag[((rg * (KW - 1) + z) * 4 * R + y) * 64 + lane];
+                    if (joined) frag[(rg * (KW - 1) * 4 * R + y) * 64 + lane] = v;  // where the lane alone has read
+                    else give(v, y >> 2, y & 3);
+                }
+                if (joined) {
+#pragma unroll 1
+                    for (int y = 0; y < 4 * R; ++y) give(frag[(rg * (KW - 1) * 4 * R + y) * 64 + lane], y >> 2, y & 3);
+                }
+            }
+        }
+        if (cut && kg == 0 && g == 0) a.part_ml[(int64_t)part_at * (PASS == kFront ? a.f_tile : kRows) + (rg * NT + n) * 16 + r] = make_float2(m, all_l);
+    }
+    lds_barrier();
 }
 
 template <int D, int NT, int RG, int PASS>
