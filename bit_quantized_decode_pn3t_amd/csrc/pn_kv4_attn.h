@@ -1317,7 +1317,27 @@ template <int D, int NT, int RG> struct Shape {
 // 73 and 80 us).
 template <int D, int NT, int RG> constexpr int waves_per_simd() { return D < 256 && NT == 1 && RG == 1 ? 4 : 2; }
 
-// The parts of the shared keys' sums for a row, as lane (r, g) sees them.
+// Where the parts of the shared keys' sums for a row are.
+struct FrontPlace {
+    int32_t first, parts;  // in f_part; parts 0: none
+    int32_t local;         // the row in its tile
+};
+// Without a row (not live) nothing is read.
+__device__ __forceinline__ FrontPlace front_place(const AttnArgs &a, const Member &in, int64_t query, int q_head, bool live)
+{
+    FrontPlace p = {0, 0, 0};
+    if (live) {
+        const int head = q_head / a.group, row = (int32_t)(query - in.q0) * a.group + q_head - head * a.group;
+        const int tile = row / in.rows;
+        const int2 item = a.items[(int64_t)(in.tile + tile) * a.c.heads + head];
+        p.first = item.x;
+        p.parts = item.y;
+        p.local = row - tile * in.rows;
+    }
+    return p;
+}
+
+// As lane (r, g) sees them.
 struct FrontRow {
     const float4_t *at;   // of the first part
     const float2 *ml;
@@ -1326,25 +1346,32 @@ struct FrontRow {
     float top;            // their largest maximum
     float own, front;     // factors of the row's own sum and of the parts relative to top
 };
+template <int D> __device__ __forceinline__ void front_at(const AttnArgs &a, const FrontPlace &p, int g, FrontRow &f)
+{
+    // (groups that overlap may leave an entry unwritten)
+    const bool ok = p.first >= 0 && p.parts > 0 && p.parts < a.grid - p.first;
+    const int64_t first = ok ? p.first : 0;
+    f.parts = ok ? p.parts : 0;
+    f.step = (int64_t)a.f_tile * (D / 4);
+    f.at = (const float4_t *)a.f_part + first * f.step + (p.local >> 4) * (D * 4) + (p.local & 15) + 16 * g;
+    f.ml = a.f_part_ml + first * a.f_tile + p.local;
+}
+// The factors for a row's own (m, l) and parts of `sum` relative to f.top.  All are 0 where nothing is visible.
+__device__ __forceinline__ void front_factors(const AttnArgs &a, float m, float l, float sum, FrontRow &f)
+{
+    const float all = max2(m, f.top);
+    const float f0 = __builtin_amdgcn_exp2f((m - all) * a.c2), f1 = __builtin_amdgcn_exp2f((f.top - all) * a.c2);
+    const float total = l * f0 + sum * f1, by = total > 0.0f ? 1.0f / total : 0.0f;
+    f.own = f0 * by;
+    f.front = f1 * by;
+}
 
-// Joined with the row's own (m, l).  Without a row nothing is read; all factors
-// are 0 where nothing is visible.  For all lanes of a wave together.
+// Joined with the row's own (m, l), for all lanes of a wave together.
 template <int D>
-__device__ __forceinline__ FrontRow front_row(const AttnArgs &a, int b, int64_t query, int q_head, bool live, float m, float l, int g)
+__device__ __forceinline__ FrontRow front_row(const AttnArgs &a, const FrontPlace &p, float m, float l, int g)
 {
     FrontRow f;
-    f.parts = 0;
-    if (live) {
-        const Member in = a.members[b];
-        const int head = q_head / a.group, row = (int32_t)(query - in.q0) * a.group + q_head - head * a.group;
-        const int tile = row / in.rows, local = row - tile * in.rows;
-        const int2 item = a.items[(int64_t)(in.tile + tile) * a.c.heads + head];
-        f.step = (int64_t)a.f_tile * (D / 4);
-        f.at = (const float4_t *)a.f_part + item.x * f.step + (local >> 4) * (D * 4) + (local & 15) + 16 * g;
-        f.ml = a.f_part_ml + (int64_t)item.x * a.f_tile + local;
-        // (groups that overlap may leave an entry unwritten)
-        f.parts = item.x >= 0 && item.y > 0 && item.y < a.grid - item.x ? item.y : 0;
-    }
+    front_at<D>(a, p, g, f);
     float top = kLowest, sum = 0.0f;
     for (int j = g; j < f.parts; j += 4) top = max2(top, f.ml[(int64_t)j * a.f_tile].x);
     f.top = top = group_max(top);
@@ -1352,12 +1379,7 @@ __device__ __forceinline__ FrontRow front_row(const AttnArgs &a, int b, int64_t 
         const float2 x = f.ml[(int64_t)j * a.f_tile];
         sum += x.y * __builtin_amdgcn_exp2f((x.x - top) * a.c2);
     }
-    sum = group_sum(sum);
-    const float all = max2(m, top);
-    const float f0 = __builtin_amdgcn_exp2f((m - all) * a.c2), f1 = __builtin_amdgcn_exp2f((top - all) * a.c2);
-    const float total = l * f0 + sum * f1, by = total > 0.0f ? 1.0f / total : 0.0f;
-    f.own = f0 * by;
-    f.front = f1 * by;
+    front_factors(a, m, l, group_sum(sum), f);
     return f;
 }
 
@@ -1380,6 +1402,49 @@ __device__ __forceinline__ float4_t front_sum(const AttnArgs &a, const FrontRow 
             if (j0 + j < f.parts) v += x[j] * __builtin_amdgcn_exp2f((w[j] - f.top) * a.c2);
     }
     return v * f.front;
+}
+
+// Product y of a row, v relative to its own (m, l), joined with its parts: of
+// few of them all that is needed is on its way at once.
+template <int D>
+__device__ __forceinline__ float4_t front_join(const AttnArgs &a, const FrontPlace &p, float m, float l, float4_t v, int y, int g)
+{
+    constexpr int kFew = 8;
+    FrontRow f;
+    front_at<D>(a, p, g, f);
+    float4_t x[kFew];
+    float2 ml[kFew];
+    const int few = f.parts < kFew ? f.parts : kFew;
+    if (few > 0) {  // (not a place of the row's)
+#pragma unroll
+        for (int j = 0; j < kFew; ++j) {
+            const int64_t at = j < few ? j : 0;
+            x[j] = f.at[at * f.step + 64 * y];
+            ml[j] = f.ml[at * a.f_tile];
+        }
+    }
+    f.top = kLowest;
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kFew; ++j)
+        if (j < few) f.top = max2(f.top, ml[j].x);
+    for (int j = kFew; j < f.parts; ++j) f.top = max2(f.top, f.ml[(int64_t)j * a.f_tile].x);
+    float4_t all = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < kFew; ++j)
+        if (j < few) {
+            const float w = __builtin_amdgcn_exp2f((ml[j].x - f.top) * a.c2);
+            sum += ml[j].y * w;
+            all += x[j] * w;
+        }
+    for (int j = kFew; j < f.parts; ++j) {
+        const float2 z = f.ml[(int64_t)j * a.f_tile];
+        const float w = __builtin_amdgcn_exp2f((z.x - f.top) * a.c2);
+        sum += z.y * w;
+        all += f.at[j * f.step + 64 * y] * w;
+    }
+    front_factors(a, m, l, sum, f);
+    return v * f.own + all * f.front;
 }
 
 // One item (or part of one) of request b, by the whole workgroup.  ml: a wave's
@@ -1422,6 +1487,17 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Item &item, int 
     Pages held[S::kAhead + 1];
 #pragma unroll
     for (int i = 0; i <= S::kAhead; ++i) held[i] = pages_of(a, row, max_pages, place(e + KW * i), e + KW * i < e1);
+    // where the shared keys' parts are, for the end
+    FrontPlace fronts[joins(PASS) ? NT : 1];
+    const bool joined = joins(PASS) && !cut && w.skip > 0;  // the same for the item
+    if (joined) {
+        const Member in = a.members[b];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int at = row0 + 16 * n + r, i = at / a.group;
+            fronts[n] = front_place(a, in, w.q0 + i, head * a.group + at - i * a.group, at < rows);
+        }
+    }
     // the queries into LDS
     for (int y = tid; y < RG * NT * 2 * R * 64; y += kThreads) {
         const int at = tile0 + 16 * (y / (2 * R * 64)) + (y & 15), i = at / a.group;
@@ -1528,19 +1604,19 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Item &item, int 
         const bool live = row_at < rows;
         const int q_head = head * a.group + row_at - i * a.group;
         uint16_t *out = a.out + (w.q0 + i) * a.ldo + (int64_t)q_head * D;
-        FrontRow front;
-        const bool joined = joins(PASS) && !cut && w.skip > 0;  // the same for the item
-        if (joined) {
-            front = front_row<D>(a, b, w.q0 + i, q_head, live, m, all_l, g);
-            f *= front.own;
-        } else if (!cut) {
+        if (!cut && !joined) {
             f = all_l > 0.0f ? f / all_l : 0.0f;
         }
+        auto join = [&](float4_t v, int y) {  // product y of all
+            if constexpr (joins(PASS)) {
+                if (live) v = front_join<D>(a, fronts[n], m, all_l, v, y, g);
+            }
+            return v;
+        };
         auto give = [&](float4_t v, int y, int i4) {  // block y, product i4
             if (cut) {
                 if (live) part[((rg * NT + n) * 4 * R + 4 * y + i4) * 64 + lane] = v;
             } else {
-                if (joined && live) v += front_sum(a, front, 4 * y + i4);
                 store_row(live ? out : nullptr, v, y, i4, g);
             }
         };
@@ -1554,7 +1630,7 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Item &item, int 
                 float4_t v = frag[f4 * 64 + lane];
 #pragma unroll
                 for (int z = 1; z < kWaves; ++z) v += frag[(z * 4 * R + f4) * 64 + lane];
-                give(v, y, wave & 3);
+                give(joined ? join(v, f4) : v, y, wave & 3);
             }
         } else {  // the first along the keys adds the others'
             if (kg > 0) {
@@ -1574,7 +1650,7 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Item &item, int 
                 }
                 if (joined) {
 #pragma unroll 1
-                    for (int y = 0; y < 4 * R; ++y) give(frag[(rg * (KW - 1) * 4 * R + y) * 64 + lane], y >> 2, y & 3);
+                    for (int y = 0; y < 4 * R; ++y) give(join(frag[(rg * (KW - 1) * 4 * R + y) * 64 + lane], y), y >> 2, y & 3);
                 }
             }
         }
@@ -2026,7 +2102,8 @@ __global__ __launch_bounds__(kThreads) void kv4_prompt(AttnArgs a)
             if constexpr (PASS == kTail) {
                 const int row_at = row0 + 16 * n + r, i = row_at / a.group, q_head = head * a.group + row_at - i * a.group;
                 if (w.skip > 0) {
-                    const FrontRow front = front_row<D>(a, b, w.q0 + i, q_head, row_at < rows, m[n], all_l, g);
+                    const FrontPlace place = front_place(a, a.members[b], w.q0 + i, q_head, row_at < rows);
+                    const FrontRow front = front_row<D>(a, place, m[n], all_l, g);
                     f = 1.0f;
 #pragma unroll
                     for (int y = 0; y < 4 * R; ++y) {
@@ -2120,7 +2197,7 @@ __global__ __launch_bounds__(64 * W) void kv4_join(AttnArgs a, int groups)
         if constexpr (PASS == kTail) {
             const int b = (int)((uint32_t)c.head >> 16);
             if (uniform(a.members[b].skip) > 0) {
-                const FrontRow front = front_row<D>(a, b, c.q0 + q, q_head, live, m, l, g);
+                const FrontRow front = front_row<D>(a, front_place(a, a.members[b], c.q0 + q, q_head, live), m, l, g);
                 f = front.own;
                 if (live) o = o * f + front_sum(a, front, 4 * y + wave);
                 f = 1.0f;

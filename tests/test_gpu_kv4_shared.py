@@ -159,6 +159,12 @@ def test_tails_split_over_workgroups(dim, q):
     run([21, dim, q], [q, q, 1], [5000, 300, 4200], [2], [20], dim, 32, 1, 16 if q > 1 else 3, own_columns=False)
 
 
+@pytest.mark.parametrize("dim,q", [(64, 1), (128, 1), (256, 1), (64, 40), (128, 20), (256, 12)])
+def test_many_parts_and_split_tails(dim, q):
+    """A prefix in more parts than are joined at once, tails in parts, few rows and many."""
+    run([23, dim, q], [q, 1], [4500, 40], [2], [110], dim, 32, 1, 16 if q > 1 else 3, own_columns=False)
+
+
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_several_row_tiles(dim):
     """Requests of more rows than a workgroup takes of them, over a prefix in parts."""
