@@ -519,10 +519,12 @@ __device__ __forceinline__ bool own_item(const AttnArgs &a, Line &t, Item &m, in
 // kFront: workgroup 0 notes the members; the others' parts, in order: group,
 // row tile, head, place along the keys.  All items are cut into parts of up to
 // T steps, T the least with which the parts are no more than the workgroups:
-// equal parts, one a workgroup, as an item's start and end cost as much as some
-// eight steps (parts of an even line, of two items in most workgroups: 64
-// requests behind 16384 tokens 53 us, this way 37).  More than 64 groups are
-// not searched for T: it is their mean.  False: no such part.
+// equal parts, one a workgroup, so that none starts and ends two items.  Against
+// parts of an even line, when this was taken, whole calls: 64 requests behind
+// 16384 tokens 72.4 -> 69.8 us, 32 behind 65536 138.2 -> 135.6, 4 behind 1024
+// 22.6 -> 21.4, but 16 of 8 drafts behind 5024 68.9 -> 72.0 and three groups of
+// 15 83.4 -> 86.3.  More than 64 groups are not searched for T: it is their
+// mean.  False: no such part.
 struct FrontLds {
     int64_t scan[kWaves];
     int64_t steps;

@@ -8,7 +8,25 @@
 // is unpacked and multiplied for all rows of a tile at once.  The rows' sums
 // stay in fp32, relative to their own maxima, and in as many parts as
 // workgroups shared a tile's keys.  The second launch gives each request's
-// queries its own keys and joins them with those parts.
+// queries its own keys and joins them with those parts: a workgroup an item
+// (kOwn), or dealt as pn_kv4_attn deals them, with its join (kTail).
+//
+// A tile is up to four 16-row groups, two where heads are 256 wide: what the
+// registers hold.  Its eight waves take every eighth step of 32 tokens and do
+// not wait for one another.  A form whose waves unpacked the keys together into
+// LDS had a barrier a step: 64 requests behind 16384 tokens 71 us and 32 behind
+// 65536 161, this form's first version 61 and 115.
+//
+// What bounds it: issue of vector instructions and products, and what is run
+// once.  64 requests behind 16384 tokens, 128 wide (25.8 GFLOP): kFront 56.5 us,
+// vector instructions active 56 % of a SIMD's time, products 24 %, which barely
+// overlap (two waves a SIMD of 32 products and 128 fma each, ns: 463 and 483
+// alone, 778 one after the other).  kOwn 17.6: about 5 until its first step, 5
+// for that and the waves' join, 5 for further steps, 3.6 for the front's parts.
+// 32 behind 65536, 256 wide (51.5 GFLOP): 112 us, vector instructions 62 %,
+// then 24.4 and 11.3.  Each request by pn_kv4_attn instead, passes of one run:
+// 64 requests 230 us (here 75), 32 393 (137); 16 of 8 drafts behind 5024 71.0
+// (71.7) and 4 behind 1024 16.8 (19.4): there sharing does not pay.
 #include "pn_kv4_attn.h"
 
 namespace {
@@ -54,6 +72,10 @@ Plan plan(const pn_kv4_cache *c, int q_heads, int B, int G, int64_t total_q, int
     spread((max_q * group + 15) / 16, most, tiles, each);
     p.tiles = (int)tiles;
     const int64_t tails = max_kv - max_shared * c->page_size;
+    // A line where tails are long and items few (32 requests of up to 4000 own
+    // tokens, 256 wide: a workgroup an item 61.6 us, a line 31.7 and 17.0 for its
+    // join when this was taken); else an item a workgroup (64 requests of up to
+    // 1000, 128 wide: 22.1 us, a line 30.3 before its join).
     p.line = p.own.rg > 1 || (tails > 2 * kShare * kStep && B * c->heads * tiles < 2 * device_cus());
     if (!p.line) {
         p.own.nt = (int)each;

@@ -18,6 +18,10 @@
 // whole length where there are rows enough); the next step's loads, past the
 // caches, are in flight meanwhile.  Chunks of a row leave their sums and K
 // keys in the workspace, and logp_join joins them.
+//
+// What bounds it: 509 rows of 248320 (505 MB) 93 us, 5.4 TB/s, with vector
+// instructions (17.6 an entry) active 74 % of a SIMD's time, and 5.9 for the
+// join; one row of 62080 6.3 and 4.4, two launches.
 #include <type_traits>
 
 #include "pn_device.h"

@@ -9,6 +9,10 @@
 // there; the two means are the only things its threads wait for each other
 // for.  Everything is fp32, rounded once where it is written; sums of squares
 // run per thread, then over the wave and the waves in a fixed order.
+//
+// What bounds it: memory in large calls, 8191 rows of 5120 with a gate (755 MB)
+// 136 us, 5.5 TB/s; a launch and the reductions in small ones, 512 rows 7.6 us,
+// one row 3.8.
 #include "pn_device.h"
 #include "pn_kv4.h"
 
@@ -53,8 +57,7 @@ template <bool HALF> __device__ __forceinline__ float4_t load_rows(const void *r
 
 // 1 / (1 + exp(-z)).  The product z log2(e) is kept to twice its precision,
 // as exp2 turns its rounding into one of |z| steps; the reciprocal is refined
-// once.  Beyond 88 the result stays 1, below -88 it is under 2^-126.  (With
-// expf and a division this was a third of the arithmetic of a row.)
+// once.  Beyond 88 the result stays 1, below -88 it is under 2^-126.
 __device__ __forceinline__ float sigmoid(float z)
 {
     z = z < -88.0f ? -88.0f : z > 88.0f ? 88.0f : z;  // a NaN stays

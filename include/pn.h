@@ -571,8 +571,8 @@ pn_status pn_residual_norm(const pn_residual_norm_desc *d, void *stream);
  * An entry of -inf (a masked one) or NaN has p = 0 and is no alternative; +inf
  * counts as the largest finite value.  Places past the alternatives there are
  * get -1 and -inf.  A row without a finite entry gives -inf, entropy 0 and no
- * alternatives.  ln p and entropy are computed in fp32 sums of fp64 and
- * rounded once.
+ * alternatives.  The sum of exp is fp64, the entropy's sum fp32; results
+ * are rounded once to fp32.
  *   logits   : rows of row_type (PN_ROWS_*), ld >= V elements, any alignment
  *              of its type
  *   scale    : 2^-100 .. 2^64 (the inverse of a temperature)
