@@ -97,6 +97,13 @@ bool shared_fit(const pn_kv4_cache *c, int q_heads, int B, int G, int64_t total_
            rows <= INT32_MAX / 4 && (rows / 16 + G) * c->heads <= INT32_MAX / 2 && (max_q * (q_heads / c->heads) / 16 + 1) * B * c->heads <= INT32_MAX;
 }
 
+// A launch holds less than 2^32 threads.
+bool launches_fit(const Plan &p, const pn_kv4_cache *c, int B)
+{
+    constexpr int64_t most = (int64_t)UINT32_MAX / kThreads;
+    return p.grid <= most && (p.line || (int64_t)B * c->heads * p.tiles <= most);
+}
+
 bool raise_shared()
 {
     return raise_pass<kFront>() && raise_pass<kTail>() && raise_pass<kOwn>();
@@ -115,7 +122,8 @@ extern "C" size_t pn_kv4_attn_shared_workspace(const pn_kv4_cache *cache, int q_
     const int64_t pages = (max_kv + cache->page_size - 1) / cache->page_size;
     if (max_shared > pages) max_shared = pages;
     if (!shared_fit(cache, q_heads, B, G, total_q, max_q, max_kv, max_shared)) return 0;
-    return plan(cache, q_heads, B, G, total_q, max_q, max_kv, max_shared).bytes();
+    const Plan p = plan(cache, q_heads, B, G, total_q, max_q, max_kv, max_shared);
+    return launches_fit(p, cache, B) ? p.bytes() : 0;
 }
 
 extern "C" pn_status pn_kv4_attn_shared(const pn_kv4_cache *cache, const uint16_t *q, int64_t ldq, int q_heads,
@@ -143,6 +151,7 @@ extern "C" pn_status pn_kv4_attn_shared(const pn_kv4_cache *cache, const uint16_
     if (!shared_fit(cache, q_heads, B, G, total_q, max_q, max_kv, max_shared)) return PN_EUNSUPPORTED;
     if (total_q == 0) return PN_OK;
     Plan p = plan(cache, q_heads, B, G, total_q, max_q, max_kv, max_shared);
+    if (!launches_fit(p, cache, B)) return PN_EUNSUPPORTED;
     if (ws_bytes < p.bytes()) return PN_ESHAPE;
     if (!once_per_device(kAttrKv4Shared, raise_shared)) return PN_ELAUNCH;
 

@@ -49,3 +49,14 @@ def test_nothing_to_do_and_sizes():
                 (4, 3, 1, 0, 1, 128, 4), (4, 3, 1, 1 << 30, 1, 128, 4)):
         assert size(c, *bad) == 0
     assert B.lib().pn_kv4_attn_shared_workspace(None, 4, 3, 1, 3, 1, 128, 4) == 0
+
+
+@pytest.mark.parametrize("requests,groups,status", [(32767, 1, ESHAPE), (32768, 1, EUNSUPPORTED), (65535, 1, EUNSUPPORTED),
+                                                    (4, 65535, EUNSUPPORTED)])
+def test_more_items_than_a_launch_holds(requests, groups, status):
+    """A workgroup of 512 threads to an item: 2^32 threads from 2^23 items on."""
+    c = cache(heads=256)
+    kw = dict(ARGS, ldq=16384, ldo=16384, q_heads=256, B=requests, G=groups, total_q=requests, ws_bytes=16)
+    assert B.pn_kv4_attn_shared(c, **kw, stream=0, check=False) == status
+    size = B.pn_kv4_attn_shared_workspace(c, 256, requests, groups, requests, 1, 128, 4)
+    assert (size == 0) == (status == EUNSUPPORTED)
