@@ -175,11 +175,24 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void residual_norm(NormArgs 
     }
 }
 
-template <int W, int V, bool HALF> pn_status launch(const NormArgs &a, hipStream_t s)
+// A launch holds less than 2^32 threads; further rows go into further ones.
+template <int W, int V, bool HALF> pn_status launch(NormArgs a, hipStream_t s)
 {
-    const int64_t blocks = W == 1 ? (a.T + 3) / 4 : a.T;
-    hipLaunchKernelGGL((residual_norm<W, V, HALF>), dim3((unsigned)blocks), dim3(W == 1 ? 256 : 64 * W), 0, s, a);
-    return hipGetLastError() == hipSuccess ? PN_OK : PN_ELAUNCH;
+    constexpr int kThreads = W == 1 ? 256 : 64 * W, kRows = W == 1 ? 4 : 1, kBytes = HALF ? 2 : 4;
+    constexpr int64_t kMost = (int64_t)UINT32_MAX / kThreads * kRows;
+    const int64_t all = a.T;
+    for (int64_t t = 0; t < all; t += kMost) {
+        a.T = all - t < kMost ? all - t : kMost;
+        const unsigned blocks = (unsigned)((a.T + kRows - 1) / kRows);
+        hipLaunchKernelGGL((residual_norm<W, V, HALF>), dim3(blocks), dim3(kThreads), 0, s, a);
+        if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
+        a.h += kMost * a.ldh;
+        if (a.y) a.y = (const uint8_t *)a.y + kMost * a.ldy * kBytes;
+        if (a.z) a.z = (const uint8_t *)a.z + kMost * a.ldz * kBytes;
+        if (a.h_out) a.h_out += kMost * a.ldho;
+        if (a.x) a.x += kMost * a.ldx;
+    }
+    return PN_OK;
 }
 
 template <int W, int V, int MAX, bool HALF> pn_status pick(const NormArgs &a, int v, hipStream_t s)

@@ -218,3 +218,18 @@ def test_offsets_past_32_bits():
     for t in range(3):
         s["h_out"][t, :n] = buf[t * ld:t * ld + n]
     check(s, ref)
+
+
+def test_more_rows_than_a_launch_holds():
+    """Four rows to 256 threads, less than 2^32 threads to a launch."""
+    T, n = (1 << 26) + 7, 3
+    h = torch.randn((T, 4), dtype=torch.float32, device="cuda")
+    x = torch.full((T, 8), FILL, dtype=torch.float16, device="cuda")
+    B.pn_residual_norm(T=T, n=n, h=h, ldh=4, y=None, ldy=0, row_type="f32", gate="none", z=None, ldz=0, post=False,
+                       post_gain=None, scale=1.0, chan_scale=None, pre_gain=None, eps=EPS, h_out=None, ldho=0, x=x, ldx=8)
+    torch.cuda.synchronize()
+    for at in (0, (1 << 26) - 12, T - 300):
+        part = host(h[at:at + 300], n)
+        _, _, ref, bound = R.residual_norm(part, None, False, None, "none", None, 1.0, None, None, EPS)
+        got = x[at:at + 300].double().cpu().numpy()
+        assert (np.abs(got[:, :n] - ref) <= bound).all() and (got[:, n:] == FILL).all()
