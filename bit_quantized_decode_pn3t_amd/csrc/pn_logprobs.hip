@@ -423,13 +423,25 @@ bool sizes_fit(int64_t rows, int64_t V, int K)
     return rows <= INT32_MAX && V <= INT32_MAX && K <= PN_LOGPROBS_MAX_TOP && rows * tiles <= INT32_MAX;
 }
 
-template <bool HALF> pn_status launch(const LogpArgs &a, int64_t rows, hipStream_t s)
+template <bool HALF> pn_status launch(LogpArgs a, int64_t rows, hipStream_t s)
 {
-    const dim3 blocks((unsigned)(rows * a.chunks)), threads(64 * kWaves);
-    if (a.chunks == 1) {
-        hipLaunchKernelGGL((logp_scan<HALF, true>), blocks, threads, 0, s, a);
-        return hipGetLastError() == hipSuccess ? PN_OK : PN_ELAUNCH;
+    const dim3 threads(64 * kWaves);
+    if (a.chunks == 1) {  // a launch holds less than 2^32 threads; further rows go into further ones
+        constexpr int64_t kMost = (int64_t)UINT32_MAX / (64 * kWaves);
+        for (int64_t r = 0; r < rows; r += kMost) {
+            const int64_t n = rows - r < kMost ? rows - r : kMost;
+            hipLaunchKernelGGL((logp_scan<HALF, true>), dim3((unsigned)n), threads, 0, s, a);
+            if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
+            a.x = (const uint8_t *)a.x + kMost * a.ld * (HALF ? 2 : 4);
+            if (a.tokens) a.tokens += kMost * a.ld_tok;
+            if (a.logp) a.logp += kMost * a.ld_lp;
+            if (a.entropy) a.entropy += kMost;
+            if (a.top_ids) a.top_ids += kMost * a.ld_top;
+            if (a.top_logp) a.top_logp += kMost * a.ld_top;
+        }
+        return PN_OK;
     }
+    const dim3 blocks((unsigned)(rows * a.chunks));  // fewer rows than workgroups()
     hipLaunchKernelGGL((logp_scan<HALF, false>), blocks, threads, 0, s, a);
     if (hipGetLastError() != hipSuccess) return PN_ELAUNCH;
     hipLaunchKernelGGL((logp_join<HALF>), dim3((unsigned)rows), threads, 0, s, a);

@@ -193,3 +193,19 @@ def test_offsets_past_32_bits():
     ws = torch.empty(B.pn_logprobs_workspace(2, V, 4), dtype=torch.uint8, device="cuda")
     B.pn_logprobs(buf, "f16", ld, 2, V, 1.0, tok, 2, 2, logp, 2, H, 4, ids, best, 4, ws, ws.numel())
     check([t.cpu().numpy() for t in (logp, H, ids, best)], x, 1.0, tokens, 4)
+
+
+def test_more_rows_than_a_launch_holds():
+    """A row to 256 threads, less than 2^32 threads to a launch."""
+    rows, V, K = (1 << 24) + 5, 3, 2
+    x = torch.randn((rows, V), dtype=torch.float32, device="cuda")
+    tok = torch.randint(0, V, (rows, 1), dtype=torch.int32, device="cuda")
+    logp, H, best = (torch.full(s, 7.0, device="cuda") for s in ((rows, 1), (rows,), (rows, K)))
+    ids = torch.full((rows, K), 7, dtype=torch.int32, device="cuda")
+    need = B.pn_logprobs_workspace(rows, V, K)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    B.pn_logprobs(x, "f32", V, rows, V, 1.0, tok, 1, 1, logp, 1, H, K, ids, best, K, ws, need)
+    torch.cuda.synchronize()
+    for at in (0, (1 << 24) - 100, rows - 200):
+        cut = slice(at, at + 200)
+        check([t[cut].cpu().numpy() for t in (logp, H, ids, best)], x[cut].cpu().numpy(), 1.0, tok[cut].cpu().numpy(), K)
