@@ -489,7 +489,9 @@ pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, int64_t ldq,
  *                pn_kv4_attn_shared_workspace says (else PN_ESHAPE); calls that
  *                may overlap need their own
  * PN_EUNSUPPORTED: as pn_kv4_attn; G > 65535, max_shared * page_size > 2^30 - 1,
- * total_q * q_heads / heads > 2^29 - 1 or B * q_heads * (max_q / 16 + 1) > 2^31 - 1. */
+ * total_q * q_heads / heads > 2^29 - 1, B * q_heads * (max_q / 16 + 1) > 2^31 - 1,
+ * or a launch of 2^23 workgroups (about heads times the larger of the requests
+ * and the groups, for each tile of rows). */
 size_t pn_kv4_attn_shared_workspace(const pn_kv4_cache *cache, int q_heads, int B, int G, int64_t total_q,
                                     int64_t max_q, int64_t max_kv, int64_t max_shared);
 pn_status pn_kv4_attn_shared(const pn_kv4_cache *cache, const uint16_t *q, int64_t ldq, int q_heads,
