@@ -527,7 +527,7 @@ __device__ __forceinline__ bool own_item(const AttnArgs &a, Line &t, Item &m, in
 // mean.  False: no such part.
 struct FrontLds {
     int64_t scan[kWaves];
-    int64_t steps;
+    int64_t before, steps;  // (not in scan, which slower waves may still read)
     int32_t b, found;
 };
 
@@ -631,7 +631,7 @@ __device__ __forceinline__ bool front_item(const AttnArgs &a, FrontLds &s, Line 
                 size(b, items, steps);
                 const int64_t n = items * quotient(steps + T - 1, T);
                 if (me < before + n) {
-                    s.scan[0] = before;
+                    s.before = before;
                     s.steps = steps;
                     s.b = b;
                     s.found = 1;
@@ -643,7 +643,7 @@ __device__ __forceinline__ bool front_item(const AttnArgs &a, FrontLds &s, Line 
         __syncthreads();
         if (!s.found) return false;
         t.b = s.b;
-        before = s.scan[0];
+        before = s.before;
         steps = s.steps;
     }
     t.b = uniform(t.b);
