@@ -89,6 +89,29 @@ Plan plan(const pn_kv4_cache *c, int q_heads, int B, int G, int64_t total_q, int
     return p;
 }
 
+// At least the plan's bytes, and growing with every size: a plan for less may
+// need more (fewer rows spread over other tiles, a line where there were items),
+// and what is kept for the largest call has to serve it.  The front's rows are
+// counted with the largest tile that the rows allow, the own keys' parts as if
+// every call dealt them as a line.
+size_t room(const pn_kv4_cache *c, int q_heads, int B, int G, int64_t total_q, int64_t max_q, int64_t max_kv)
+{
+    const int64_t rows = total_q * (q_heads / c->heads), groups = (rows + 15) / 16;
+    const int64_t most = c->dim == 256 ? 2 : 4, least = c->dim == 256 ? 1 : 2;  // least: two workgroups share a compute unit
+    const int64_t tile = 16 * (groups < least ? least : groups < most ? groups : most);
+    const int64_t units = device_cus() * tile, items = (rows + G * 16 * most) * c->heads;
+    const int64_t front = tile + (G > 64 ? units + items : units > items ? units : items);
+    size_t n = B * sizeof(Member) + round16((size_t)(rows / 16 + G + 1) * c->heads * sizeof(int2));
+    n += (size_t)front * (sizeof(float2) + c->dim * sizeof(float));
+    if (max_kv > 2 * kShare * kStep) {  // else no item is cut
+        const Cut t = cut(c, q_heads, B, max_q, max_kv, 0, 0);
+        Cut all = t;
+        if (t.rg == 1 && t.nt < least) all.nt = (int)least;
+        n += round16(device_cus() * (part_bytes(c, all) + sizeof(Cutoff)));
+    }
+    return n;
+}
+
 bool shared_fit(const pn_kv4_cache *c, int q_heads, int B, int G, int64_t total_q, int64_t max_q, int64_t max_kv,
                 int64_t max_shared)
 {
@@ -123,7 +146,7 @@ extern "C" size_t pn_kv4_attn_shared_workspace(const pn_kv4_cache *cache, int q_
     if (max_shared > pages) max_shared = pages;
     if (!shared_fit(cache, q_heads, B, G, total_q, max_q, max_kv, max_shared)) return 0;
     const Plan p = plan(cache, q_heads, B, G, total_q, max_q, max_kv, max_shared);
-    return launches_fit(p, cache, B) ? p.bytes() : 0;
+    return launches_fit(p, cache, B) ? room(cache, q_heads, B, G, total_q, max_q, max_kv) : 0;
 }
 
 extern "C" pn_status pn_kv4_attn_shared(const pn_kv4_cache *cache, const uint16_t *q, int64_t ldq, int q_heads,

@@ -485,9 +485,12 @@ pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, int64_t ldq,
  *   max_shared : >= 1, at least every shared[g] (of a larger one the first
  *                max_shared pages are shared)
  *   other arguments as for pn_kv4_attn
- *   ws         : device, 16-byte aligned, at least what
- *                pn_kv4_attn_shared_workspace says (else PN_ESHAPE); calls that
- *                may overlap need their own
+ *   ws         : device, 16-byte aligned, what pn_kv4_attn_shared_workspace
+ *                says (less than the call needs: PN_ESHAPE).  That grows with
+ *                B, G, total_q, max_q and max_kv, so that what the largest
+ *                call needs serves every smaller one.  Sums of the shared keys
+ *                are kept in fp32 for all queries: 4 * total_q * q_heads * dim
+ *                bytes are part of it.  Calls that may overlap need their own
  * PN_EUNSUPPORTED: as pn_kv4_attn; G > 65535, max_shared * page_size > 2^30 - 1,
  * total_q * q_heads / heads > 2^29 - 1, B * q_heads * (max_q / 16 + 1) > 2^31 - 1,
  * or a launch of 2^23 workgroups (about heads times the larger of the requests
