@@ -68,6 +68,8 @@ __device__ __forceinline__ float sigmoid(float z)
     const float d = 1.0f + e, r = __builtin_amdgcn_rcpf(d);
     return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
 }
+// z / (1 + exp(-z)); 0 at -inf, where the product would be NaN.
+__device__ __forceinline__ float silu(float z) { return (z < -88.0f ? -88.0f : z) * sigmoid(z); }
 
 // Sum over a row's threads: W waves, in every one of them.
 template <int W> __device__ __forceinline__ float row_sum(float v, float *part)
@@ -130,7 +132,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void residual_norm(NormArgs 
                 float g = 1.0f;
                 if (a.gate == PN_GATE_PLAIN) g = z[i][e];
                 else if (a.gate == PN_GATE_SIGMOID) g = sigmoid(z[i][e]);
-                else if (a.gate == PN_GATE_SILU) g = z[i][e] * sigmoid(z[i][e]);
+                else if (a.gate == PN_GATE_SILU) g = silu(z[i][e]);
                 h[i][e] = __builtin_fmaf(f[e] * g, u[i][e], h[i][e]);
             }
         }

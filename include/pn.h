@@ -536,8 +536,9 @@ pn_status pn_spec_verify(const float *target, int64_t ldt, const float *draft, i
  *        y * post_gain / sqrt(mean(y^2) + eps)        (post 1)
  *   h' = h + scale * chan_scale * g(z) * u            (y NULL: h' = h)
  *   x  = fp16(h' * pre_gain / sqrt(mean(h'^2) + eps))
- * with g(z) = 1, z, 1 / (1 + exp(-z)) or z / (1 + exp(-z)) (PN_GATE_*), in fp32
- * throughout; gains and chan_scale that are NULL count as 1.  x is what
+ * with g(z) = 1, z, 1 / (1 + exp(-z)) or z / (1 + exp(-z)) (PN_GATE_*; both of
+ * the last are 0 at z = -inf), in fp32 throughout (squares that leave its range
+ * count as infinite, x is 0 then); gains and chan_scale that are NULL count as 1.  x is what
  * pn_gemv, pn_gemm_smallm and pn_gemm_prefill read.
  *   h, h_out : fp32 rows.  h_out may be h (same ld) or NULL (only x wanted)
  *   y, z     : rows of row_type (PN_ROWS_*); z with a gate only, ldz 0: one row
