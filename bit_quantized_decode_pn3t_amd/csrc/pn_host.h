@@ -48,6 +48,44 @@ inline bool type_ok(int t) { return t == PN_PN3T || t == PN_PN4T; }
 inline int wpb(int t) { return t == PN_PN3T ? 80 : 64; }
 inline bool aligned4(const void *p) { return ((uintptr_t)p & 3) == 0; }
 
+// Rows in memory (none of them where `at` is null), for checks of overlaps.
+struct Rows {
+    const void *at;
+    int64_t pitch, bytes, count;  // pitch >= bytes, or one row
+};
+
+// Whether the bytes [lo, hi) meet one of the rows.
+inline bool meets(const Rows &r, uintptr_t lo, uintptr_t hi)
+{
+    const uintptr_t at = (uintptr_t)r.at;
+    if (hi <= at) return false;
+    if (lo <= at) return true;
+    if (r.count == 1) return lo - at < (uintptr_t)r.bytes;
+    const uintptr_t p = (uintptr_t)r.pitch, last = (uintptr_t)r.count - 1;
+    uintptr_t row = (lo - at) / p;  // the last that starts at lo or before
+    if (row > last) row = last;
+    return lo < at + row * p + (uintptr_t)r.bytes || (row < last && at + (row + 1) * p < hi);
+}
+
+// Whether a and b share a byte.  Rows may lie between each other's.
+inline bool overlap(const Rows &a, const Rows &b)
+{
+    if (!a.at || !b.at || a.bytes < 1 || b.bytes < 1 || a.count < 1 || b.count < 1) return false;
+    const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
+    const uintptr_t x1 = x + (uintptr_t)((a.count - 1) * a.pitch + a.bytes), y1 = y + (uintptr_t)((b.count - 1) * b.pitch + b.bytes);
+    if (x >= y1 || y >= x1) return false;
+    if (a.count > 1 && b.count > 1 && a.pitch == b.pitch) {  // columns of one buffer: their places in a pitch
+        const uintptr_t p = (uintptr_t)a.pitch, off = y >= x ? (y - x) % p : (p - (x - y) % p) % p;
+        return off < (uintptr_t)a.bytes || off + (uintptr_t)b.bytes > p;
+    }
+    const Rows &few = a.count < b.count ? a : b, &many = a.count < b.count ? b : a;
+    for (int64_t i = 0; i < few.count; ++i) {
+        const uintptr_t at = (uintptr_t)few.at + (uintptr_t)(i * few.pitch);
+        if (meets(many, at, at + (uintptr_t)few.bytes)) return true;
+    }
+    return false;
+}
+
 // Checks shared by every entry point that takes a packed matrix.
 inline pn_status check_matrix(int t, const void *W, int64_t N, int64_t K)
 {

@@ -218,24 +218,6 @@ template <bool HALF> pn_status run(const NormArgs &a, hipStream_t s)
     return pick<16, 3, 8, HALF>(a, (groups + 1023) / 1024, s);
 }
 
-// Rows in memory, for the check of overlaps.
-struct Rows {
-    const void *at;
-    int64_t pitch, bytes, count;
-};
-
-// Whether a and b share a byte.  Rows that interleave with the same pitch (columns of one buffer) need not.
-bool overlap(const Rows &a, const Rows &b)
-{
-    if (!a.at || !b.at) return false;
-    const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
-    const uintptr_t x1 = x + (uintptr_t)((a.count - 1) * a.pitch + a.bytes), y1 = y + (uintptr_t)((b.count - 1) * b.pitch + b.bytes);
-    if (x >= y1 || y >= x1) return false;
-    if (a.pitch != b.pitch || a.count < 2 || b.count < 2) return true;
-    const uintptr_t p = (uintptr_t)a.pitch, off = y >= x ? (y - x) % p : (p - (x - y) % p) % p;
-    return off < (uintptr_t)a.bytes || off + (uintptr_t)b.bytes > p;
-}
-
 }  // namespace
 
 extern "C" pn_status pn_residual_norm(const pn_residual_norm_desc *d, void *stream)
