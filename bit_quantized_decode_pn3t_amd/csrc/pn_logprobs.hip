@@ -472,7 +472,21 @@ extern "C" pn_status pn_logprobs(const void *logits, int row_type, int64_t ld, i
         if (!aligned(p, 4)) return PN_EALIGN;
     if (!sizes_fit(rows, V, K)) return PN_EUNSUPPORTED;
     if (rows == 0) return PN_OK;
-    if (ws_bytes < pn_logprobs_workspace(rows, V, K)) return PN_ESHAPE;
+    const size_t need = pn_logprobs_workspace(rows, V, K);
+    if (ws_bytes < need) return PN_ESHAPE;
+    const Rows inputs[] = {{logits, ld * (row_type == PN_ROWS_F16 ? 2 : 4), V * (row_type == PN_ROWS_F16 ? 2 : 4), rows},
+                           {tokens, ld_tok * 4, n_tok * (int64_t)4, rows}};
+    const Rows outputs[] = {{logp, ld_lp * 4, n_tok * (int64_t)4, rows},
+                            {entropy, 0, rows * 4, 1},
+                            {top_ids, ld_top * 4, K * (int64_t)4, rows},
+                            {top_logp, ld_top * 4, K * (int64_t)4, rows},
+                            {ws, 0, (int64_t)need, 1}};
+    for (const Rows &o : outputs) {
+        for (const Rows &i : inputs)
+            if (overlap(o, i)) return PN_EINVAL;
+        for (const Rows *other = outputs; other != &o; ++other)
+            if (overlap(o, *other)) return PN_EINVAL;
+    }
     LogpArgs a;
     a.x = logits;
     a.tokens = tokens;

@@ -575,7 +575,7 @@ pn_status pn_residual_norm(const pn_residual_norm_desc *d, void *stream);
  *   top_ids[r][i], top_logp[r][i] = the K entries of largest x, largest first,
  *                    the lower index of equals, and their ln p
  * An entry of -inf (a masked one) or NaN has p = 0 and is no alternative; +inf
- * counts as the largest finite value.  Places past the alternatives there are
+ * counts as the largest finite value of fp32.  Places past the alternatives there are
  * get -1 and -inf.  A row without a finite entry gives -inf, entropy 0 and no
  * alternatives.  The sum of exp is fp64, the entropy's sum fp32; results
  * are rounded once to fp32.
@@ -589,7 +589,9 @@ pn_status pn_residual_norm(const pn_residual_norm_desc *d, void *stream);
  *              rows of ld_top >= K
  *   rows     : >= 0 (0 does nothing);  V 1..2^31-1;  rows * ceil(V / 1024) <
  *              2^31, else PN_EUNSUPPORTED
- *   ws       : device, 8-byte aligned, at least pn_logprobs_workspace bytes */
+ *   ws       : device, 8-byte aligned, at least pn_logprobs_workspace bytes,
+ *              which grow with rows, V and K
+ *   Outputs and ws overlap neither inputs nor each other, else PN_EINVAL. */
 #define PN_LOGPROBS_MAX_TOP 64
 size_t pn_logprobs_workspace(int64_t rows, int64_t V, int K);
 pn_status pn_logprobs(const void *logits, int row_type, int64_t ld, int64_t rows, int64_t V, float scale,
