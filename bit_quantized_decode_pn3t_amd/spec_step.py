@@ -235,14 +235,21 @@ class Requests:
 
     def score(self, logits, tokens, top=0, scale=1.0):
         """ln p of tokens [rows, n] in softmax(scale * logits), the rows'
-        entropies, and the `top` most probable tokens with their ln p."""
+        entropies, and the `top` most probable tokens with their ln p.
+        logits: fp32 or fp16 [rows, vocab]."""
         rows, n = tokens.shape
         dev, vocab = self.device, self.model.vocab
-        tokens = tokens.int().contiguous()
+        kind = {torch.float32: "f32", torch.float16: "f16"}.get(logits.dtype)
+        if kind is None or logits.shape != (rows, vocab):
+            raise ValueError("scores of %d rows need fp32 or fp16 logits [%d, %d], not %s %s"
+                             % (rows, rows, vocab, logits.dtype, list(logits.shape)))
+        if logits.stride(1) != 1 or logits.stride(0) < vocab:
+            logits = logits.contiguous()
+        tokens = torch.where((tokens >= 0) & (tokens < vocab), tokens, -1).int().contiguous()
         logp, entropy = torch.empty((rows, n), device=dev), torch.empty(rows, device=dev)
         ids, best = torch.empty((rows, top), dtype=torch.int32, device=dev), torch.empty((rows, top), device=dev)
         ws = torch.empty(B.pn_logprobs_workspace(rows, vocab, top), dtype=torch.uint8, device=dev)
-        B.pn_logprobs(logits, "f32", logits.stride(0), rows, vocab, scale, tokens, n, n, logp, n, entropy, top,
+        B.pn_logprobs(logits, kind, logits.stride(0), rows, vocab, scale, tokens, n, n, logp, n, entropy, top,
                       ids if top else None, best if top else None, top, ws, ws.numel())
         return logp, entropy, ids, best
 
