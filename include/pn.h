@@ -479,11 +479,21 @@ pn_status pn_kv4_attn(const pn_kv4_cache *cache, const uint16_t *q, int64_t ldq,
  * Columns below shared[g] of a table row are not read, unless a query of the
  * request stands inside the shared pages: then all of that request's pages are
  * its own row's (as pn_kv4_plan's rows hold them).  A prefix ends with a page;
- * tokens behind its last whole page are each request's own.
+ * tokens behind its last whole page are each request's own.  Roundings are
+ * pn_kv4_attn's but for one: shared tokens' weights are summed after they are
+ * rounded to fp16, which pn_kv4_attn does before.
+ * A call is two launches or three, and pays where a group has many queries on a
+ * long prefix: 64 behind 16384 tokens 3 times as fast as pn_kv4_attn for each,
+ * 4 behind 1024 or 16 of 8 drafts behind 5024 no faster.  Work is dealt as if
+ * no request had more than max_kv - max_shared * page_size tokens of its own:
+ * one that has more (outside of all groups, behind a shorter prefix, with a
+ * query inside the shared pages) may have a single workgroup a head and tile
+ * read them (16616 tokens, 128 wide: 93 us more).  Such requests do better in a
+ * call of pn_kv4_attn.
  *   g_start    : int32 [G + 1], not decreasing;  shared: int32 [G], below 1: none
  *   prefix     : int32, G rows of ld_prefix >= max_shared
  *   max_shared : >= 1, at least every shared[g] (of a larger one the first
- *                max_shared pages are shared)
+ *                max_shared pages are shared); best the largest shared[g]
  *   other arguments as for pn_kv4_attn
  *   ws         : device, 16-byte aligned, what pn_kv4_attn_shared_workspace
  *                says (less than the call needs: PN_ESHAPE).  That grows with
@@ -590,7 +600,8 @@ pn_status pn_residual_norm(const pn_residual_norm_desc *d, void *stream);
  *   rows     : >= 0 (0 does nothing);  V 1..2^31-1;  rows * ceil(V / 1024) <
  *              2^31, else PN_EUNSUPPORTED
  *   ws       : device, 8-byte aligned, at least pn_logprobs_workspace bytes,
- *              which grow with rows, V and K
+ *              which grow with rows, V and K; calls that may overlap need
+ *              their own
  *   Outputs and ws overlap neither inputs nor each other, else PN_EINVAL. */
 #define PN_LOGPROBS_MAX_TOP 64
 size_t pn_logprobs_workspace(int64_t rows, int64_t V, int K);
